@@ -12,6 +12,10 @@ function names mirror the C entry points of ``include/moe_ffn.h``:
     forward               -> moe_forward
     forward_routed        -> moe_forward_routed
 
+The operators around the layer (``include/moe_block.h``: embedding, block
+norms, linear cross entropy, gradient clipping) are in ``block.py`` and are
+reached from here by the same names.
+
 There is no CPU fallback: if the library is missing or a call returns an
 error status, a ``MoEError`` is raised.
 """
@@ -108,7 +112,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_forward_fp8_nvfp4": ([pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                                    vp], ci),
     }
-    for name, (args, res) in sigs.items():
+    from .block import SIGS
+    for name, (args, res) in {**sigs, **SIGS}.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
@@ -394,3 +399,8 @@ __all__ = ["Problem", "MoEError", "MoEFFN", "load", "workspace_size", "alloc_wor
            "prepared_scales_size", "prepare_weights", "forward_fp8_nvfp4", "selected_kernel",
            "forward_routed", "prepare_weights_mxfp4", "selftest_wait_timeout",
            "backward_workspace_size", "alloc_backward_workspace", "backward", "backward_routed"]
+
+from . import block as _block  # noqa: E402  (uses the names above)
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += _block.__all__

@@ -1,0 +1,156 @@
+"""Binding of the operators around the expert layer (``include/moe_block.h``):
+token embedding, the norms of a block with its gate and residual, the linear
+cross entropy, and the clipping of gradients by their global norm.
+
+As in the package's other entry points, outputs and workspaces are the
+caller's tensors, work goes to the current stream (or ``stream``), and an
+error status raises ``MoEError``.  Tensors that do not have the type, shape or
+row stride of their problem raise ``ValueError`` before the library is called.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import MOE_OK, MoEError, load
+
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
+
+_vp, _sz, _ci = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+
+
+def _dtype(d) -> int:
+    if d not in _DTYPES:
+        raise ValueError(f"unsupported dtype {d}: torch.bfloat16 or torch.float32")
+    return _DTYPES[d]
+
+
+class NormProblem(ctypes.Structure):
+    """Mirror of ``moe_norm_problem``; made with ``NormProblem.make``."""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("branch_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("ld_branch", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ld_residual_out", ctypes.c_int64), ("ld_normed", ctypes.c_int64)]
+
+    @classmethod
+    def make(cls, T, H, branch_dtype=torch.bfloat16, residual_dtype=torch.bfloat16,
+             weight_dtype=torch.bfloat16, gate="none", eps=1e-6, weight_offset=0.0,
+             residual_scale=1.0, branch_scale=1.0, ld_branch=0, ld_residual=0,
+             ld_residual_out=0, ld_normed=0):
+        """``gate``: "none", "channel" ([H]), "token" ([T]) or "element" ([T, H]).
+        The row strides (elements) are 0 for dense rows."""
+        if gate not in GATES:
+            raise ValueError(f"gate must be one of {sorted(GATES)}")
+        T, H = int(T), int(H)
+        p = cls(T, H, _dtype(branch_dtype), _dtype(residual_dtype), _dtype(weight_dtype),
+                GATES[gate], float(eps), float(weight_offset), float(residual_scale),
+                float(branch_scale), int(ld_branch), int(ld_residual), int(ld_residual_out),
+                int(ld_normed))
+        p._rows, p._cols = (T, H), (H,)
+        p._b, p._r, p._w = branch_dtype, residual_dtype, weight_dtype
+        p._ld = tuple((int(ld) or H, 1) for ld in (ld_branch, ld_residual, ld_residual_out,
+                                                   ld_normed))
+        p._gate = {"none": None, "channel": (H,), "token": (T,), "element": (T, H)}[gate]
+        return p
+
+
+SIGS = {
+    "moe_block_norm_forward": ([_vp] * 9, _ci),
+    "moe_block_norm_workspace_size": ([_vp], _sz),
+    "moe_block_norm_backward": ([_vp] * 14 + [_sz, _vp], _ci),
+}
+
+
+def _bad(t, what):
+    raise ValueError(f"expected a CUDA tensor of {what}, got {t.dtype} {tuple(t.shape)} with "
+                     f"strides {t.stride()} on {t.device}")
+
+
+def _dense(t: Optional[torch.Tensor], dtype, shape):
+    """The address of a dense tensor of this type and shape (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, f"{dtype} {tuple(shape)}, dense")
+    return t.data_ptr()
+
+
+def _rows(t: Optional[torch.Tensor], dtype, shape, strides):
+    """The address of rows of this type, shape and stride (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != strides:
+        # the stride of a single row, or of rows of one column, says nothing
+        if not (t.dtype is dtype and t.shape == shape and t.is_cuda
+                and (shape[0] <= 1 or t.stride(0) == strides[0])
+                and (shape[1] <= 1 or t.stride(1) == 1)):
+            _bad(t, f"{dtype} {shape} with strides {strides}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _ws_of(n: int, fn: str, device) -> torch.Tensor:
+    """A 256-byte aligned workspace of n bytes with a cleared status word."""
+    if n == 0:
+        raise MoEError(fn, 1)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    ws = ws[(-ws.data_ptr()) % 256:][:n]
+    ws[:4].zero_()
+    return ws
+
+
+def block_norm_forward(p: NormProblem, residual, branch=None, w_post=None, gate=None, w_pre=None,
+                       residual_out=None, normed=None, stream=None) -> None:
+    """residual_out = residual_scale * residual + branch_scale * gate * rmsnorm(branch) * w_post
+    and normed = rmsnorm(residual_out) * w_pre, in one pass.  Without ``w_post`` the branch is
+    added unnormed; without ``branch`` only ``normed`` of the residual is computed; without
+    ``w_pre`` only the residual update.  ``residual_out`` may be ``residual``."""
+    b, r, ro, n = p._ld
+    rc = load().moe_block_norm_forward(
+        ctypes.byref(p), _rows(branch, p._b, p._rows, b), _dense(w_post, p._w, p._cols),
+        _dense(gate, p._w, p._gate), _rows(residual, p._r, p._rows, r),
+        _dense(w_pre, p._w, p._cols), _rows(residual_out, p._r, p._rows, ro),
+        _rows(normed, p._b, p._rows, n), _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_block_norm_forward", rc)
+
+
+def alloc_block_norm_workspace(p: NormProblem, device="cuda") -> torch.Tensor:
+    """The workspace of ``block_norm_backward``."""
+    return _ws_of(load().moe_block_norm_workspace_size(ctypes.byref(p)),
+                  "moe_block_norm_workspace_size", device)
+
+
+def block_norm_backward(p: NormProblem, residual_out, d_residual, ws, branch=None, w_post=None,
+                        gate=None, w_pre=None, d_normed=None, d_residual_out=None, d_branch=None,
+                        d_w_post=None, d_gate=None, d_w_pre=None, stream=None) -> None:
+    """Gradients of ``block_norm_forward`` from its inputs and the ``residual_out`` it stored
+    (without a branch: the residual): d_residual always, d_branch, d_w_post, d_gate and d_w_pre
+    for the inputs given.  ``d_residual_out`` (None: zero) is the gradient residual_out gets from
+    later layers; ``d_residual`` may be the same tensor."""
+    b, r, ro, n = p._ld
+    rc = load().moe_block_norm_backward(
+        ctypes.byref(p), _rows(branch, p._b, p._rows, b), _dense(w_post, p._w, p._cols),
+        _dense(gate, p._w, p._gate), _rows(residual_out, p._r, p._rows, ro),
+        _dense(w_pre, p._w, p._cols), _rows(d_residual_out, p._r, p._rows, ro),
+        _rows(d_normed, p._b, p._rows, n), _rows(d_residual, p._r, p._rows, r),
+        _rows(d_branch, p._b, p._rows, b), _dense(d_w_post, p._w, p._cols),
+        _dense(d_gate, p._w, p._gate), _dense(d_w_pre, p._w, p._cols), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_block_norm_backward", rc)
+
+
+__all__ = ["NormProblem", "block_norm_forward", "block_norm_backward",
+           "alloc_block_norm_workspace", "DTYPE_BF16", "DTYPE_F32"]

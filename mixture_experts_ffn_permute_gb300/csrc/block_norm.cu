@@ -1,0 +1,597 @@
+// RMS norms after and before a block, fused with the block's gate and the
+// residual update, and their backward (moe_block_norm_* of
+// include/moe_block.h has the formulas).
+//
+// Forward, per row: one read of the branch and the residual, kept in
+// registers through both row sums (mean y^2, then mean residual_out^2), one
+// write of residual_out and normed.  HBM bound: 2 (branch + residual type)
+// bytes per element.
+//
+// Backward, per row, with u = r' / rms(r'), v = y / rms(y), a = dn w_pre':
+//   g  = d_residual_out + (a - u mean(a u)) / rms(r')
+//   B  = branch_scale g,  c = B gate w_post',  S = sum(c v)
+//   d_residual = residual_scale g,  d_branch = (c - v S / H) / rms(y)
+//   d_w_pre += dn u,  d_w_post += B gate v,  d_gate += B v w_post'
+// The statistics are recomputed (the rows are read anyway): one round of row
+// sums gives sum r'^2, sum a r' and sum y^2, a second gives S.  Every thread
+// keeps the same columns on all rows of its block, so the column sums over
+// tokens are two fp32 accumulators per column in registers; each block
+// writes its sums to the workspace and a second kernel adds the blocks' in
+// order.  A channel gate shares the accumulator of w_post: with
+// A = sum_t B v, d_w_post = gate A and d_gate = w_post' A.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/moe_block.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowwise.cuh"
+
+namespace moe {
+namespace {
+
+struct NormParams {
+  const void* branch;
+  const void* residual;  // forward: residual; backward: residual_out
+  WeightPtr w_post, w_pre, gate;
+  void* residual_out;
+  void* normed;
+  const void* d_residual_out;
+  const void* d_normed;
+  void* d_residual;
+  void* d_branch;
+  void* d_gate;  // token and element gates
+  float* part;   // backward: [blocks][2][H] column sums (w_pre, w_post)
+  long ld_branch, ld_residual, ld_residual_out, ld_normed;
+  int T, H, gate_kind;
+  float eps, offset, residual_scale, branch_scale, inv_h;
+};
+
+// gate * x for the eight columns of one step
+template <bool kWide>
+__device__ __forceinline__ void apply_gate(float (&x)[8], const NormParams& p, long row, int v,
+                                           int tid, int n, float token_gate) {
+  if (p.gate_kind == MOE_GATE_TOKEN) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= token_gate;
+  } else if (p.gate_kind != MOE_GATE_NONE) {
+    float g[8];
+    load_weight8<kWide>(g, p.gate, p.gate_kind == MOE_GATE_ELEMENT ? row * p.H : 0, v, tid, n, p.H);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= g[j];
+  }
+}
+
+// One row per warp (kWarp) or per block of at most kThreads threads.
+template <typename TB, typename TR, int kSteps, int kThreads, bool kWarp, bool kWide>
+__global__ void __launch_bounds__(kThreads)
+block_norm_fwd_kernel(const NormParams p) {
+  pdl_enter();
+  __shared__ float s_sum[2][32];
+  const int n = kWarp ? 32 : blockDim.x;
+  const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const long row = kWarp ? static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= p.T) return;  // whole warps (kWarp) only
+  const bool has_branch = p.branch != nullptr;
+  Oct<TB> y[kSteps];
+  Oct<TR> r[kSteps];
+  const TR* rrow = static_cast<const TR*>(p.residual) + row * p.ld_residual;
+  if (has_branch) {
+    const TB* yrow = static_cast<const TB*>(p.branch) + row * p.ld_branch;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) load_oct<kWide>(y[v], yrow, v, tid, n, p.H);
+  }
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) load_oct<kWide>(r[v], rrow, v, tid, n, p.H);
+
+  float x[kSteps][8];  // residual_out, unrounded
+  if (has_branch) {
+    float scale = p.branch_scale;
+    const bool post = p.w_post.p != nullptr;
+    if (post) {
+      float ss[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] = fmaf(y[v].get(j), y[v].get(j), ss[0]);
+      row_sum<kWarp>(ss, s_sum[0]);
+      scale *= rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+    }
+    const float tg = p.gate_kind == MOE_GATE_TOKEN ? p.gate.at(row) : 1.f;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      float w[8];
+      if (post) {
+        load_weight8<kWide>(w, p.w_post, 0, v, tid, n, p.H);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = scale * (w[j] + p.offset);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = scale;
+      }
+      apply_gate<kWide>(w, p, row, v, tid, n, tg);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[v][j] = fmaf(p.residual_scale, r[v].get(j), w[j] * y[v].get(j));
+    }
+    TR* orow = static_cast<TR*>(p.residual_out) + row * p.ld_residual_out;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) store_oct<kWide>(x[v], orow, v, tid, n, p.H);
+  } else {
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] = r[v].get(j);
+  }
+  if (!p.normed) return;
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      // columns past the row hold zeros of r and y, but 0 * inf of a gate is not 0
+      if (oct_col<kWide>(v, j, tid, n) < p.H) ss[0] = fmaf(x[v][j], x[v][j], ss[0]);
+  row_sum<kWarp>(ss, s_sum[1]);
+  const float rstd = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+  TB* nrow = static_cast<TB*>(p.normed) + row * p.ld_normed;
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+    float w[8];
+    load_weight8<kWide>(w, p.w_pre, 0, v, tid, n, p.H);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = x[v][j] * rstd * (w[j] + p.offset);
+    store_oct<kWide>(w, nrow, v, tid, n, p.H);
+  }
+}
+
+// Rows blockIdx.x * rows_per_pass + ..., grid-strided; kWarp: eight warps of a
+// block each take a row and their column sums are joined at the end.
+template <typename TB, typename TR, int kSteps, int kThreads, bool kWarp, bool kWide>
+__global__ void __launch_bounds__(kThreads)
+block_norm_bwd_kernel(const NormParams p) {
+  pdl_enter();
+  __shared__ float s_sum[2][3 * 32];
+  extern __shared__ float s_cols[];  // kWarp: [8 warps][2][H]
+  const int n = kWarp ? 32 : blockDim.x;
+  const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int warp = threadIdx.x >> 5;
+  const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr,
+             pre = p.d_normed != nullptr;
+  float acc_pre[kSteps][8] = {}, acc_post[kSteps][8] = {};
+  const long stride = static_cast<long>(gridDim.x) * (kWarp ? 8 : 1);
+  for (long row = kWarp ? static_cast<long>(blockIdx.x) * 8 + warp : blockIdx.x; row < p.T;
+       row += stride) {
+    Oct<TB> y[kSteps], dn[kSteps];
+    Oct<TR> r[kSteps], dr[kSteps];
+    const TR* rrow = static_cast<const TR*>(p.residual) + row * p.ld_residual_out;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      if (pre) {
+        load_oct<kWide>(r[v], rrow, v, tid, n, p.H);
+        load_oct<kWide>(dn[v], static_cast<const TB*>(p.d_normed) + row * p.ld_normed, v, tid, n,
+                        p.H);
+      }
+      if (has_branch)
+        load_oct<kWide>(y[v], static_cast<const TB*>(p.branch) + row * p.ld_branch, v, tid, n, p.H);
+      if (p.d_residual_out)
+        load_oct<kWide>(dr[v], static_cast<const TR*>(p.d_residual_out) + row * p.ld_residual_out,
+                        v, tid, n, p.H);
+    }
+    float s3[3] = {0.f, 0.f, 0.f};  // sum r'^2, sum a r', sum y^2
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      float w[8];
+      if (pre) load_weight8<kWide>(w, p.w_pre, 0, v, tid, n, p.H);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (oct_col<kWide>(v, j, tid, n) >= p.H) continue;
+        if (pre) {
+          const float x = r[v].get(j);
+          s3[0] = fmaf(x, x, s3[0]);
+          s3[1] = fmaf(dn[v].get(j) * (w[j] + p.offset), x, s3[1]);
+        }
+        if (post) s3[2] = fmaf(y[v].get(j), y[v].get(j), s3[2]);
+      }
+    }
+    row_sum<kWarp>(s3, s_sum[0]);
+    const float rstd = pre ? rsqrtf(fmaf(s3[0], p.inv_h, p.eps)) : 0.f;
+    const float mean_au = rstd * s3[1] * p.inv_h;
+    const float ystd = post ? rsqrtf(fmaf(s3[2], p.inv_h, p.eps)) : 1.f;
+    // g, the gradient of residual_out
+    float g[kSteps][8];
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      float w[8];
+      if (pre) load_weight8<kWide>(w, p.w_pre, 0, v, tid, n, p.H);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x = p.d_residual_out ? dr[v].get(j) : 0.f;
+        if (pre) {
+          const float u = r[v].get(j) * rstd, d = dn[v].get(j);
+          acc_pre[v][j] = fmaf(d, u, acc_pre[v][j]);
+          x = fmaf(rstd, fmaf(-u, mean_au, d * (w[j] + p.offset)), x);
+        }
+        g[v][j] = x;
+      }
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = has_branch ? p.residual_scale * g[v][j] : g[v][j];
+      store_oct<kWide>(o, static_cast<TR*>(p.d_residual) + row * p.ld_residual, v, tid, n, p.H);
+    }
+    if (!has_branch) continue;
+    // with k = B * (channel or element gate): c = k w_post' (token gate apart)
+    const float tg = p.gate_kind == MOE_GATE_TOKEN ? p.gate.at(row) : 1.f;
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      float w[8], k[8];
+      if (post) load_weight8<kWide>(w, p.w_post, 0, v, tid, n, p.H);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = post ? w[j] + p.offset : 1.f;
+        k[j] = p.branch_scale * g[v][j];
+      }
+      if (p.gate_kind == MOE_GATE_ELEMENT) {
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = k[j] * (y[v].get(j) * ystd) * w[j];
+        const long at = row * p.H;
+        if (p.w_post.f32)
+          store_oct<kWide>(d, static_cast<float*>(p.d_gate) + at, v, tid, n, p.H);
+        else
+          store_oct<kWide>(d, static_cast<Bf16*>(p.d_gate) + at, v, tid, n, p.H);
+      }
+      // the sum over tokens of w_post (token gate: of tg k v; channel: before the gate)
+      if (p.gate_kind != MOE_GATE_ELEMENT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc_post[v][j] = fmaf(tg * k[j], y[v].get(j) * ystd, acc_post[v][j]);
+      }
+      if (p.gate_kind == MOE_GATE_ELEMENT || p.gate_kind == MOE_GATE_CHANNEL)
+        apply_gate<kWide>(k, p, row, v, tid, n, 1.f);
+      if (p.gate_kind == MOE_GATE_ELEMENT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc_post[v][j] = fmaf(k[j], y[v].get(j) * ystd, acc_post[v][j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[v][j] = k[j] * w[j];  // c
+        if (oct_col<kWide>(v, j, tid, n) < p.H)
+          s1[0] = fmaf(g[v][j], y[v].get(j) * ystd, s1[0]);
+      }
+    }
+    float mean_cv = 0.f;
+    if (post || p.gate_kind == MOE_GATE_TOKEN) {
+      row_sum<kWarp>(s1, s_sum[1]);
+      if (post) mean_cv = s1[0] * p.inv_h;
+      if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) {
+        if (p.w_post.f32) static_cast<float*>(p.d_gate)[row] = s1[0];
+        else from_float(static_cast<Bf16*>(p.d_gate)[row], s1[0]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        o[j] = tg * ystd * fmaf(-(y[v].get(j) * ystd), mean_cv, g[v][j]);
+      store_oct<kWide>(o, static_cast<TB*>(p.d_branch) + row * p.ld_branch, v, tid, n, p.H);
+    }
+  }
+  if (!p.part) return;
+  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.H;
+  if (kWarp) {
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = oct_col<kWide>(v, j, tid, n);
+        if (c < p.H) {
+          s_cols[(warp * 2 + 0) * p.H + c] = acc_pre[v][j];
+          s_cols[(warp * 2 + 1) * p.H + c] = acc_post[v][j];
+        }
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.H; c += 256) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) t += s_cols[w * 2 * p.H + c];
+      part[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = oct_col<kWide>(v, j, tid, n);
+        if (c < p.H) {
+          part[c] = acc_pre[v][j];
+          part[p.H + c] = acc_post[v][j];
+        }
+      }
+  }
+}
+
+// Sum of the blocks' column sums: 32 columns x 8 runs of blocks per CTA.
+__global__ void __launch_bounds__(256)
+block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, WeightPtr w_post,
+                       WeightPtr gate, int channel_gate, float offset, void* d_w_pre,
+                       void* d_w_post, void* d_gate) {
+  pdl_enter();
+  __shared__ float s[2][8][32];
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float a = 0.f, b = 0.f;
+  if (c < H) {
+#pragma unroll 4
+    for (int i = q; i < blocks; i += 8) {
+      const float* row = part + static_cast<long>(i) * 2 * H;
+      a += row[c];
+      b += row[H + c];
+    }
+  }
+  s[0][q][lane] = a;
+  s[1][q][lane] = b;
+  __syncthreads();
+  if (q || c >= H) return;
+  a = b = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a += s[0][i][lane];
+    b += s[1][i][lane];
+  }
+  auto put = [&](void* d, float x) {
+    if (!d) return;
+    if (w_post.f32) static_cast<float*>(d)[c] = x;
+    else from_float(static_cast<Bf16*>(d)[c], x);
+  };
+  put(d_w_pre, a);
+  put(d_w_post, channel_gate ? gate.at(c) * b : b);
+  if (channel_gate) put(d_gate, (w_post.p ? w_post.at(c) + offset : 1.f) * b);
+}
+
+// Threads and row mapping.  The forward gives a row to a warp up to 1024
+// columns (32 per lane: the row sums then need no barrier), the backward up to
+// 256 (its column sums would not fit the registers of more); wider rows take
+// a block of one step (8 columns) a thread up to 512 threads, else two steps.
+struct Shape {
+  bool warp;
+  int steps, threads;
+};
+Shape norm_shape(int H, bool bwd) {
+  if (H <= 256) return {true, 1, 256};
+  if (!bwd && H <= 1024) return {true, H <= 512 ? 2 : 4, 256};
+  const int steps = H <= 512 * 8 ? 1 : 2;
+  return {false, steps, ceil_div(ceil_div(H, 8 * steps), 32) * 32};
+}
+
+// Blocks of the backward: what the SMs hold at once, and no more than one for
+// a row (eight rows for the warp form).
+int norm_bwd_blocks(int T, int H) {
+  const Shape s = norm_shape(H, true);
+  const int per_sm = std::max(1, std::min(1024 / s.threads, 4));
+  return std::max(1, std::min(num_sms() * per_sm, s.warp ? ceil_div(T, 8) : T));
+}
+
+int elt(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+bool dtype_ok(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+int check_norm(const moe_norm_problem* p) {
+  if (!p || p->T < 0 || p->H < 1) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(p->branch_dtype) || !dtype_ok(p->residual_dtype) || !dtype_ok(p->weight_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (p->H > MOE_MAX_NORM_WIDTH) return MOE_ERR_UNSUPPORTED_SHAPE;
+  for (const int64_t ld : {p->ld_branch, p->ld_residual, p->ld_residual_out, p->ld_normed})
+    if (ld != 0 && (ld < p->H || ld > (1LL << 40))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+size_t norm_part_bytes(const moe_norm_problem* p) {
+  return sizeof(float) * 2 * static_cast<size_t>(p->H) * norm_bwd_blocks(p->T, p->H);
+}
+
+constexpr size_t kNormHeader = 256;  // status word
+
+// Collects the pointer checks and whether every row takes 16-byte accesses.
+struct RowCheck {
+  bool ok = true, wide = true;
+  void add(const void* p, int dtype, long ld) {
+    if (!p) return;
+    if (!aligned(p, elt(dtype))) ok = false;
+    if (!aligned(p, 16) || (ld * elt(dtype)) % 16 != 0) wide = false;
+  }
+};
+
+NormParams norm_params(const moe_norm_problem* p) {
+  NormParams k{};
+  k.T = p->T;
+  k.H = p->H;
+  k.gate_kind = p->gate_kind;
+  k.eps = p->eps;
+  k.offset = p->weight_offset;
+  k.residual_scale = p->residual_scale;
+  k.branch_scale = p->branch_scale;
+  k.inv_h = 1.f / static_cast<float>(p->H);
+  k.ld_branch = p->ld_branch ? p->ld_branch : p->H;
+  k.ld_residual = p->ld_residual ? p->ld_residual : p->H;
+  k.ld_residual_out = p->ld_residual_out ? p->ld_residual_out : p->H;
+  k.ld_normed = p->ld_normed ? p->ld_normed : p->H;
+  return k;
+}
+
+template <bool kBwd, typename TB, typename TR, int kSteps, int kThreads, bool kWarp, bool kWide>
+cudaError_t launch_norm_impl(const NormParams& k, int threads, int blocks, cudaStream_t s) {
+  if constexpr (kBwd)
+    return launch_kernel(block_norm_bwd_kernel<TB, TR, kSteps, kThreads, kWarp, kWide>,
+                         dim3(blocks), dim3(threads),
+                         kWarp && k.part ? sizeof(float) * 16 * k.H : 0, s, 1, k);
+  else
+    return launch_kernel(block_norm_fwd_kernel<TB, TR, kSteps, kThreads, kWarp, kWide>,
+                         dim3(blocks), dim3(threads), 0, s, 1, k);
+}
+
+template <bool kBwd, typename TB, typename TR, bool kWide>
+cudaError_t launch_norm_shape(const NormParams& k, int blocks, cudaStream_t s) {
+  const Shape sh = norm_shape(k.H, kBwd);
+  const int n = sh.threads;
+  if (sh.warp) {
+    if (sh.steps == 1) return launch_norm_impl<kBwd, TB, TR, 1, 256, true, kWide>(k, n, blocks, s);
+    if constexpr (!kBwd)
+      return sh.steps == 2 ? launch_norm_impl<kBwd, TB, TR, 2, 256, true, kWide>(k, n, blocks, s)
+                           : launch_norm_impl<kBwd, TB, TR, 4, 256, true, kWide>(k, n, blocks, s);
+  }
+  return sh.steps == 1 ? launch_norm_impl<kBwd, TB, TR, 1, 512, false, kWide>(k, n, blocks, s)
+         : n <= 512    ? launch_norm_impl<kBwd, TB, TR, 2, 512, false, kWide>(k, n, blocks, s)
+                       : launch_norm_impl<kBwd, TB, TR, 2, 1024, false, kWide>(k, n, blocks, s);
+}
+
+template <bool kBwd>
+cudaError_t launch_norm(const moe_norm_problem* p, const NormParams& k, bool wide, int blocks,
+                        cudaStream_t s) {
+  const bool bf = p->branch_dtype == MOE_DTYPE_BF16, rf = p->residual_dtype == MOE_DTYPE_BF16;
+  auto go = [&](auto w) {
+    constexpr bool kWide = decltype(w)::value;
+    if (bf)
+      return rf ? launch_norm_shape<kBwd, Bf16, Bf16, kWide>(k, blocks, s)
+                : launch_norm_shape<kBwd, Bf16, float, kWide>(k, blocks, s);
+    return rf ? launch_norm_shape<kBwd, float, Bf16, kWide>(k, blocks, s)
+              : launch_norm_shape<kBwd, float, float, kWide>(k, blocks, s);
+  };
+  return wide ? go(std::true_type{}) : go(std::false_type{});
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_block_norm_forward(const moe_norm_problem* p, const void* branch,
+                                      const void* w_post, const void* gate, const void* residual,
+                                      const void* w_pre, void* residual_out, void* normed,
+                                      void* stream) {
+  const int rc = check_norm(p);
+  if (rc != MOE_OK) return rc;
+  set_last_launch_count(0);
+  if (p->T == 0) return MOE_OK;  // tensors without elements may have null pointers
+  const bool has_branch = branch != nullptr;
+  if (!residual || has_branch != (residual_out != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!has_branch && (w_post || gate || p->gate_kind != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (p->gate_kind != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((w_pre != nullptr) != (normed != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!has_branch && !normed) return MOE_ERR_INVALID_ARG;
+  NormParams k = norm_params(p);
+  if (residual_out == residual && k.ld_residual != k.ld_residual_out) return MOE_ERR_INVALID_ARG;
+  RowCheck c;
+  c.wide = p->H % 8 == 0;
+  c.add(branch, p->branch_dtype, k.ld_branch);
+  c.add(normed, p->branch_dtype, k.ld_normed);
+  c.add(residual, p->residual_dtype, k.ld_residual);
+  c.add(residual_out, p->residual_dtype, k.ld_residual_out);
+  c.add(w_post, p->weight_dtype, p->H);
+  c.add(w_pre, p->weight_dtype, p->H);
+  c.add(gate, p->weight_dtype, p->H);
+  if (!c.ok) return MOE_ERR_MISALIGNED;
+  const bool wf = p->weight_dtype == MOE_DTYPE_F32;
+  k.branch = branch;
+  k.residual = residual;
+  k.w_post = {w_post, wf};
+  k.w_pre = {w_pre, wf};
+  k.gate = {gate, wf};
+  k.residual_out = residual_out;
+  k.normed = normed;
+  if (launch_norm<false>(p, k, c.wide, norm_shape(p->H, false).warp ? ceil_div(p->T, 8) : p->T,
+                         static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  set_last_launch_count(1);
+  return MOE_OK;
+}
+
+extern "C" size_t moe_block_norm_workspace_size(const moe_norm_problem* p) {
+  if (check_norm(p) != MOE_OK) return 0;
+  return kNormHeader + (norm_part_bytes(p) + 255) / 256 * 256;
+}
+
+extern "C" int moe_block_norm_backward(const moe_norm_problem* p, const void* branch,
+                                       const void* w_post, const void* gate,
+                                       const void* residual_out, const void* w_pre,
+                                       const void* d_residual_out, const void* d_normed,
+                                       void* d_residual, void* d_branch, void* d_w_post,
+                                       void* d_gate, void* d_w_pre, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  const int rc = check_norm(p);
+  if (rc != MOE_OK) return rc;
+  if (!ws) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
+  if (ws_bytes < moe_block_norm_workspace_size(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const bool channel = p->gate_kind == MOE_GATE_CHANNEL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  set_last_launch_count(0);
+  if (!aligned(d_w_post, elt(p->weight_dtype)) || !aligned(d_w_pre, elt(p->weight_dtype)))
+    return MOE_ERR_MISALIGNED;
+  if (p->T == 0) {  // no tokens: the weights' gradients are zero
+    const size_t n = static_cast<size_t>(p->H) * elt(p->weight_dtype);
+    for (void* d : {d_w_post, d_w_pre, channel ? d_gate : nullptr})
+      if (d) {
+        if (cudaMemsetAsync(d, 0, n, s) != cudaSuccess) return MOE_ERR_CUDA;
+        ++launches;
+      }
+    set_last_launch_count(launches);
+    return MOE_OK;
+  }
+  const bool has_branch = branch != nullptr, pre = w_pre != nullptr;
+  if (!d_residual || has_branch != (d_branch != nullptr) || pre != (d_normed != nullptr) ||
+      (pre && !residual_out))
+    return MOE_ERR_INVALID_ARG;
+  if (!has_branch && (w_post || gate || p->gate_kind != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (p->gate_kind != MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((d_w_post != nullptr) != (w_post != nullptr) || (d_gate != nullptr) != (gate != nullptr) ||
+      (d_w_pre != nullptr) != pre)
+    return MOE_ERR_INVALID_ARG;
+  if (!has_branch && !pre) return MOE_ERR_INVALID_ARG;
+  NormParams k = norm_params(p);
+  if (d_residual == d_residual_out && k.ld_residual != k.ld_residual_out)
+    return MOE_ERR_INVALID_ARG;
+  RowCheck c;
+  c.wide = p->H % 8 == 0;
+  c.add(branch, p->branch_dtype, k.ld_branch);
+  c.add(d_branch, p->branch_dtype, k.ld_branch);
+  c.add(d_normed, p->branch_dtype, k.ld_normed);
+  c.add(residual_out, p->residual_dtype, k.ld_residual_out);
+  c.add(d_residual_out, p->residual_dtype, k.ld_residual_out);
+  c.add(d_residual, p->residual_dtype, k.ld_residual);
+  for (const void* w : {w_post, w_pre, gate, static_cast<const void*>(d_gate)})
+    c.add(w, p->weight_dtype, p->H);
+  if (!c.ok) return MOE_ERR_MISALIGNED;
+  const bool wf = p->weight_dtype == MOE_DTYPE_F32;
+  k.branch = branch;
+  k.residual = residual_out;
+  k.w_post = {w_post, wf};
+  k.w_pre = {w_pre, wf};
+  k.gate = {gate, wf};
+  k.d_residual_out = d_residual_out;
+  k.d_normed = d_normed;
+  k.d_residual = d_residual;
+  k.d_branch = d_branch;
+  k.d_gate = d_gate;
+  const bool cols = pre || w_post || channel;
+  k.part = cols ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kNormHeader) : nullptr;
+  const int blocks = norm_bwd_blocks(p->T, p->H);
+  if (launch_norm<true>(p, k, c.wide, blocks, s) != cudaSuccess) return MOE_ERR_CUDA;
+  ++launches;
+  if (cols) {
+    if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32)), dim3(256), 0, s, 1,
+                      static_cast<const float*>(k.part), blocks, p->H, k.w_post, k.gate,
+                      channel ? 1 : 0, p->weight_offset, d_w_pre, d_w_post, d_gate) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    ++launches;
+  }
+  set_last_launch_count(launches);
+  return MOE_OK;
+}

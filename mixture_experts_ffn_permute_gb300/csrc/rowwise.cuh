@@ -1,0 +1,215 @@
+// Row access shared by the operators around the expert layer: eight elements
+// of a row per thread and step, held as loaded (bf16 pairs stay packed), as
+// 16-byte vectors where the rows allow it and as single elements otherwise;
+// and sums over a row's threads.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace moe {
+
+struct Bf16 {
+  uint16_t bits;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(Bf16 x) {
+  return __uint_as_float(static_cast<uint32_t>(x.bits) << 16);
+}
+__device__ __forceinline__ void from_float(float& d, float x) { d = x; }
+__device__ __forceinline__ void from_float(Bf16& d, float x) {
+  d.bits = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+// 16 bytes that are read (written) once: past L1, so that the weights stay.
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_stream16(void* p, uint4 v) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// Eight elements as loaded.
+template <typename T>
+struct Oct;
+
+template <>
+struct Oct<Bf16> {
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int j) const {
+    return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+  __device__ __forceinline__ void load(const Bf16* p) {
+    const uint4 v = load_stream16(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void store(Bf16* p) const {
+    store_stream16(p, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  __device__ __forceinline__ void set_bits(int j, Bf16 x) {
+    if (j & 1) w[j >> 1] |= static_cast<uint32_t>(x.bits) << 16;
+    else w[j >> 1] = x.bits;
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+  }
+};
+
+template <>
+struct Oct<float> {
+  float f[8];
+  __device__ __forceinline__ float get(int j) const { return f[j]; }
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = load_stream16(p + 4 * h);
+      f[4 * h] = __uint_as_float(v.x), f[4 * h + 1] = __uint_as_float(v.y);
+      f[4 * h + 2] = __uint_as_float(v.z), f[4 * h + 3] = __uint_as_float(v.w);
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      store_stream16(p + 4 * h,
+                     make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
+                                __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])));
+  }
+  __device__ __forceinline__ void set_bits(int j, float x) { f[j] = x; }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = x[i];
+  }
+};
+
+// The columns of step v of thread `tid` of `n` threads on a row: kWide, eight
+// neighbours (a 16-byte vector of bf16, two of fp32; the width is a multiple
+// of 8); otherwise eight single columns n apart, so that the threads' single
+// loads stay coalesced.
+template <bool kWide>
+__device__ __forceinline__ int oct_col(int v, int j, int tid, int n) {
+  return kWide ? (v * n + tid) * 8 + j : (v * 8 + j) * n + tid;
+}
+
+template <bool kWide, typename T>
+__device__ __forceinline__ void load_oct(Oct<T>& o, const T* row, int v, int tid, int n, int H) {
+  if (kWide) {
+    const int c = oct_col<true>(v, 0, tid, n);
+    if (c < H) {
+      o.load(row + c);
+    } else {
+      const float z[8] = {};
+      o.set(z);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = oct_col<false>(v, j, tid, n);
+      T x{};
+      if (c < H) x = row[c];
+      o.set_bits(j, x);
+    }
+  }
+}
+
+template <bool kWide, typename T>
+__device__ __forceinline__ void store_oct(const float (&x)[8], T* row, int v, int tid, int n,
+                                          int H) {
+  if (kWide) {
+    const int c = oct_col<true>(v, 0, tid, n);
+    if (c < H) {
+      Oct<T> o;
+      o.set(x);
+      o.store(row + c);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = oct_col<false>(v, j, tid, n);
+      if (c < H) from_float(row[c], x[j]);
+    }
+  }
+}
+
+// A weight vector whose type is known at run time only (bf16 or fp32).
+struct WeightPtr {
+  const void* p;
+  bool f32;
+  __device__ __forceinline__ float at(long c) const {
+    return f32 ? __ldg(static_cast<const float*>(p) + c)
+               : __uint_as_float(
+                     static_cast<uint32_t>(__ldg(static_cast<const unsigned short*>(p) + c)) << 16);
+  }
+};
+
+template <bool kWide>
+__device__ __forceinline__ void load_weight8(float (&x)[8], const WeightPtr& w, long at0, int v,
+                                             int tid, int n, int H) {
+  if (kWide) {
+    const int c = oct_col<true>(v, 0, tid, n);
+    if (c >= H) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    } else if (w.f32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(w.p) + at0 + c);
+      const float4 a = __ldg(q), b = __ldg(q + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      const uint4 a =
+          __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(w.p) + at0 + c));
+      x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
+      x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = oct_col<false>(v, j, tid, n);
+      x[j] = c < H ? w.at(at0 + c) : 0.f;
+    }
+  }
+}
+
+// Sums over the threads of one row, every thread getting the totals.  kWarp:
+// the row's threads are one warp.  Otherwise they are the block, `s` is
+// kN * 32 floats of shared memory that the next call must not share with this
+// one (two buffers alternate), and the order of the sum is fixed.
+template <bool kWarp, int kN>
+__device__ __forceinline__ void row_sum(float (&x)[kN], float* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  if (kWarp) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s[i * 32 + warp] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    x[i] = lane < nw ? s[i * 32 + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,87 @@
+"""CPU checks of the entry points of include/moe_block.h: bad arguments are
+refused on the host, before any CUDA call (no kernel is launched here)."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_ffn_permute_gb300 as moe
+from mixture_experts_ffn_permute_gb300 import _build
+
+A = 1 << 20  # a 256-byte aligned address that is never dereferenced
+BIG = 1 << 50
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return moe.load()
+
+
+def norm(gate="none", **kw):
+    fields = {k: kw.pop(k) for k in list(kw) if k in ("T", "H", "branch_dtype", "gate_kind")}
+    p = moe.NormProblem.make(8, 64, gate=gate, **kw)
+    for k, v in fields.items():
+        setattr(p, k, v)
+    return p
+
+
+def norm_fwd(lib, p, **kw):
+    a = dict(branch=A, w_post=A, gate=None, residual=A, w_pre=A, residual_out=A, normed=A)
+    a.update(kw)
+    return lib.moe_block_norm_forward(ctypes.byref(p), *a.values(), None)
+
+
+def norm_bwd(lib, p, **kw):
+    a = dict(branch=A, w_post=A, gate=None, residual_out=A, w_pre=A, d_residual_out=A, d_normed=A,
+             d_residual=A, d_branch=A, d_w_post=A, d_gate=None, d_w_pre=A, ws=A, n=BIG)
+    a.update(kw)
+    return lib.moe_block_norm_backward(ctypes.byref(p), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), 1), (dict(H=0), 1), (dict(H=16385), 2), (dict(branch_dtype=2), 1),
+    (dict(gate_kind=4), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(ld_branch=63), 1), (dict(ld_normed=-64), 1), (dict(ld_residual=1 << 41), 1)])
+def test_norm_rejects_bad_problems(lib, kw, code):
+    assert norm_fwd(lib, norm(**kw)) == code
+    assert norm_bwd(lib, norm(**kw)) == code
+    assert lib.moe_block_norm_workspace_size(ctypes.byref(norm(**kw))) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(residual=None), 1), (dict(residual_out=None), 1), (dict(branch=None), 1),
+    (dict(w_pre=None), 1), (dict(normed=None), 1), (dict(gate=A), 1),
+    (dict(branch=None, residual_out=None), 1),  # a post norm without a branch
+    (dict(branch=None, residual_out=None, w_post=None, w_pre=None, normed=None), 1),
+    (dict(branch=A + 1), 3), (dict(w_pre=A + 1), 3), (dict(normed=A + 1), 3)])
+def test_norm_forward_rejects_bad_tensors(lib, kw, code):
+    assert norm_fwd(lib, norm(), **kw) == code
+
+
+def test_norm_forward_rejects_missing_gate_and_in_place_strides(lib):
+    assert norm_fwd(lib, norm("channel")) == 1
+    assert norm_fwd(lib, norm(ld_residual=128)) == 1  # residual_out is residual, other stride
+    assert lib.moe_block_norm_forward(None, *[A] * 7, None) == 1
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(d_residual=None), 1), (dict(d_branch=None), 1), (dict(d_normed=None), 1),
+    (dict(residual_out=None), 1), (dict(d_w_post=None), 1), (dict(d_w_pre=None), 1),
+    (dict(d_gate=A), 1), (dict(ws=None), 1), (dict(ws=A + 16), 3), (dict(n=255), 4),
+    (dict(d_w_post=A + 1), 3), (dict(d_residual=A + 1), 3),
+    (dict(branch=None, d_branch=None), 1)])
+def test_norm_backward_rejects_bad_tensors(lib, kw, code):
+    assert norm_bwd(lib, norm(), **kw) == code
+
+
+def test_norm_problem_rejects_unknown_options():
+    with pytest.raises(ValueError):
+        moe.NormProblem.make(4, 64, gate="row")
+    with pytest.raises(ValueError):
+        moe.NormProblem.make(4, 64, branch_dtype=torch.float16)
+
+
+def test_norm_without_rows_launches_nothing(lib):
+    assert norm_fwd(lib, norm(T=0), branch=None, residual=None, residual_out=None) == 0
+    assert moe.last_launch_count() == 0
