@@ -96,6 +96,62 @@ MOE_API int moe_block_norm_backward(const moe_norm_problem* p, const void* branc
                                     void* d_gate, void* d_w_pre, void* ws, size_t ws_bytes,
                                     void* stream);
 
+/* ---- Gradient clipping by the global norm ---------------------------------
+ *   norm = grad_scale * sqrt(sum over all tensors and elements of grad^2)
+ *   coef = min(1, max_norm / (norm + eps))
+ *   out  = grad * (grad_scale * coef)
+ * grad_scale undoes a loss scale in the same pass.  Squares are summed in
+ * fp32 over at most 128 elements of one thread, those sums in fp64; a
+ * thread's sum that overflows fp32 or falls below 2^-80 is taken again in
+ * fp64, so the norm overflows only where it is above the fp32 range itself. */
+typedef struct moe_grad_tensor {
+  const void* grad; /* device, numel elements, dense; any element alignment */
+  void* out;        /* device, same type; may be grad; NULL: counted, not written */
+  int64_t numel;
+  int32_t dtype; /* moe_dtype */
+  int32_t reserved;
+} moe_grad_tensor;
+
+#define MOE_MAX_GRAD_TENSORS (1 << 16)
+
+/* Bytes of workspace for n tensors (0 if n is out of range). */
+MOE_API size_t moe_clip_workspace_size(int32_t n);
+
+/*   tensors   [n] in HOST memory, read before the call returns
+ *   max_norm  >= 0; +infinity: only grad_scale is applied
+ *   norm_out  [2] fp32 device out: norm and coef
+ * A norm that is not finite gives the coef its formula has (0 for infinity,
+ * NaN for NaN); the caller can read it from norm_out.  In place, a factor of
+ * exactly 1 writes nothing. */
+MOE_API int moe_clip_grad_norm(int32_t n, const moe_grad_tensor* tensors, float grad_scale,
+                               float max_norm, float eps, float* norm_out, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* ---- Embedding ------------------------------------------------------------ */
+typedef struct moe_embed_problem {
+  int32_t T, V, H;      /* tokens, vocabulary, width */
+  int32_t table_dtype;  /* moe_dtype of table and d_table */
+  int32_t out_dtype;    /* of out and d_out */
+  float scale;
+} moe_embed_problem;
+
+/* out[t] = scale * table[ids[t]]; a zero row for a masked token.
+ *   ids [T] int32, table [V, H], out [T, H], dense
+ *   ws  optional (NULL): any workspace whose status word gets the report of
+ *       an id at or above V */
+MOE_API int moe_embedding_forward(const moe_embed_problem* p, const int32_t* ids,
+                                  const void* table, void* out, void* ws, void* stream);
+
+/* Bytes of workspace of the backward (0 if the problem is invalid). */
+MOE_API size_t moe_embedding_workspace_size(const moe_embed_problem* p);
+
+/* d_table[v] = scale * sum of d_out[t] over the tokens with ids[t] = v, for
+ * every v (zero rows where there is none; masked tokens count nowhere).  The
+ * tokens are sorted by id (stable), so the order of the sums is fixed. */
+MOE_API int moe_embedding_backward(const moe_embed_problem* p, const int32_t* ids,
+                                   const void* d_out, void* d_table, void* ws, size_t ws_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -62,7 +62,53 @@ class NormProblem(ctypes.Structure):
         return p
 
 
+class EmbedProblem(ctypes.Structure):
+    """Mirror of ``moe_embed_problem``; made with ``EmbedProblem.make``."""
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, T, V, H, table_dtype=torch.bfloat16, out_dtype=torch.bfloat16, scale=1.0):
+        p = cls(int(T), int(V), int(H), _dtype(table_dtype), _dtype(out_dtype), float(scale))
+        p._ids, p._out, p._table = (p.T,), (p.T, p.H), (p.V, p.H)
+        p._t, p._o = table_dtype, out_dtype
+        return p
+
+
+class _GradTensor(ctypes.Structure):
+    """Mirror of ``moe_grad_tensor``."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GradList:
+    """The gradient tensors of a model, as ``clip_grad_norm`` takes them: dense CUDA tensors of
+    bf16 and fp32, and where each clipped gradient goes (``outs``; default: in place; None in the
+    list: counted in the norm, not written).  It keeps the tensors alive and is made anew when
+    they are replaced."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("one output (or None) for each gradient")
+        self.table = (_GradTensor * len(self.grads))()
+        for e, g, o in zip(self.table, self.grads, self.outs):
+            e.grad, e.numel, e.dtype = _dense(g, g.dtype, g.shape), g.numel(), _dtype(g.dtype)
+            e.out = _dense(o, g.dtype, g.shape)
+
+    def __len__(self):
+        return len(self.grads)
+
+
 SIGS = {
+    "moe_clip_workspace_size": ([ctypes.c_int32], _sz),
+    "moe_clip_grad_norm": ([ctypes.c_int32, _vp] + [ctypes.c_float] * 3 + [_vp, _vp, _sz, _vp],
+                           _ci),
+    "moe_embedding_forward": ([_vp] * 6, _ci),
+    "moe_embedding_workspace_size": ([_vp], _sz),
+    "moe_embedding_backward": ([_vp] * 5 + [_sz, _vp], _ci),
     "moe_block_norm_forward": ([_vp] * 9, _ci),
     "moe_block_norm_workspace_size": ([_vp], _sz),
     "moe_block_norm_backward": ([_vp] * 14 + [_sz, _vp], _ci),
@@ -152,5 +198,48 @@ def block_norm_backward(p: NormProblem, residual_out, d_residual, ws, branch=Non
         raise MoEError("moe_block_norm_backward", rc)
 
 
-__all__ = ["NormProblem", "block_norm_forward", "block_norm_backward",
+def alloc_clip_workspace(grads: GradList, device="cuda") -> torch.Tensor:
+    """The workspace of ``clip_grad_norm``."""
+    return _ws_of(load().moe_clip_workspace_size(len(grads)), "moe_clip_workspace_size", device)
+
+
+def clip_grad_norm(grads: GradList, max_norm: float, norm, ws, grad_scale: float = 1.0,
+                   eps: float = 1e-6, stream=None) -> None:
+    """Scales every gradient by ``grad_scale * min(1, max_norm / (total + eps))`` with total =
+    grad_scale * their global L2 norm; ``norm`` ([2] fp32, on the GPU) gets total and the
+    coefficient.  Nothing is read back to the host."""
+    rc = load().moe_clip_grad_norm(len(grads.grads), ctypes.addressof(grads.table), grad_scale,
+                                   max_norm, eps, _dense(norm, torch.float32, (2,)),
+                                   ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_clip_grad_norm", rc)
+
+
+def embedding_forward(p: EmbedProblem, ids, table, out, ws=None, stream=None) -> None:
+    """out[t] = scale * table[ids[t]] (int32 ids; a zero row where negative).  With ``ws`` (any
+    workspace) an id outside the vocabulary is recorded in its status word."""
+    rc = load().moe_embedding_forward(
+        ctypes.byref(p), _dense(ids, torch.int32, p._ids), _dense(table, p._t, p._table),
+        _dense(out, p._o, p._out), ws.data_ptr() if ws is not None else None, _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_embedding_forward", rc)
+
+
+def alloc_embedding_workspace(p: EmbedProblem, device="cuda") -> torch.Tensor:
+    """The workspace of ``embedding_backward``."""
+    return _ws_of(load().moe_embedding_workspace_size(ctypes.byref(p)),
+                  "moe_embedding_workspace_size", device)
+
+
+def embedding_backward(p: EmbedProblem, ids, d_out, d_table, ws, stream=None) -> None:
+    """d_table[v] = scale * sum of d_out over the tokens of id v, every row written."""
+    rc = load().moe_embedding_backward(
+        ctypes.byref(p), _dense(ids, torch.int32, p._ids), _dense(d_out, p._o, p._out),
+        _dense(d_table, p._t, p._table), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_embedding_backward", rc)
+
+
+__all__ = ["NormProblem", "EmbedProblem", "GradList", "clip_grad_norm", "alloc_clip_workspace",
+           "embedding_forward", "embedding_backward", "alloc_embedding_workspace", "block_norm_forward", "block_norm_backward",
            "alloc_block_norm_workspace", "DTYPE_BF16", "DTYPE_F32"]

@@ -85,3 +85,78 @@ def test_norm_problem_rejects_unknown_options():
 def test_norm_without_rows_launches_nothing(lib):
     assert norm_fwd(lib, norm(T=0), branch=None, residual=None, residual_out=None) == 0
     assert moe.last_launch_count() == 0
+
+
+# ------------------------------------------------------------------ clipping
+def table(*rows):
+    """moe_grad_tensor rows of (grad, out, numel, dtype)."""
+    t = (moe.block._GradTensor * max(1, len(rows)))()
+    for e, (e.grad, e.out, e.numel, e.dtype) in zip(t, rows):
+        pass
+    return t
+
+
+def clip(lib, rows=((A, A, 8, 0),), n=None, scale=1.0, max_norm=1.0, eps=1e-6, out=A, ws=A,
+         ws_bytes=BIG):
+    return lib.moe_clip_grad_norm(len(rows) if n is None else n, table(*rows), scale, max_norm,
+                                  eps, out, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), 1), (dict(n=65537), 2), (dict(out=None), 1), (dict(out=A + 2), 3),
+    (dict(ws=None), 1), (dict(ws=A + 128), 3), (dict(ws_bytes=256), 4), (dict(max_norm=-1.0), 1),
+    (dict(max_norm=float("nan")), 1), (dict(eps=-1e-6), 1), (dict(eps=float("inf")), 1),
+    (dict(scale=float("inf")), 1), (dict(rows=((A, A, 8, 2),)), 1),
+    (dict(rows=((A, A, -1, 0),)), 1), (dict(rows=((None, A, 8, 0),)), 1),
+    (dict(rows=((A + 1, A, 8, 0),)), 3), (dict(rows=((A, A + 2, 8, 1),)), 3),
+    (dict(rows=((A, A, 1 << 43, 0),)), 2), (dict(rows=((A, A, 1 << 42, 0),) * 3), 2)])
+def test_clip_rejects(lib, kw, code):
+    assert clip(lib, **kw) == code
+
+
+def test_clip_workspace_size(lib):
+    assert lib.moe_clip_workspace_size(-1) == 0
+    assert lib.moe_clip_workspace_size(65537) == 0
+    assert 0 < lib.moe_clip_workspace_size(0) <= lib.moe_clip_workspace_size(65536)
+
+
+def test_grad_list_refuses():
+    with pytest.raises(ValueError):
+        moe.GradList([torch.zeros(4)])  # not on the GPU
+    with pytest.raises(ValueError):
+        moe.GradList([], [None])
+
+
+# ------------------------------------------------------------------ embedding
+def embed(**kw):
+    p = moe.EmbedProblem.make(8, 100, 64)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), 1), (dict(V=0), 1), (dict(H=0), 1), (dict(table_dtype=5), 1),
+    (dict(out_dtype=-1), 1), (dict(H=(1 << 20) + 1), 2), (dict(V=(1 << 28) + 1), 2),
+    (dict(V=1 << 28, H=1 << 20), 2)])
+def test_embedding_rejects_bad_problems(lib, kw, code):
+    p = embed(**kw)
+    assert lib.moe_embedding_forward(ctypes.byref(p), A, A, A, None, None) == code
+    assert lib.moe_embedding_backward(ctypes.byref(p), A, A, A, A, BIG, None) == code
+    assert lib.moe_embedding_workspace_size(ctypes.byref(p)) == 0
+
+
+def test_embedding_rejects_bad_tensors(lib):
+    p = ctypes.byref(embed())
+    fwd, bwd = lib.moe_embedding_forward, lib.moe_embedding_backward
+    for i in range(3):
+        a = [A, A, A]
+        a[i] = None
+        assert fwd(p, *a, None, None) == 1 and bwd(p, *a, A, BIG, None) == 1
+        a[i] = A + 1
+        assert fwd(p, *a, None, None) == 3 and bwd(p, *a, A, BIG, None) == 3
+    assert fwd(p, A, A, A, A + 4, None) == 3
+    assert bwd(p, A, A, A, None, BIG, None) == 1
+    assert bwd(p, A, A, A, A + 4, BIG, None) == 3
+    assert bwd(p, A, A, A, A, lib.moe_embedding_workspace_size(p) - 1, None) == 4
+    assert fwd(None, A, A, A, None, None) == 1
