@@ -152,6 +152,41 @@ MOE_API int moe_embedding_backward(const moe_embed_problem* p, const int32_t* id
                                    const void* d_out, void* d_table, void* ws, size_t ws_bytes,
                                    void* stream);
 
+/* ---- Linear cross entropy --------------------------------------------------
+ * With the logits z_tv = logit_scale * <x_t, w_v> of token t, which are
+ * computed tile by tile on the tensor cores (fp32 accumulation) and never
+ * kept whole:
+ *   lse[t]  = log sum_v exp(z_tv)
+ *   loss[t] = lse[t] - z_t,labels[t]   (0 for a masked token)
+ * and, given the gradients d_loss [T] of loss and (optionally) d_lse [T] of
+ * lse, with d_loss[t] taken as 0 for a masked token:
+ *   d z_tv = (d_loss[t] + d_lse[t]) exp(z_tv - lse[t]) - d_loss[t] [v = labels[t]]
+ *   dx[t]  = logit_scale * sum_v d z_tv w_v
+ *   dw[v]  = logit_scale * sum_t d z_tv x_t
+ * x [T, H] and w [V, H] bf16, dense, 16-byte aligned; H a multiple of 8;
+ * loss, lse, d_loss, d_lse fp32.  The backward recomputes the logits in pieces
+ * of the vocabulary and rounds d z to bf16 for its two products, as the layer's
+ * backward does its intermediate gradients; sums are fp32. */
+typedef struct moe_ce_problem {
+  int32_t T, H, V;
+  float logit_scale;
+} moe_ce_problem;
+
+/* Bytes of workspace of the forward, and of both directions (0 if the problem
+ * is invalid). */
+MOE_API size_t moe_linear_ce_workspace_size(const moe_ce_problem* p);
+MOE_API size_t moe_linear_ce_backward_workspace_size(const moe_ce_problem* p);
+
+MOE_API int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, const void* w,
+                                  const int32_t* labels, float* loss, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* lse as the forward wrote it; d_lse may be NULL (zero). */
+MOE_API int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, const void* w,
+                                   const int32_t* labels, const float* lse, const float* d_loss,
+                                   const float* d_lse, void* dx, void* dw, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libmoeffn.so")
 SOURCES = ["api.cu", "route_permute.cu", "grouped_gemm.cu", "grouped_gemm_swap.cu",
            "grouped_gemm_fp4.cu", "grouped_gemm_swap2.cu", "grouped_gemm_fp4_pair.cu",
            "grouped_gemm_bwd.cu", "grouped_mlp_decode.cu", "route_backward.cu", "noalloc.cu",
-           "selftest.cu", "block_norm.cu", "grad_clip.cu", "embedding.cu"]
+           "selftest.cu", "block_norm.cu", "grad_clip.cu", "embedding.cu",
+           "linear_ce.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

@@ -76,6 +76,18 @@ class EmbedProblem(ctypes.Structure):
         return p
 
 
+class CEProblem(ctypes.Structure):
+    """Mirror of ``moe_ce_problem``; made with ``CEProblem.make``."""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("logit_scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, T, H, V, logit_scale=1.0):
+        p = cls(int(T), int(H), int(V), float(logit_scale))
+        p._rows, p._x, p._w = (p.T,), (p.T, p.H), (p.V, p.H)
+        return p
+
+
 class _GradTensor(ctypes.Structure):
     """Mirror of ``moe_grad_tensor``."""
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
@@ -103,6 +115,10 @@ class GradList:
 
 
 SIGS = {
+    "moe_linear_ce_workspace_size": ([_vp], _sz),
+    "moe_linear_ce_backward_workspace_size": ([_vp], _sz),
+    "moe_linear_ce_forward": ([_vp] * 7 + [_sz, _vp], _ci),
+    "moe_linear_ce_backward": ([_vp] * 10 + [_sz, _vp], _ci),
     "moe_clip_workspace_size": ([ctypes.c_int32], _sz),
     "moe_clip_grad_norm": ([ctypes.c_int32, _vp] + [ctypes.c_float] * 3 + [_vp, _vp, _sz, _vp],
                            _ci),
@@ -240,6 +256,37 @@ def embedding_backward(p: EmbedProblem, ids, d_out, d_table, ws, stream=None) ->
         raise MoEError("moe_embedding_backward", rc)
 
 
-__all__ = ["NormProblem", "EmbedProblem", "GradList", "clip_grad_norm", "alloc_clip_workspace",
+def alloc_linear_ce_workspace(p: CEProblem, backward: bool = False, device="cuda") -> torch.Tensor:
+    """The workspace of ``linear_ce_forward``, or of both directions."""
+    fn = "moe_linear_ce_backward_workspace_size" if backward else "moe_linear_ce_workspace_size"
+    return _ws_of(getattr(load(), fn)(ctypes.byref(p)), fn, device)
+
+
+def linear_ce_forward(p: CEProblem, x, w, labels, loss, lse, ws, stream=None) -> None:
+    """loss[t] = logsumexp_v(z) - z[labels[t]] and lse [T] fp32 of the logits z = logit_scale *
+    x w^T (x [T, H], w [V, H] bf16), which are not kept.  A negative label masks its token."""
+    rc = load().moe_linear_ce_forward(
+        ctypes.byref(p), _dense(x, torch.bfloat16, p._x), _dense(w, torch.bfloat16, p._w),
+        _dense(labels, torch.int32, p._rows), _dense(loss, torch.float32, p._rows),
+        _dense(lse, torch.float32, p._rows), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_linear_ce_forward", rc)
+
+
+def linear_ce_backward(p: CEProblem, x, w, labels, lse, d_loss, dx, dw, ws, d_lse=None,
+                       stream=None) -> None:
+    """dx [T, H] and dw [V, H] (bf16) from the gradients of loss and, optionally, of lse."""
+    rc = load().moe_linear_ce_backward(
+        ctypes.byref(p), _dense(x, torch.bfloat16, p._x), _dense(w, torch.bfloat16, p._w),
+        _dense(labels, torch.int32, p._rows), _dense(lse, torch.float32, p._rows),
+        _dense(d_loss, torch.float32, p._rows), _dense(d_lse, torch.float32, p._rows),
+        _dense(dx, torch.bfloat16, p._x), _dense(dw, torch.bfloat16, p._w), ws.data_ptr(),
+        ws.numel(), _raw_stream(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_linear_ce_backward", rc)
+
+
+__all__ = ["NormProblem", "EmbedProblem", "CEProblem", "linear_ce_forward", "linear_ce_backward",
+           "alloc_linear_ce_workspace", "GradList", "clip_grad_norm", "alloc_clip_workspace",
            "embedding_forward", "embedding_backward", "alloc_embedding_workspace", "block_norm_forward", "block_norm_backward",
            "alloc_block_norm_workspace", "DTYPE_BF16", "DTYPE_F32"]

@@ -160,3 +160,63 @@ def test_embedding_rejects_bad_tensors(lib):
     assert bwd(p, A, A, A, A + 4, BIG, None) == 3
     assert bwd(p, A, A, A, A, lib.moe_embedding_workspace_size(p) - 1, None) == 4
     assert fwd(None, A, A, A, None, None) == 1
+
+
+# ------------------------------------------------------------------ linear cross entropy
+def ce(**kw):
+    p = moe.CEProblem.make(8, 64, 100)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+def ce_fwd(lib, p, **kw):
+    a = dict(x=A, w=A, labels=A, loss=A, lse=A, ws=A, n=BIG)
+    a.update(kw)
+    return lib.moe_linear_ce_forward(ctypes.byref(p), *a.values(), None)
+
+
+def ce_bwd(lib, p, **kw):
+    a = dict(x=A, w=A, labels=A, lse=A, d_loss=A, d_lse=None, dx=A, dw=A, ws=A, n=BIG)
+    a.update(kw)
+    return lib.moe_linear_ce_backward(ctypes.byref(p), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), 1), (dict(H=0), 1), (dict(V=0), 1), (dict(logit_scale=float("nan")), 1),
+    (dict(H=65), 2), (dict(H=(1 << 20) + 8), 2), (dict(V=(1 << 26) + 1), 2),
+    (dict(T=1 << 26, V=1 << 26), 2)])
+def test_ce_rejects_bad_problems(lib, kw, code):
+    p = ce(**kw)
+    assert ce_fwd(lib, p) == code and ce_bwd(lib, p) == code
+    assert lib.moe_linear_ce_workspace_size(ctypes.byref(p)) == 0
+    assert lib.moe_linear_ce_backward_workspace_size(ctypes.byref(p)) == 0
+
+
+@pytest.mark.parametrize("name", ["x", "w", "labels", "lse"])
+def test_ce_rejects_bad_tensors(lib, name):
+    for f in (ce_fwd, ce_bwd):
+        assert f(lib, ce(), **{name: None}) == 1
+        assert f(lib, ce(), **{name: A + 2}) == 3
+
+
+def test_ce_rejects_outputs_and_workspaces(lib):
+    p = ce()
+    assert ce_fwd(lib, p, loss=None) == 1 and ce_fwd(lib, p, loss=A + 2) == 3
+    for k in ("d_loss", "dx", "dw"):
+        assert ce_bwd(lib, p, **{k: None}) == 1 and ce_bwd(lib, p, **{k: A + 2}) == 3
+    assert ce_bwd(lib, p, d_lse=A + 2) == 3
+    for f, size in ((ce_fwd, lib.moe_linear_ce_workspace_size), (ce_bwd, None)):
+        assert f(lib, p, ws=None) == 1 and f(lib, p, ws=A + 128) == 3
+        assert f(lib, p, n=256) == 4
+    n = lib.moe_linear_ce_workspace_size(ctypes.byref(p))
+    assert ce_fwd(lib, p, n=n - 1) == 4
+    # one workspace serves both directions
+    assert lib.moe_linear_ce_backward_workspace_size(ctypes.byref(p)) >= n
+
+
+def test_ce_workspace_does_not_hold_the_logits(lib):
+    """A batch whose logits would take 17 GB in bf16."""
+    p = moe.CEProblem.make(65536, 4096, 131072)
+    logits = 2 * 65536 * 131072
+    assert lib.moe_linear_ce_backward_workspace_size(ctypes.byref(p)) < logits / 8
