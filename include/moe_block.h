@@ -165,8 +165,8 @@ MOE_API int moe_embedding_backward(const moe_embed_problem* p, const int32_t* id
  *   dw[v]  = logit_scale * sum_t d z_tv x_t
  * x [T, H] and w [V, H] bf16, dense, 16-byte aligned; H a multiple of 8;
  * loss, lse, d_loss, d_lse fp32.  The backward recomputes the logits in pieces
- * of the vocabulary and rounds d z to bf16 for its two products, as the layer's
- * backward does its intermediate gradients; sums are fp32. */
+ * of the vocabulary and rounds d z / max |d_loss| to bf16 for its two products,
+ * as the layer's backward does its intermediate gradients; sums are fp32. */
 typedef struct moe_ce_problem {
   int32_t T, H, V;
   float logit_scale;

@@ -160,6 +160,7 @@ block_norm_bwd_kernel(const NormParams p) {
   const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr,
              pre = p.d_normed != nullptr;
   float acc_pre[kSteps][8] = {}, acc_post[kSteps][8] = {};
+  int sums = 0;  // the row sums' two buffers alternate
   const long stride = static_cast<long>(gridDim.x) * (kWarp ? 8 : 1);
   for (long row = kWarp ? static_cast<long>(blockIdx.x) * 8 + warp : blockIdx.x; row < p.T;
        row += stride) {
@@ -195,7 +196,7 @@ block_norm_bwd_kernel(const NormParams p) {
         if (post) s3[2] = fmaf(y[v].get(j), y[v].get(j), s3[2]);
       }
     }
-    row_sum<kWarp>(s3, s_sum[0]);
+    row_sum<kWarp>(s3, s_sum[sums++ & 1]);
     const float rstd = pre ? rsqrtf(fmaf(s3[0], p.inv_h, p.eps)) : 0.f;
     const float mean_au = rstd * s3[1] * p.inv_h;
     const float ystd = post ? rsqrtf(fmaf(s3[2], p.inv_h, p.eps)) : 1.f;
@@ -265,7 +266,7 @@ block_norm_bwd_kernel(const NormParams p) {
     }
     float mean_cv = 0.f;
     if (post || p.gate_kind == MOE_GATE_TOKEN) {
-      row_sum<kWarp>(s1, s_sum[1]);
+      row_sum<kWarp>(s1, s_sum[sums++ & 1]);
       if (post) mean_cv = s1[0] * p.inv_h;
       if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) {
         if (p.w_post.f32) static_cast<float*>(p.d_gate)[row] = s1[0];
@@ -315,6 +316,302 @@ block_norm_bwd_kernel(const NormParams p) {
   }
 }
 
+// ------------------------------------------------------------------ streamed rows
+// The same rows and sums for many rows of 16-byte accesses: a block stays on its
+// SM, keeps its columns' weights in registers and copies the rows to come into
+// shared memory (cp.async, every thread its own octets) while it works on the
+// present one, so that the two row sums' barriers do not leave HBM idle.  The
+// phases read their octets from shared memory again rather than hold them.
+constexpr int kMaxDepth = 4;  // rows in shared memory, the present one among them
+
+// weight + offset, times `scale` and (channel gate) the gate, of this thread's
+// columns; zero past the row
+__device__ __forceinline__ void load_weights(float (&w)[8], const NormParams& p,
+                                             const WeightPtr& ptr, bool gated, float scale, int v,
+                                             int tid, int n) {
+  if (ptr.p) {
+    load_weight8<true>(w, ptr, 0, v, tid, n, p.H);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = scale * (w[j] + p.offset);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = scale;
+  }
+  if (gated && p.gate_kind == MOE_GATE_CHANNEL) {
+    float g[8];
+    load_weight8<true>(g, p.gate, 0, v, tid, n, p.H);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] *= g[j];
+  }
+}
+
+template <typename TB, typename TR, int kSteps>
+__global__ void __launch_bounds__(512, 1)
+block_norm_fwd_stream_kernel(const NormParams p, int depth) {
+  pdl_enter();
+  __shared__ float s_sum[2][32];
+  extern __shared__ __align__(16) uint8_t s_rows[];
+  const int tid = threadIdx.x, n = blockDim.x;
+  const uint32_t yb = n * 16 * oct_vecs<TB>(), rb = n * 16 * oct_vecs<TR>();  // bytes of a step
+  const uint32_t row_bytes = kSteps * (yb + rb), ring = smem_u32(s_rows);
+  const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr;
+  auto fetch = [&](long row, int slot) {
+    if (row < p.T) {
+      const uint32_t at = ring + slot * row_bytes;
+#pragma unroll
+      for (int v = 0; v < kSteps; ++v) {
+        const int c = oct_col<true>(v, 0, tid, n);
+        if (c >= p.H) continue;
+        if (has_branch)
+          oct_copy(at + v * yb, static_cast<const TB*>(p.branch) + row * p.ld_branch + c, tid, n);
+        oct_copy(at + kSteps * yb + v * rb,
+                 static_cast<const TR*>(p.residual) + row * p.ld_residual + c, tid, n);
+      }
+    }
+    copy_async_commit();
+  };
+  const long stride = gridDim.x;
+  for (int i = 0; i < depth - 1; ++i) fetch(blockIdx.x + i * stride, i);
+  float w_post[kSteps][8], w_pre[kSteps][8];
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+    load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
+    load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
+  }
+  int slot = 0, sums = 0;  // the row sums' two buffers alternate
+  for (long row = blockIdx.x; row < p.T; row += stride) {
+    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    copy_async_wait(depth - 1);
+    const uint32_t at = ring + slot * row_bytes;
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    float x[kSteps][8];  // residual_out, unrounded
+    if (has_branch) {
+      float scale = p.gate_kind == MOE_GATE_TOKEN ? p.gate.at(row) : 1.f;
+      if (post) {
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < kSteps; ++v) {
+          if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+          Oct<TB> y;
+          oct_read(y, at + v * yb, tid, n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss[0] = fmaf(y.get(j), y.get(j), ss[0]);
+        }
+        row_sum<false>(ss, s_sum[sums++ & 1]);
+        scale *= rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+      }
+      TR* orow = static_cast<TR*>(p.residual_out) + row * p.ld_residual_out;
+#pragma unroll
+      for (int v = 0; v < kSteps; ++v) {
+        if (oct_col<true>(v, 0, tid, n) >= p.H) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[v][j] = 0.f;
+          continue;
+        }
+        Oct<TB> y;
+        Oct<TR> r;
+        oct_read(y, at + v * yb, tid, n);
+        oct_read(r, at + kSteps * yb + v * rb, tid, n);
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = scale * w_post[v][j];
+        if (p.gate_kind == MOE_GATE_ELEMENT) apply_gate<true>(g, p, row, v, tid, n, 1.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.residual_scale, r.get(j), g[j] * y.get(j));
+        store_oct<true>(x[v], orow, v, tid, n, p.H);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < kSteps; ++v) {
+        const bool in = oct_col<true>(v, 0, tid, n) < p.H;
+        Oct<TR> r;
+        if (in) oct_read(r, at + kSteps * yb + v * rb, tid, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = in ? r.get(j) : 0.f;
+      }
+    }
+    if (!p.normed) continue;
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] = fmaf(x[v][j], x[v][j], ss[0]);
+    row_sum<false>(ss, s_sum[sums++ & 1]);
+    const float rstd = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+    TB* nrow = static_cast<TB*>(p.normed) + row * p.ld_normed;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] *= rstd * w_pre[v][j];
+      store_oct<true>(x[v], nrow, v, tid, n, p.H);
+    }
+  }
+}
+
+template <typename TB, typename TR, int kSteps>
+__global__ void __launch_bounds__(512, 1)
+block_norm_bwd_stream_kernel(const NormParams p, int depth) {
+  pdl_enter();
+  __shared__ float s_sum[2][3 * 32];
+  extern __shared__ __align__(16) uint8_t s_rows[];
+  const int tid = threadIdx.x, n = blockDim.x;
+  const uint32_t bb = n * 16 * oct_vecs<TB>(), rb = n * 16 * oct_vecs<TR>();  // bytes of a step
+  const uint32_t row_bytes = 2 * kSteps * (bb + rb), ring = smem_u32(s_rows);
+  // a row's parts in shared memory
+  const uint32_t at_y = 0, at_dn = kSteps * bb, at_r = 2 * kSteps * bb, at_dr = at_r + kSteps * rb;
+  const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr,
+             pre = p.d_normed != nullptr, later = p.d_residual_out != nullptr;
+  const bool token = p.gate_kind == MOE_GATE_TOKEN, element = p.gate_kind == MOE_GATE_ELEMENT;
+  auto fetch = [&](long row, int slot) {
+    if (row < p.T) {
+      const uint32_t at = ring + slot * row_bytes;
+      const TB* y = static_cast<const TB*>(p.branch) + row * p.ld_branch;
+      const TB* dn = static_cast<const TB*>(p.d_normed) + row * p.ld_normed;
+      const TR* r = static_cast<const TR*>(p.residual) + row * p.ld_residual_out;
+      const TR* dr = static_cast<const TR*>(p.d_residual_out) + row * p.ld_residual_out;
+#pragma unroll
+      for (int v = 0; v < kSteps; ++v) {
+        const int c = oct_col<true>(v, 0, tid, n);
+        if (c >= p.H) continue;
+        if (pre) {
+          oct_copy(at + at_r + v * rb, r + c, tid, n);
+          oct_copy(at + at_dn + v * bb, dn + c, tid, n);
+        }
+        if (has_branch) oct_copy(at + at_y + v * bb, y + c, tid, n);
+        if (later) oct_copy(at + at_dr + v * rb, dr + c, tid, n);
+      }
+    }
+    copy_async_commit();
+  };
+  const long stride = gridDim.x;
+  for (int i = 0; i < depth - 1; ++i) fetch(blockIdx.x + i * stride, i);
+  // w_pre', and branch_scale * gate (channel) * w_post'
+  float w_pre[kSteps][8], w_post[kSteps][8];
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+    load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
+    load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
+  }
+  float acc_pre[kSteps][8] = {}, acc_post[kSteps][8] = {};
+  int slot = 0, sums = 0;  // the row sums' two buffers alternate
+  for (long row = blockIdx.x; row < p.T; row += stride) {
+    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    copy_async_wait(depth - 1);
+    const uint32_t at = ring + slot * row_bytes;
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    float s3[3] = {0.f, 0.f, 0.f};  // sum r'^2, sum a r', sum y^2
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+      if (pre) {
+        Oct<TR> r;
+        Oct<TB> dn;
+        oct_read(r, at + at_r + v * rb, tid, n);
+        oct_read(dn, at + at_dn + v * bb, tid, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = r.get(j);
+          s3[0] = fmaf(x, x, s3[0]);
+          s3[1] = fmaf(dn.get(j) * w_pre[v][j], x, s3[1]);
+        }
+      }
+      if (post) {
+        Oct<TB> y;
+        oct_read(y, at + at_y + v * bb, tid, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s3[2] = fmaf(y.get(j), y.get(j), s3[2]);
+      }
+    }
+    row_sum<false>(s3, s_sum[sums++ & 1]);
+    const float rstd = pre ? rsqrtf(fmaf(s3[0], p.inv_h, p.eps)) : 0.f;
+    const float mean_au = rstd * s3[1] * p.inv_h;
+    const float ystd = post ? rsqrtf(fmaf(s3[2], p.inv_h, p.eps)) : 1.f;
+    const float tg = token ? p.gate.at(row) : 1.f;
+    float g[kSteps][8];  // the gradient of residual_out; then c, without the token gate
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+      Oct<TR> r, dr;
+      Oct<TB> dn;
+      if (pre) {
+        oct_read(r, at + at_r + v * rb, tid, n);
+        oct_read(dn, at + at_dn + v * bb, tid, n);
+      }
+      if (later) oct_read(dr, at + at_dr + v * rb, tid, n);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x = later ? dr.get(j) : 0.f;
+        if (pre) {
+          const float u = r.get(j) * rstd, d = dn.get(j);
+          acc_pre[v][j] = fmaf(d, u, acc_pre[v][j]);
+          x = fmaf(rstd, fmaf(-u, mean_au, d * w_pre[v][j]), x);
+        }
+        g[v][j] = x;
+        o[j] = has_branch ? p.residual_scale * x : x;
+      }
+      store_oct<true>(o, static_cast<TR*>(p.d_residual) + row * p.ld_residual, v, tid, n, p.H);
+      if (!has_branch) continue;
+      Oct<TB> y;
+      oct_read(y, at + at_y + v * bb, tid, n);
+      float gate[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gate[j] = tg;
+      if (element) {
+        load_weight8<true>(gate, p.gate, row * p.H, v, tid, n, p.H);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = g[v][j] * (y.get(j) * ystd) * w_post[v][j];
+        if (p.w_post.f32)
+          store_oct<true>(o, static_cast<float*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+        else
+          store_oct<true>(o, static_cast<Bf16*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float vj = y.get(j) * ystd;
+        acc_post[v][j] = fmaf(gate[j] * g[v][j], vj, acc_post[v][j]);
+        g[v][j] *= element ? gate[j] * w_post[v][j] : w_post[v][j];
+        s1[0] = fmaf(g[v][j], vj, s1[0]);
+      }
+    }
+    if (!has_branch) continue;
+    float mean_cv = 0.f;
+    if (post || token) {
+      row_sum<false>(s1, s_sum[sums++ & 1]);
+      if (post) mean_cv = s1[0] * p.inv_h;
+      if (token && tid == 0) {
+        if (p.w_post.f32) static_cast<float*>(p.d_gate)[row] = s1[0];
+        else from_float(static_cast<Bf16*>(p.d_gate)[row], s1[0]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+      Oct<TB> y;
+      oct_read(y, at + at_y + v * bb, tid, n);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        o[j] = tg * ystd * fmaf(-(y.get(j) * ystd), mean_cv, g[v][j]);
+      store_oct<true>(o, static_cast<TB*>(p.d_branch) + row * p.ld_branch, v, tid, n, p.H);
+    }
+  }
+  copy_async_wait(0);
+  if (!p.part) return;
+  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.H;
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+    const int c = oct_col<true>(v, 0, tid, n);
+    if (c >= p.H) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      part[c + j] = acc_pre[v][j];
+      part[p.H + c + j] = p.branch_scale * acc_post[v][j];
+    }
+  }
+}
+
 // Sum of the blocks' column sums: 32 columns x 8 runs of blocks per CTA.
 __global__ void __launch_bounds__(256)
 block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, WeightPtr w_post,
@@ -357,23 +654,41 @@ block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, Weight
 // columns (32 per lane: the row sums then need no barrier), the backward up to
 // 256 (its column sums would not fit the registers of more); wider rows take
 // a block of one step (8 columns) a thread up to 512 threads, else two steps.
+//
+// The streamed form takes rows of 16-byte accesses that a block would take,
+// up to 8192 columns, two steps a thread, where every SM has several rows to
+// work on and the ring holds at least two rows.  512 threads an SM in either
+// form: the backward's registers allow no more.
 struct Shape {
-  bool warp;
-  int steps, threads;
+  bool warp, stream;
+  int steps, threads, per_sm, depth;
 };
-Shape norm_shape(int H, bool bwd) {
-  if (H <= 256) return {true, 1, 256};
-  if (!bwd && H <= 1024) return {true, H <= 512 ? 2 : 4, 256};
+constexpr int kStreamRows = 4;            // rows per SM from which rows are streamed
+constexpr int kStreamBytes = 200 * 1024;  // shared memory of an SM for the rings
+
+Shape norm_shape(const moe_norm_problem* p, bool bwd, bool wide) {
+  const int H = p->H;
+  if (H <= 256) return {true, false, 1, 256, 2, 0};
+  const bool warp = !bwd && H <= 1024;
+  if (wide && !warp && H <= 512 * 16 && p->T >= kStreamRows * num_sms()) {
+    Shape s{false, true, 2, ceil_div(ceil_div(H, 16), 32) * 32, 0, 0};
+    s.per_sm = std::max(1, 512 / s.threads);
+    const int elt_bytes = (p->branch_dtype == MOE_DTYPE_F32 ? 4 : 2) +
+                          (p->residual_dtype == MOE_DTYPE_F32 ? 4 : 2);
+    const int row = s.threads * 16 * elt_bytes * (bwd ? 2 : 1);
+    s.depth = std::min(kMaxDepth, kStreamBytes / s.per_sm / row);
+    if (s.depth >= 2) return s;
+  }
+  if (warp) return {true, false, H <= 512 ? 2 : 4, 256, 0, 0};
   const int steps = H <= 512 * 8 ? 1 : 2;
-  return {false, steps, ceil_div(ceil_div(H, 8 * steps), 32) * 32};
+  const int threads = ceil_div(ceil_div(H, 8 * steps), 32) * 32;
+  return {false, false, steps, threads, std::max(1, 512 / threads), 0};
 }
 
 // Blocks of the backward: what the SMs hold at once, and no more than one for
 // a row (eight rows for the warp form).
-int norm_bwd_blocks(int T, int H) {
-  const Shape s = norm_shape(H, true);
-  const int per_sm = std::max(1, std::min(1024 / s.threads, 4));
-  return std::max(1, std::min(num_sms() * per_sm, s.warp ? ceil_div(T, 8) : T));
+int norm_blocks(int T, const Shape& s) {
+  return std::max(1, std::min(num_sms() * s.per_sm, s.warp ? ceil_div(T, 8) : T));
 }
 
 int elt(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
@@ -393,7 +708,10 @@ int check_norm(const moe_norm_problem* p) {
 }
 
 size_t norm_part_bytes(const moe_norm_problem* p) {
-  return sizeof(float) * 2 * static_cast<size_t>(p->H) * norm_bwd_blocks(p->T, p->H);
+  // whichever form the tensors' alignment calls for
+  return sizeof(float) * 2 * static_cast<size_t>(p->H) *
+         std::max(norm_blocks(p->T, norm_shape(p, true, true)),
+                  norm_blocks(p->T, norm_shape(p, true, false)));
 }
 
 constexpr size_t kNormHeader = 256;  // status word
@@ -436,10 +754,23 @@ cudaError_t launch_norm_impl(const NormParams& k, int threads, int blocks, cudaS
                          dim3(blocks), dim3(threads), 0, s, 1, k);
 }
 
+template <bool kBwd, typename TB, typename TR>
+cudaError_t launch_norm_stream(const NormParams& k, const Shape& sh, cudaStream_t s) {
+  auto kern = kBwd ? block_norm_bwd_stream_kernel<TB, TR, 2> : block_norm_fwd_stream_kernel<TB, TR, 2>;
+  const size_t smem = static_cast<size_t>(sh.depth) * sh.threads * 16 * (sizeof(TB) + sizeof(TR)) *
+                      (kBwd ? 2 : 1);
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kStreamBytes);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kern, dim3(norm_blocks(k.T, sh)), dim3(sh.threads), smem, s, 1, k, sh.depth);
+}
+
 template <bool kBwd, typename TB, typename TR, bool kWide>
-cudaError_t launch_norm_shape(const NormParams& k, int blocks, cudaStream_t s) {
-  const Shape sh = norm_shape(k.H, kBwd);
+cudaError_t launch_norm_shape(const NormParams& k, const Shape& sh, cudaStream_t s) {
   const int n = sh.threads;
+  const int blocks = kBwd ? norm_blocks(k.T, sh) : sh.warp ? ceil_div(k.T, 8) : k.T;
+  if constexpr (kWide)
+    if (sh.stream) return launch_norm_stream<kBwd, TB, TR>(k, sh, s);
   if (sh.warp) {
     if (sh.steps == 1) return launch_norm_impl<kBwd, TB, TR, 1, 256, true, kWide>(k, n, blocks, s);
     if constexpr (!kBwd)
@@ -452,16 +783,16 @@ cudaError_t launch_norm_shape(const NormParams& k, int blocks, cudaStream_t s) {
 }
 
 template <bool kBwd>
-cudaError_t launch_norm(const moe_norm_problem* p, const NormParams& k, bool wide, int blocks,
+cudaError_t launch_norm(const moe_norm_problem* p, const NormParams& k, bool wide, const Shape& sh,
                         cudaStream_t s) {
   const bool bf = p->branch_dtype == MOE_DTYPE_BF16, rf = p->residual_dtype == MOE_DTYPE_BF16;
   auto go = [&](auto w) {
     constexpr bool kWide = decltype(w)::value;
     if (bf)
-      return rf ? launch_norm_shape<kBwd, Bf16, Bf16, kWide>(k, blocks, s)
-                : launch_norm_shape<kBwd, Bf16, float, kWide>(k, blocks, s);
-    return rf ? launch_norm_shape<kBwd, float, Bf16, kWide>(k, blocks, s)
-              : launch_norm_shape<kBwd, float, float, kWide>(k, blocks, s);
+      return rf ? launch_norm_shape<kBwd, Bf16, Bf16, kWide>(k, sh, s)
+                : launch_norm_shape<kBwd, Bf16, float, kWide>(k, sh, s);
+    return rf ? launch_norm_shape<kBwd, float, Bf16, kWide>(k, sh, s)
+              : launch_norm_shape<kBwd, float, float, kWide>(k, sh, s);
   };
   return wide ? go(std::true_type{}) : go(std::false_type{});
 }
@@ -505,7 +836,7 @@ extern "C" int moe_block_norm_forward(const moe_norm_problem* p, const void* bra
   k.gate = {gate, wf};
   k.residual_out = residual_out;
   k.normed = normed;
-  if (launch_norm<false>(p, k, c.wide, norm_shape(p->H, false).warp ? ceil_div(p->T, 8) : p->T,
+  if (launch_norm<false>(p, k, c.wide, norm_shape(p, false, c.wide),
                          static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
   set_last_launch_count(1);
@@ -582,8 +913,9 @@ extern "C" int moe_block_norm_backward(const moe_norm_problem* p, const void* br
   k.d_gate = d_gate;
   const bool cols = pre || w_post || channel;
   k.part = cols ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kNormHeader) : nullptr;
-  const int blocks = norm_bwd_blocks(p->T, p->H);
-  if (launch_norm<true>(p, k, c.wide, blocks, s) != cudaSuccess) return MOE_ERR_CUDA;
+  const Shape sh = norm_shape(p, true, c.wide);
+  const int blocks = norm_blocks(p->T, sh);
+  if (launch_norm<true>(p, k, c.wide, sh, s) != cudaSuccess) return MOE_ERR_CUDA;
   ++launches;
   if (cols) {
     if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32)), dim3(256), 0, s, 1,

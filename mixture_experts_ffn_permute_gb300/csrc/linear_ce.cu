@@ -13,20 +13,36 @@
 // L2:
 //   G  = a exp(z - lse) - b [v = label]  the forward's GEMM with another
 //                                        epilogue, [T, piece] to the workspace
-//   dx += G W_piece    A = G K-major, B = W_piece read MN-major (as stored)
-//   dW_piece = G^T x   A = G, B = x, both read MN-major (as stored)
-// with a = scale (d_loss + d_lse), b = scale d_loss.  The two products are
-// tiles of one launch.  dx is kept in fp32 in the workspace from piece to
+//   dx += S G W_piece    A = G K-major, B = W_piece read MN-major (as stored)
+//   dW_piece = S G^T x   A = G, B = x, both read MN-major (as stored)
+// with a = (d_loss + d_lse) / s, b = d_loss / s, S = scale s and s the largest
+// finite |d_loss|.  G is rounded to bf16: under a mean, where every token has
+// the same d_loss, its largest entries, the labels', are then -(1 - p) and not
+// all rounded by the same amount (which would scale both gradients by up to
+// 1 + 2^-8).  S multiplies the fp32 results.  The two products are tiles of
+// one launch.  dx is kept in fp32 in the workspace from piece to
 // piece (each element is one thread's in every piece, so the order of its sum
 // is fixed) and rounded once by the last; with one piece it is written
 // directly.
 //
-// Warp roles (192 threads, one CTA per SM, tiles round-robin over the pairs):
-//   warp 0     TMA producer: 6 stages of 16 KB of A and up to 16 KB of B per CTA
+// Operands move in stages of 128 along K.  Where a matrix's row length is a
+// multiple of 64 one bulk-tensor copy brings a stage of an operand as two
+// 64-column planes, every row one 256-byte segment; otherwise two copies of
+// 128-byte rows do (they zero-fill past the row's end, which planes cannot).
+//
+// The tensor core's fp32 accumulator loses a little at every step, always
+// toward zero, which does not average out over a row of logits: at K = 4096 lse
+// was 1e-6 of its value too small.  The forward therefore takes the
+// accumulator out every 1024 of K and adds the parts in registers (128
+// columns a thread, eight epilogue warps), while the tensor core fills the
+// other accumulator.
+//
+// Warp roles (one CTA per SM, tiles dealt to the pairs in a fixed order):
+//   warp 0     TMA producer: 3 stages of 32 KB of A and up to 32 KB of B per CTA
 //   warp 1     TMEM allocation, MMA issue (the leader CTA's)
-//   warps 2-5  epilogue, thread = token (or vocabulary) row of the tile; two
-//              accumulators of 256 columns, so it overlaps the next mainloop;
-//              bf16 tiles leave through swizzled staging and bulk-tensor stores
+//   warps 2..  epilogue, thread = row of the tile; two accumulators of 256
+//              columns, so it overlaps the next mainloop; bf16 tiles leave
+//              through swizzled staging and bulk-tensor stores
 // Every wait is bounded (ptx.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -46,45 +62,54 @@ namespace {
 
 constexpr int kTileM = 256;  // rows of a pair tile, 128 per CTA
 constexpr int kTileN = 256;  // columns at most
-constexpr int kTileK = 64;
-constexpr int kStagesCe = 6;
-constexpr uint32_t kABytesCe = 128 * kTileK * 2;     // 16 KB
-constexpr uint32_t kBBytesCe = kTileN / 2 * kTileK * 2;
+constexpr int kTileK = 128;  // one stage
+constexpr int kStagesCe = 3;
+constexpr uint32_t kPlane = 128 * 64 * 2;            // 128 rows x 64 columns, 16 KB
+constexpr uint32_t kABytesCe = 2 * kPlane;
+constexpr uint32_t kBBytesCe = 2 * kPlane;
 constexpr uint32_t kStageCe = kABytesCe + kBBytesCe;
-constexpr uint32_t kBoxCe = 64 * 64 * 2;             // MN-major box: 64 columns x 64 rows
+constexpr int kPromote = 8;  // forward: stages per accumulation in TMEM (K = 1024)
 constexpr uint32_t kStagingBox = 32 * 128;           // 32 rows x 64 bf16
 constexpr int kStagingBuffers = 2;
 constexpr uint32_t kStagingCe = 4 * kStagingBuffers * kStagingBox;
 constexpr size_t kSmemCe = 1024 + kStagesCe * kStageCe + kStagingCe + 256;
 static_assert(kSmemCe <= 232448, "shared memory budget");
 constexpr int kGroupM = 8;  // m-tiles whose sweep over the n-tiles shares B tiles in L2
-constexpr int kThreadsCe = 192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // One GEMM: C[M, N] = A B^T over K, by pair tiles.
 struct Gemm {
-  int m_tiles, n_tiles, ksteps;
+  int m_tiles, n_tiles, ksteps;  // ksteps: stages of 128
   int n_step;                 // columns per tile (a multiple of 32, <= 256)
   int M, N;                   // extents (rows and columns beyond are not written)
   bool a_mn, b_mn;            // operand stored [K, M] (resp. [K, N]): read MN-major
+  bool a_planes, b_planes;    // one copy per stage (row length a multiple of 64)
+  int a_rows;                 // K-major A: rows per CTA that are loaded (128, fewer for small M)
   bool add, keep;             // fp32 accumulation over launches: add acc, keep it in acc
   __host__ __device__ int tiles() const { return m_tiles * n_tiles; }
 };
 
 enum class CeMode : int { kLse = 0, kGrad = 1, kProducts = 2 };
+// Epilogue warps: one per TMEM lane quadrant, two in the forward (each half
+// of the columns)
+template <CeMode kMode>
+__host__ __device__ constexpr int epi_warps() { return kMode == CeMode::kLse ? 8 : 4; }
+template <CeMode kMode>
+__host__ __device__ constexpr int threads_ce() { return 64 + 32 * epi_warps<kMode>(); }
 
 struct CeParams {
   Gemm g[2];            // kProducts: dx then dW; otherwise g[0]
   const int32_t* labels;
   int v0, V;            // first vocabulary row of the piece; vocabulary
   float scale;
-  float2* part;         // kLse: [n_tiles][T] (max, sum) in log2 units
+  float2* part;         // kLse: [2 n_tiles][T] (max, sum) of a tile's halves in log2 units
   float* label_logit;   // kLse: [T]
   const float* lse;     // kGrad
   const float* d_loss;
   const float* d_lse;   // or NULL
   float* acc;           // kProducts: dx in fp32 [T, N]
+  const float* unit;    // kGrad, kProducts: s, the unit of G
   uint32_t* status;
 };
 
@@ -98,12 +123,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Descriptor of an MN-major operand: boxes of 64 columns x 64 K rows with the
-// 128-byte swizzle; leading offset = the next 64 columns (one box), stride
+// Descriptor of an MN-major operand: planes of 64 columns x 128 K rows with the
+// 128-byte swizzle; leading offset = the next 64 columns (one plane), stride
 // offset = 8 K rows.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
   return sw128_kmajor_desc(smem_addr) ^ (static_cast<uint64_t>(1u) << 16) ^
-         (static_cast<uint64_t>(kBoxCe >> 4) << 16);
+         (static_cast<uint64_t>(kPlane >> 4) << 16);
 }
 
 __device__ __forceinline__ void fence_async_shared() {
@@ -119,11 +144,44 @@ __device__ __forceinline__ void tile_of(const Gemm& g, int i, int& m, int& n) {
   m = grp * kGroupM + (within - n * size);
 }
 
+// The tiles of one CTA pair of `pairs`, in order: g[0]'s round-robin, then
+// g[1]'s so that the pairs whose share of g[0] was one tile shorter take their
+// first `lead` tiles of g[1] while the others finish, the rest round-robin.
+struct Deal {
+  int pair, pairs, mine0, rem, tiles0, tiles1, lead;
+  __device__ __forceinline__ Deal(const CeParams& p, int pair_, int pairs_) {
+    pair = pair_;
+    pairs = pairs_;
+    tiles0 = p.g[0].tiles();
+    tiles1 = p.g[1].tiles();
+    rem = tiles0 % pairs;
+    mine0 = tiles0 / pairs + (pair < rem ? 1 : 0);
+    lead = rem ? (p.g[0].ksteps + p.g[1].ksteps / 2) / max(1, p.g[1].ksteps) : 0;
+  }
+  // tile number `i` of this pair: false past the last; `second`: of g[1]
+  __device__ __forceinline__ bool at(int i, int& tile, bool& second) const {
+    second = i >= mine0;
+    if (!second) {
+      tile = i * pairs + pair;
+      return true;
+    }
+    int j = i - mine0;
+    if (pair >= rem) {
+      if (j < lead) {
+        tile = j * (pairs - rem) + (pair - rem);
+        return tile < tiles1;
+      }
+      j -= lead;
+    }
+    tile = lead * (pairs - rem) + j * pairs + pair;
+    return tile < tiles1;
+  }
+};
+
 template <CeMode kMode>
-__global__ void __launch_bounds__(kThreadsCe, 1)
+__global__ void __launch_bounds__(threads_ce<kMode>(), 1)
 linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMaps m1,
                  const __grid_constant__ CeParams p) {
-  pdl_enter();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = smem;
@@ -147,7 +205,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * 128);
+      mbar_init(&tempty[b], 2 * 32 * epi_warps<kMode>());
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -164,10 +222,11 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int tiles0 = p.g[0].tiles();
-  const int total = tiles0 + (kMode == CeMode::kProducts ? p.g[1].tiles() : 0);
-  const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
-  auto second = [&](int tile) { return kMode == CeMode::kProducts && tile >= tiles0; };
+  // nothing above touches global memory
+  pdl_enter();
+  const Deal deal(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
+  int tile, m, n;
+  bool two;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -176,38 +235,49 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
       int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
-      for (int tile = first; tile < total; tile += stride) {
+      for (int i = 0; deal.at(i, tile, two); ++i) {
         if (*abort_flag) break;
-        const bool two = second(tile);
         const Gemm& g = p.g[two];
         const CeMaps& maps = two ? m1 : m0;
-        int m, n;
-        tile_of(g, two ? tile - tiles0 : tile, m, n);
+        tile_of(g, tile, m, n);
         const int row0 = m * kTileM + static_cast<int>(rank) * 128;
         const int half = g.n_step / 2;
         const int col0 = n * g.n_step + static_cast<int>(rank) * half;
-        const uint32_t bytes = 2 * (kABytesCe + static_cast<uint32_t>(half) * kTileK * 2);
+        const bool a_mn = g.a_mn, b_mn = g.b_mn, a_planes = g.a_planes, b_planes = g.b_planes;
+        const uint32_t a_plane = static_cast<uint32_t>(g.a_rows) * 128, b_plane = half * 128;
+        // one CTA's rows may hold the whole of a small M
+        const bool a_load = rank == 0 || g.M > 128;
+        const uint32_t bytes = (g.M > 128 ? 4 : 2) * a_plane + 4 * b_plane;
+        const int ksteps = g.ksteps;
+        // with one m-tile every pair reads the same A: each starts elsewhere in
+        // K, so that they do not all ask for the same lines at once
+        int kb = g.m_tiles == 1 ? deal.pair % ksteps : 0;
         bool ok = true;
-        for (int kb = 0; kb < g.ksteps; ++kb) {
+        for (int j = 0; j < ksteps; ++j) {
           if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = pair::mapa(smem_u32(&full[stage]), 0);
           uint8_t* a = sA + stage * kABytesCe;
           uint8_t* b = sB + stage * kBBytesCe;
           const int k0 = kb * kTileK;
-          if (g.a_mn) {
-            pair::tma_load(a, &maps.a, row0, k0, bar, pol);
-            pair::tma_load(a + kBoxCe, &maps.a, row0 + 64, k0, bar, pol);
-          } else {
-            pair::tma_load(a, &maps.a, k0, row0, bar, pol);
+          if (a_load) {
+            const int c = a_mn ? row0 : k0, r = a_mn ? k0 : row0;
+            if (a_planes) {
+              pair::tma_load_3d(a, &maps.a, 0, r, c / 64, bar, pol);
+            } else {
+              pair::tma_load(a, &maps.a, c, r, bar, pol);
+              pair::tma_load(a + a_plane, &maps.a, c + 64, r, bar, pol);
+            }
           }
-          if (g.b_mn) {  // 128 columns: n_step is 256
-            pair::tma_load(b, &maps.b, col0, k0, bar, pol);
-            pair::tma_load(b + kBoxCe, &maps.b, col0 + 64, k0, bar, pol);
+          const int c = b_mn ? col0 : k0, r = b_mn ? k0 : col0;
+          if (b_planes) {
+            pair::tma_load_3d(b, &maps.b, 0, r, c / 64, bar, pol);
           } else {
-            pair::tma_load(b, &maps.b, k0, col0, bar, pol);
+            pair::tma_load(b, &maps.b, c, r, bar, pol);
+            pair::tma_load(b + b_plane, &maps.b, c + 64, r, bar, pol);
           }
           ++issued;
+          if (++kb == ksteps) kb = 0;
           if (++stage == kStagesCe) { stage = 0; phase ^= 1; }
         }
         if (!ok) { *abort_flag = 1; break; }
@@ -227,40 +297,46 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     if (leader && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int local = 0;
-      for (int tile = first; tile < total; tile += stride, ++local) {
+      int seg = 0;  // accumulations so far: they alternate between the two accumulators
+      bool ok = true;
+      for (int i = 0; ok && deal.at(i, tile, two); ++i) {
         if (*abort_flag) break;
-        const bool two = second(tile);
         const Gemm& g = p.g[two];
         const bool a_mn = g.a_mn, b_mn = g.b_mn;
         const int ksteps = g.ksteps;
         const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(g.n_step)) |
                                (static_cast<uint32_t>(a_mn) << 15) |
                                (static_cast<uint32_t>(b_mn) << 16);
-        const int buf = local & 1;
-        const uint32_t tph = (local >> 1) & 1;
-        if (!mbar_wait(&tempty[buf], tph ^ 1, p.status)) { *abort_flag = 1; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * kTileN;
-        bool ok = true;
-        for (int kb = 0; kb < ksteps; ++kb) {
-          if (!mbar_wait(&full[stage], phase, p.status)) { ok = false; break; }
+        // a K=16 step is 32 bytes along a K-major plane, which holds four (the
+        // next plane four more), and 16 rows of 128 bytes of MN-major planes,
+        // which hold eight; in units of 16 bytes
+        const uint32_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;
+        const uint32_t a4 = a_mn ? 512 : static_cast<uint32_t>(g.a_rows) * 8;
+        const uint32_t b4 = b_mn ? 512 : static_cast<uint32_t>(g.n_step) * 4;
+        const int per_seg = kMode == CeMode::kLse ? kPromote : ksteps;
+        for (int k0 = 0; ok && k0 < ksteps; k0 += per_seg, ++seg) {
+          const int buf = seg & 1;
+          if (!mbar_wait(&tempty[buf], ((seg >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + stage * kABytesCe);
-          const uint32_t b = smem_u32(sB + stage * kBBytesCe);
-          // a K=16 step is 32 bytes along a K-major row, 16 rows of 128 bytes
-          // of an MN-major box
-          const uint64_t ad = a_mn ? mn_desc(a) : sw128_kmajor_desc(a);
-          const uint64_t bd = b_mn ? mn_desc(b) : sw128_kmajor_desc(b);
-          const uint32_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;  // in 16 bytes
+          const uint32_t d_tmem = tmem_base + buf * kTileN;
+          const int k1 = min(ksteps, k0 + per_seg);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(&full[stage], phase, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a = smem_u32(sA + stage * kABytesCe);
+            const uint32_t b = smem_u32(sB + stage * kBBytesCe);
+            const uint64_t ad = a_mn ? mn_desc(a) : sw128_kmajor_desc(a);
+            const uint64_t bd = b_mn ? mn_desc(b) : sw128_kmajor_desc(b);
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk)
-            pair::mma(d_tmem, ad + kk * as, bd + kk * bs, idesc, (kb | kk) != 0);
-          pair::commit_both(&empty[stage]);
-          if (++stage == kStagesCe) { stage = 0; phase ^= 1; }
+            for (int kk = 0; kk < kTileK / 16; ++kk)
+              pair::mma(d_tmem, ad + (kk & 3) * as + (kk >> 2) * a4,
+                        bd + (kk & 3) * bs + (kk >> 2) * b4, idesc, kb > k0 || kk != 0);
+            pair::commit_both(&empty[stage]);
+            if (++stage == kStagesCe) { stage = 0; phase ^= 1; }
+          }
+          if (ok) pair::commit_both(&tfull[buf]);
         }
-        if (!ok) { *abort_flag = 1; break; }
-        pair::commit_both(&tfull[buf]);
+        if (!ok) *abort_flag = 1;
       }
       pair::commit_local(drain);  // every MMA done before TMEM is released
       mbar_wait(drain, 0, p.status);
@@ -271,82 +347,107 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     const int quad = warp & 3;  // the TMEM lanes this warp may access
     uint8_t* staging = s_out + (warp - 2) * kStagingBuffers * kStagingBox;
     const int rsw = lane & 7;
-    int local = 0, n_stores = 0;
-    for (int tile = first; tile < total; tile += stride, ++local) {
+    const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tempty_leader = pair::mapa(smem_u32(tempty), 0);
+    int seg = 0, n_stores = 0;
+    bool go = true;
+    // the next accumulation is complete
+    auto wait_full = [&]() {
+      go = __all_sync(0xffffffffu, mbar_wait(&tfull[seg & 1], (seg >> 1) & 1, p.status));
+      if (!go && lane == 0) *abort_flag = 1;
+      tc_fence_after();
+      return go;
+    };
+    // it has been read (the leader's barrier of this accumulator)
+    auto release = [&]() {
+      tc_fence_before();
+      pair::arrive_remote(tempty_leader + (seg & 1) * 8);
+      ++seg;
+    };
+    for (int i = 0; go && deal.at(i, tile, two); ++i) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const bool two = second(tile);
       const Gemm& g = p.g[two];
-      int m, n;
-      tile_of(g, two ? tile - tiles0 : tile, m, n);
-      const int buf = local & 1;
-      const uint32_t tph = (local >> 1) & 1;
+      tile_of(g, tile, m, n);
       const int wrow0 = m * kTileM + static_cast<int>(rank) * 128 + quad * 32;
       const int row = wrow0 + lane;
-      const bool row_ok = row < g.M;
+      const bool row_ok = row < g.M, warp_ok = wrow0 < g.M;
       const int col0 = n * g.n_step;
       const int ncols = min(g.n_step, g.N - col0);
       int label = -1;
       float lse2 = 0.f, ga = 0.f, gb = 0.f;
       if (kMode != CeMode::kProducts && row_ok) {
-        label = __ldg(p.labels + row);
-        if (label >= p.V) label = -1;
-        label = label >= 0 ? label - p.v0 - col0 : -1;  // column of this tile, if it is one
-      }
-      if (kMode == CeMode::kGrad && row_ok) {
         const int id = __ldg(p.labels + row);
-        const float dl = id >= 0 && id < p.V ? __ldg(p.d_loss + row) : 0.f;
-        ga = p.scale * (dl + (p.d_lse ? __ldg(p.d_lse + row) : 0.f));
-        gb = p.scale * dl;
-        lse2 = __ldg(p.lse + row) * kLog2e;
+        const bool valid = id >= 0 && id < p.V;
+        if (valid) label = id - p.v0 - col0;  // column of this tile, if it is one
+        if (kMode == CeMode::kGrad) {
+          const float inv = 1.f / __ldg(p.unit);
+          const float dl = valid ? __ldg(p.d_loss + row) : 0.f;
+          ga = inv * (dl + (p.d_lse ? __ldg(p.d_lse + row) : 0.f));
+          gb = inv * dl;
+          lse2 = __ldg(p.lse + row) * kLog2e;
+        }
       }
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[buf], tph, p.status));
-      if (!ok) {
-        if (lane == 0) *abort_flag = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t t_lane =
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileN;
       const float c2 = p.scale * kLog2e;
 
       if (kMode == CeMode::kLse) {
+        // this warp's half of the columns, up to 128 of a row per thread
+        const int half = (warp - 2) >> 2, c0 = half * 128;
+        float z[4][32];
+        for (int k0 = 0; k0 < g.ksteps; k0 += kPromote) {
+          if (!wait_full()) break;
+          const uint32_t t_lane = t_quad + (seg & 1) * kTileN + c0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (warp_ok && c0 + 32 * q < ncols) {
+              uint32_t a[32];
+              __syncwarp();
+              tmem_ld_32x32b_x32(t_lane + 32 * q, a);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                z[q][j] = k0 ? z[q][j] + __uint_as_float(a[j]) : __uint_as_float(a[j]);
+            }
+          }
+          release();
+        }
+        if (!go) break;
         float mx = -INFINITY, sum = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < ncols; c += 32) {
-          __syncwarp();
-          uint32_t a[32];
-          tmem_ld_32x32b_x32(t_lane + c, a);
-          tmem_ld_wait();
-          const int left = ncols - c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = c0 + 32 * q, left = ncols - c;
+          if (!warp_ok || left <= 0) continue;
           if (label >= c && label < c + 32) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i == label) p.label_logit[row] = p.scale * __uint_as_float(a[i]);
+            for (int j = 0; j < 32; ++j)
+              if (c + j == label) p.label_logit[row] = p.scale * z[q][j];
           }
-          float z[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            z[i] = i < left ? c2 * __uint_as_float(a[i]) : -INFINITY;
           float cm = mx;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) cm = fmaxf(cm, z[i]);
-          if (cm != -INFINITY) {  // all -inf so far: the sum stays 0
+          for (int j = 0; j < 32; ++j) {
+            z[q][j] = j < left ? c2 * z[q][j] : -INFINITY;
+            cm = fmaxf(cm, z[q][j]);
+          }
+          // ordinary rows: one rescaling a chunk; all -inf so far: the sum stays 0
+          if (cm != -INFINITY) {
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s += ex2(z[i] - cm);
+            for (int j = 0; j < 32; ++j) s += ex2(z[q][j] - cm);
             sum = fmaf(sum, ex2(mx - cm), s);
             mx = cm;
           }
         }
-        if (row_ok) p.part[static_cast<long>(n) * g.M + row] = make_float2(mx, sum);
+        if (row_ok) p.part[static_cast<long>(2 * n + half) * g.M + row] = make_float2(mx, sum);
       } else {
+        if (!wait_full()) break;
+        const uint32_t t_lane = t_quad + (seg & 1) * kTileN;
         const bool f32_only = kMode == CeMode::kProducts && g.keep;
         float* acc = nullptr;
         if (kMode == CeMode::kProducts && (g.add || g.keep))
           acc = p.acc + static_cast<long>(row) * g.N + col0;
+        const CUtensorMap* out = two ? &m1.out : &m0.out;
+        const float S = kMode == CeMode::kProducts ? p.scale * __ldg(p.unit) : 1.f;
 #pragma unroll 1
-        for (int c = 0; c < kTileN; c += 64) {
-          if (c >= ncols) break;
+        for (int c = 0; c < (warp_ok ? ncols : 0); c += 64) {
           uint8_t* box = staging + (n_stores % kStagingBuffers) * kStagingBox;
           if (!f32_only) {
             if (lane == 0) bulk_wait_group_read<kStagingBuffers - 1>();
@@ -361,28 +462,34 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             tmem_ld_wait();
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+            for (int i2 = 0; i2 < 32; ++i2) v[i2] = __uint_as_float(a[i2]);
             if (kMode == CeMode::kGrad) {
+              // columns past the vocabulary, up to the store's 64: zeros, which
+              // the products read along K
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                v[i] = ga * ex2(fmaf(v[i], c2, -lse2));
-                if (cc + i == label) v[i] -= gb;
+              for (int i2 = 0; i2 < 32; ++i2) {
+                const float e = ga * ex2(fmaf(v[i2], c2, -lse2));
+                v[i2] = cc + i2 < ncols ? (cc + i2 == label ? e - gb : e) : 0.f;
               }
             } else if (acc && row_ok) {
-              // the width is a multiple of 8: whole float4 pairs
+              // the width is a multiple of 8: whole float4s
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                if (cc + i < ncols) {
-                  float4* q = reinterpret_cast<float4*>(acc + cc + i);
+              for (int i2 = 0; i2 < 32; i2 += 4) {
+                if (cc + i2 < ncols) {
+                  float4* q = reinterpret_cast<float4*>(acc + cc + i2);
                   if (g.add) {
                     const float4 o = *q;
-                    v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
+                    v[i2] += o.x, v[i2 + 1] += o.y, v[i2 + 2] += o.z, v[i2 + 3] += o.w;
                   }
-                  if (g.keep) *q = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                  if (g.keep) *q = make_float4(v[i2], v[i2 + 1], v[i2 + 2], v[i2 + 3]);
                 }
               }
             }
             if (!f32_only) {
+              if (kMode == CeMode::kProducts) {
+#pragma unroll
+                for (int i2 = 0; i2 < 32; ++i2) v[i2] *= S;
+              }
               uint8_t* srow = box + lane * 128;
 #pragma unroll
               for (int q = 0; q < 4; ++q)
@@ -394,19 +501,15 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           if (!f32_only) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) {
-              // rows and columns beyond the matrix are clipped by the map; a
-              // box with no row inside is not stored at all
-              if (wrow0 < g.M)
-                tma_store_2d(two ? &m1.out : &m0.out, box, col0 + c, wrow0);
+            if (lane == 0) {  // rows and columns past the matrix are clipped by the map
+              tma_store_2d(out, box, col0 + c, wrow0);
               bulk_commit_group();
             }
             ++n_stores;
           }
         }
+        release();
       }
-      tc_fence_before();
-      pair::arrive_remote(pair::mapa(smem_u32(&tempty[buf]), 0));  // the leader's
     }
     if (kMode != CeMode::kLse && lane == 0) bulk_wait_group<0>();
     __syncwarp();
@@ -421,6 +524,31 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     tc_fence_after();
     pair::tmem_dealloc2<512>(tmem_base);
   }
+}
+
+// s: the largest finite |d_loss| of a token that is not masked (1 if it is 0
+// or so small that its reciprocal is not a number).
+__global__ void __launch_bounds__(1024)
+ce_unit_kernel(const float* __restrict__ d_loss, const int32_t* __restrict__ labels, int T, int V,
+               float* __restrict__ unit) {
+  pdl_enter();
+  __shared__ float s[32];
+  float m = 0.f;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    const float x = fabsf(d_loss[t]);
+    const int id = labels[t];
+    if (x <= 3e38f && id >= 0 && id < V) m = fmaxf(m, x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  m = s[threadIdx.x];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (threadIdx.x == 0) *unit = m >= 0x1p-100f ? m : 1.f;
 }
 
 // lse and loss of every token from its tiles' (max, sum), in tile order: 32
@@ -478,8 +606,23 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// bf16 [rows, cols] with rows ld elements apart; boxes of 64 columns x
-// box_rows rows with the 128-byte swizzle.
+// bf16 [rows, cols] with rows ld elements apart, as planes of 64 columns; boxes
+// of two planes x box_rows rows with the 128-byte swizzle (cols a multiple
+// of 64).
+bool make_planes(CUtensorMap* map, const void* base, long rows, long cols, long ld, int box_rows) {
+  const EncodeFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(cols / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same matrix in boxes of 64 columns x box_rows rows.
 bool make_map(CUtensorMap* map, const void* base, long rows, long cols, long ld, int box_rows) {
   const EncodeFn enc = encode_fn();
   if (!enc) return false;
@@ -505,17 +648,35 @@ int tile_columns(int m_tiles, int N, int unit) {
   return n;
 }
 
-Gemm make_gemm(long M, long N, long K, int n_step, bool a_mn, bool b_mn) {
-  Gemm g{};
-  g.M = static_cast<int>(M);
-  g.N = static_cast<int>(N);
-  g.m_tiles = ceil_div(M, kTileM);
-  g.n_tiles = ceil_div(N, n_step);
-  g.ksteps = ceil_div(K, kTileK);
-  g.n_step = n_step;
-  g.a_mn = a_mn;
-  g.b_mn = b_mn;
-  return g;
+// A row-major bf16 matrix in global memory.
+struct Matrix {
+  const void* p;
+  long rows, cols, ld;
+};
+
+// C[M, N] = A B^T over K from the operands as stored ([M, K] and [N, K], or
+// [K, M] and [K, N] read MN-major) and their maps; false if a map could not be
+// made.
+bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const Matrix& a,
+               bool a_mn, const Matrix& b, bool b_mn) {
+  *g = Gemm{};
+  g->M = static_cast<int>(M);
+  g->N = static_cast<int>(N);
+  g->m_tiles = ceil_div(M, kTileM);
+  g->n_tiles = ceil_div(N, n_step);
+  g->ksteps = ceil_div(K, kTileK);
+  g->n_step = n_step;
+  g->a_mn = a_mn;
+  g->b_mn = b_mn;
+  g->a_planes = a.cols % 64 == 0;
+  g->b_planes = b.cols % 64 == 0;
+  g->a_rows = a_mn || M > 128 ? 128 : ceil_div(M, 8) * 8;
+  auto make = [](CUtensorMap* m, const Matrix& x, bool planes, int rows) {
+    return planes ? make_planes(m, x.p, x.rows, x.cols, x.ld, rows)
+                  : make_map(m, x.p, x.rows, x.cols, x.ld, rows);
+  };
+  return make(&maps->a, a, g->a_planes, g->a_rows) &&
+         make(&maps->b, b, g->b_planes, b_mn ? kTileK : n_step / 2);
 }
 
 template <CeMode kMode>
@@ -524,16 +685,20 @@ cudaError_t launch_ce(const CeMaps& m0, const CeMaps& m1, const CeParams& p, cud
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemCe));
   if (err != cudaSuccess) return err;
-  const long tiles = static_cast<long>(p.g[0].tiles()) +
-                     (kMode == CeMode::kProducts ? p.g[1].tiles() : 0);
+  const long tiles = static_cast<long>(p.g[0].tiles()) + p.g[1].tiles();
   const int pairs = static_cast<int>(std::max(1L, std::min<long>(num_sms() / 2, tiles)));
-  return launch_kernel(kern, dim3(2 * pairs), dim3(kThreadsCe), kSmemCe, s, 2, m0, m1, p);
+  return launch_kernel(kern, dim3(2 * pairs), dim3(threads_ce<kMode>()), kSmemCe, s, 2, m0, m1, p);
 }
 
 constexpr size_t kCeHeader = 256;
-// Bytes of a piece's logit gradients: about half of L2, so that both products
-// read them there.
-constexpr size_t kPieceBytes = 64u << 20;
+constexpr size_t kUnitOffset = 64;  // of s in the header
+// A piece's logit gradients: 128 MB, and 4096 vocabulary rows at least.  Larger
+// pieces mean fewer passes over dx's fp32 sums and fuller last waves, smaller
+// ones less workspace and more of the piece in L2.  The backward at
+// T=4096 H=4096 V=32000 with 16, 32, 64, 128, 256 MB and one piece: 3.02,
+// 2.17, 1.87, 1.77, 1.75, 1.74 ms; T=8192: 8.16, 5.49, 4.42, 3.96, 3.79, 3.76 ms.
+constexpr size_t kPieceBytes = 128u << 20;
+constexpr int kPieceRows = 4096;
 
 int check_ce(const moe_ce_problem* p) {
   if (!p || p->T < 0 || p->H < 1 || p->V < 1 || !std::isfinite(p->logit_scale))
@@ -554,13 +719,13 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 size_t ce_forward_bytes(const moe_ce_problem* p) {
   const int n = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
   const size_t T = static_cast<size_t>(p->T);
-  return kCeHeader + up(sizeof(float2) * T * ceil_div(p->V, n)) + up(sizeof(float) * T);
+  return kCeHeader + up(sizeof(float2) * T * 2 * ceil_div(p->V, n)) + up(sizeof(float) * T);
 }
 
 // Vocabulary rows per piece (a multiple of the tile), pieces of equal size.
 int piece_rows(const moe_ce_problem* p) {
   const long most = std::max<long>(
-      kTileM, static_cast<long>(kPieceBytes / 2 / std::max(1, p->T)) / kTileM * kTileM);
+      kPieceRows, static_cast<long>(kPieceBytes / 2 / std::max(1, p->T)) / kTileM * kTileM);
   const int pieces = ceil_div(p->V, most);
   return ceil_div(ceil_div(p->V, pieces), kTileM) * kTileM;
 }
@@ -609,22 +774,22 @@ extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, con
   const int n_step = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
   uint8_t* base = static_cast<uint8_t*>(ws) + kCeHeader;
   CeParams k{};
-  k.g[0] = make_gemm(p->T, p->V, p->H, n_step, false, false);
+  CeMaps m{};
+  if (!make_gemm(&k.g[0], &m, p->T, p->V, p->H, n_step, {x, p->T, p->H, p->H}, false,
+                 {w, p->V, p->H, p->H}, false))
+    return MOE_ERR_CUDA;
   k.labels = labels;
   k.V = p->V;
   k.scale = p->logit_scale;
   k.part = reinterpret_cast<float2*>(base);
   k.label_logit = reinterpret_cast<float*>(
-      base + up(sizeof(float2) * static_cast<size_t>(p->T) * k.g[0].n_tiles));
+      base + up(sizeof(float2) * static_cast<size_t>(p->T) * 2 * k.g[0].n_tiles));
   k.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CeMaps m{};
-  if (!make_map(&m.a, x, p->T, p->H, p->H, 128) || !make_map(&m.b, w, p->V, p->H, p->H, n_step / 2))
-    return MOE_ERR_CUDA;
   if (launch_ce<CeMode::kLse>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
   if (launch_kernel(ce_join_kernel, dim3(ceil_div(p->T, 32)), dim3(256), 0, s, 1,
                     static_cast<const float2*>(k.part), static_cast<const float*>(k.label_logit),
-                    labels, p->T, p->V, k.g[0].n_tiles, loss, lse, k.status) != cudaSuccess)
+                    labels, p->T, p->V, 2 * k.g[0].n_tiles, loss, lse, k.status) != cudaSuccess)
     return MOE_ERR_CUDA;
   set_last_launch_count(2);
   return MOE_OK;
@@ -665,26 +830,34 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
   k.d_lse = d_lse;
   k.acc = reinterpret_cast<float*>(base + up(2 * static_cast<size_t>(p->T) * rows));
   k.status = static_cast<uint32_t*>(ws);
+  float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kUnitOffset);
+  k.unit = unit;
+  if (launch_kernel(ce_unit_kernel, dim3(1), dim3(1024), 0, s, 1, d_loss, labels, p->T, p->V,
+                    unit) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++launches;
   for (int i = 0; i < pieces; ++i) {
     const int v0 = i * rows, nv = std::min(rows, p->V - v0);
     const uint8_t* wp = static_cast<const uint8_t*>(w) + 2 * static_cast<size_t>(v0) * p->H;
     uint8_t* dwp = static_cast<uint8_t*>(dw) + 2 * static_cast<size_t>(v0) * p->H;
     k.v0 = v0;
     const int n_step = tile_columns(ceil_div(p->T, kTileM), nv, kUnitGrad);
-    k.g[0] = make_gemm(p->T, nv, p->H, n_step, false, false);
+    const Matrix xm{x, p->T, p->H, p->H}, wm{wp, nv, p->H, p->H};
+    // padded to whole planes: the epilogue writes zeros there
+    const Matrix gm{grad, p->T, ceil_div(nv, 64) * 64L, rows};
     CeMaps m{}, m1{};
-    if (!make_map(&m.a, x, p->T, p->H, p->H, 128) || !make_map(&m.b, wp, nv, p->H, p->H, n_step / 2) ||
-        !make_map(&m.out, grad, p->T, nv, rows, 32))
+    k.g[1] = Gemm{};
+    if (!make_gemm(&k.g[0], &m, p->T, nv, p->H, n_step, xm, false, wm, false) ||
+        !make_map(&m.out, grad, p->T, gm.cols, rows, 32))
       return MOE_ERR_CUDA;
     if (launch_ce<CeMode::kGrad>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
-    k.g[0] = make_gemm(p->T, p->H, nv, kTileN, false, true);
+    if (!make_gemm(&k.g[0], &m, p->T, p->H, nv, kTileN, gm, false, wm, true) ||
+        !make_map(&m.out, dx, p->T, p->H, p->H, 32) ||
+        !make_gemm(&k.g[1], &m1, nv, p->H, p->T, kTileN, gm, true, xm, true) ||
+        !make_map(&m1.out, dwp, nv, p->H, p->H, 32))
+      return MOE_ERR_CUDA;
     k.g[0].add = i > 0;
     k.g[0].keep = i + 1 < pieces;
-    k.g[1] = make_gemm(nv, p->H, p->T, kTileN, true, true);
-    if (!make_map(&m.a, grad, p->T, nv, rows, 128) || !make_map(&m.b, wp, nv, p->H, p->H, 64) ||
-        !make_map(&m.out, dx, p->T, p->H, p->H, 32) || !make_map(&m1.a, grad, p->T, nv, rows, 64) ||
-        !make_map(&m1.b, x, p->T, p->H, p->H, 64) || !make_map(&m1.out, dwp, nv, p->H, p->H, 32))
-      return MOE_ERR_CUDA;
     if (launch_ce<CeMode::kProducts>(m, m1, k, s) != cudaSuccess) return MOE_ERR_CUDA;
     launches += 2;
   }

@@ -148,6 +148,50 @@ __device__ __forceinline__ void store_oct(const float (&x)[8], T* row, int v, in
   }
 }
 
+// Copies of a thread's own octets to shared memory and back, for rows read some
+// rows ahead: no other thread touches them, so no barrier is needed.  A step of
+// n threads takes n * 16 bytes (bf16) or two runs of that (fp32).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most `pending` (0 .. 3) of this thread's groups are under way.
+__device__ __forceinline__ void copy_async_wait(int pending) {
+  if (pending >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+template <typename T>
+__host__ __device__ constexpr int oct_vecs() { return static_cast<int>(sizeof(T)) / 2; }  // 16-byte vectors
+template <typename T>
+__device__ __forceinline__ void oct_copy(uint32_t step, const T* src, int tid, int n) {
+#pragma unroll
+  for (int h = 0; h < oct_vecs<T>(); ++h) copy_async16(step + (h * n + tid) * 16, src + 4 * h);
+}
+__device__ __forceinline__ void oct_read(Oct<Bf16>& o, uint32_t step, int tid, int) {
+  const uint4 v = load_shared16(step + tid * 16);
+  o.w[0] = v.x, o.w[1] = v.y, o.w[2] = v.z, o.w[3] = v.w;
+}
+__device__ __forceinline__ void oct_read(Oct<float>& o, uint32_t step, int tid, int n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 v = load_shared16(step + (h * n + tid) * 16);
+    o.f[4 * h] = __uint_as_float(v.x), o.f[4 * h + 1] = __uint_as_float(v.y);
+    o.f[4 * h + 2] = __uint_as_float(v.z), o.f[4 * h + 3] = __uint_as_float(v.w);
+  }
+}
+
 // A weight vector whose type is known at run time only (bf16 or fp32).
 struct WeightPtr {
   const void* p;

@@ -205,6 +205,23 @@ def test_row_counts(T):
     check(T, 1288, F32, BF, BF, "channel")
 
 
+# enough rows that they are streamed through shared memory, in every depth of the ring
+@pytest.mark.parametrize("H", [264, 1032, 2048, 4096, 7168, 8192])
+@pytest.mark.parametrize("tb,tr", list(itertools.product((BF, F32), repeat=2)))
+def test_streamed_rows(tb, tr, H):
+    for kind, T in (("channel", 611), ("element", 1000)):
+        check(T, H, tb, tr, F32, kind, off=0.5, seed=T)
+    check(700, H, tb, tr, BF, "token", ld=H + 8)
+
+
+@pytest.mark.parametrize("kind", ["none", "token", "element"])
+@pytest.mark.parametrize("post,pre,later", [(False, True, True), (True, False, True),
+                                            (True, True, False), (False, False, True)])
+def test_streamed_rows_with_parts_left_out(kind, post, pre, later):
+    check(1300, 1288, BF, F32, F32, kind, post=post, pre=pre, later=later)
+    check(1300, 1288, BF, BF, F32, kind, post=post, pre=pre, later=later)
+
+
 @pytest.mark.parametrize("kind", ["none", "channel", "token", "element"])
 @pytest.mark.parametrize("post,pre,later", [(False, True, True), (True, False, True),
                                             (True, True, False), (False, False, True),
@@ -221,9 +238,10 @@ def test_row_strides(H, ld):
 
 
 @pytest.mark.parametrize("H", [64, 333, 2048])
-def test_norm_alone(H):
-    s = inputs(11, H, BF, F32, F32, "none")
-    p = problem(11, H, BF, F32, F32, "none", 0.0, 0.3, 0.4)
+@pytest.mark.parametrize("T", [11, 900])
+def test_norm_alone(T, H):
+    s = inputs(T, H, BF, F32, F32, "none")
+    p = problem(T, H, BF, F32, F32, "none", 0.0, 0.3, 0.4)
     d = {k: dev(v) for k, v in s.items()}
     n = like(s["branch"])[0]
     moe.block_norm_forward(p, d["residual"], w_pre=d["w_pre"], normed=n)
@@ -236,7 +254,7 @@ def test_norm_alone(H):
                             d_residual_out=d["d_residual_out"], d_w_pre=dw)
     ref = ref_backward(s, "none", 0.0, 1.0, 0.4)  # the scales do not apply
     close(dr, *ref["residual"], F32)
-    close(dw, *ref["w_pre"], F32, sums=11)
+    close(dw, *ref["w_pre"], F32, sums=T)
 
 
 def test_in_place():
