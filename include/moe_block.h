@@ -18,8 +18,9 @@
  *     at or above the vocabulary is treated as masked and recorded as
  *     MOE_ERR_DEVICE_INDEX in the workspace's status word.
  *   - pointers need their element's alignment only, unless the entry point
- *     says otherwise; 16-byte aligned rows (base, width and row stride) take
- *     the wide-load kernels.
+ *     says otherwise; rows of a width that is a multiple of 8 whose base and
+ *     row stride are multiples of 16 bytes (bf16) or 32 (fp32) take the
+ *     kernels of wide accesses.
  *   - results are bitwise reproducible on one device (no floating-point
  *     atomics): sums over tokens are split by a rule on the sizes and the
  *     number of SMs and joined in a fixed order.

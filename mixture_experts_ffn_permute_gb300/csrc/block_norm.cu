@@ -317,151 +317,193 @@ block_norm_bwd_kernel(const NormParams p) {
 }
 
 // ------------------------------------------------------------------ streamed rows
-// The same rows and sums for many rows of 16-byte accesses: a block stays on its
+// The same rows and sums for many rows of wide accesses: a block stays on its
 // SM, keeps its columns' weights in registers and copies the rows to come into
-// shared memory (cp.async, every thread its own octets) while it works on the
+// shared memory (cp.async, every warp its own octets) while it works on the
 // present one, so that the two row sums' barriers do not leave HBM idle.  The
-// phases read their octets from shared memory again rather than hold them.
+// phases read their octets from shared memory again rather than hold them,
+// and compute in packed pairs of fp32: the backward is otherwise bound by the
+// issue of instructions (70 a element of a first version took it to 63 us at
+// T=4096 H=4096 bf16).
 constexpr int kMaxDepth = 4;  // rows in shared memory, the present one among them
 
-// weight + offset, times `scale` and (channel gate) the gate, of this thread's
-// columns; zero past the row
-__device__ __forceinline__ void load_weights(float (&w)[8], const NormParams& p,
+// scale * (weight + offset), times the gate's channel where that is its kind,
+// of this thread's columns
+__device__ __forceinline__ void load_weights(Pair (&w)[4], const NormParams& p,
                                              const WeightPtr& ptr, bool gated, float scale, int v,
                                              int tid, int n) {
+  float x[8];
   if (ptr.p) {
-    load_weight8<true>(w, ptr, 0, v, tid, n, p.H);
+    load_weight8<true>(x, ptr, 0, v, tid, n, p.H);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = scale * (w[j] + p.offset);
+    for (int j = 0; j < 8; ++j) x[j] = scale * (x[j] + p.offset);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = scale;
+    for (int j = 0; j < 8; ++j) x[j] = scale;
   }
   if (gated && p.gate_kind == MOE_GATE_CHANNEL) {
     float g[8];
     load_weight8<true>(g, p.gate, 0, v, tid, n, p.H);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] *= g[j];
+    for (int j = 0; j < 8; ++j) x[j] *= g[j];
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pair_of(x[2 * i], x[2 * i + 1]);
 }
 
-template <typename TB, typename TR, int kSteps>
-__global__ void __launch_bounds__(512, 1)
+__device__ __forceinline__ void load_gate(Pair (&w)[4], const NormParams& p, long row, int v,
+                                          int tid, int n) {
+  float x[8];
+  load_weight8<true>(x, p.gate, row * p.H, v, tid, n, p.H);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pair_of(x[2 * i], x[2 * i + 1]);
+}
+
+// kPlain: branch, w_post and w_pre given, no gate or a channel gate; the
+// general form decides by the row.
+template <typename TB, typename TR, int kSteps, bool kPlain>
+__global__ void __launch_bounds__(1024 / kSteps, 1)
 block_norm_fwd_stream_kernel(const NormParams p, int depth) {
   pdl_enter();
   __shared__ float s_sum[2][32];
   extern __shared__ __align__(16) uint8_t s_rows[];
   const int tid = threadIdx.x, n = blockDim.x;
-  const uint32_t yb = n * 16 * oct_vecs<TB>(), rb = n * 16 * oct_vecs<TR>();  // bytes of a step
+  const uint32_t yb = n * oct_align<TB>(), rb = n * oct_align<TR>();  // bytes of a step
   const uint32_t row_bytes = kSteps * (yb + rb), ring = smem_u32(s_rows);
-  const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr;
+  const bool has_branch = kPlain || p.branch != nullptr;
+  const bool post = kPlain || p.w_post.p != nullptr, pre = kPlain || p.normed != nullptr;
+  const bool token = !kPlain && p.gate_kind == MOE_GATE_TOKEN;
+  const bool element = !kPlain && p.gate_kind == MOE_GATE_ELEMENT;
+  bool in[kSteps];
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) in[v] = oct_col<true>(v, 0, tid, n) < p.H;
   auto fetch = [&](long row, int slot) {
     if (row < p.T) {
       const uint32_t at = ring + slot * row_bytes;
 #pragma unroll
       for (int v = 0; v < kSteps; ++v) {
         const int c = oct_col<true>(v, 0, tid, n);
-        if (c >= p.H) continue;
         if (has_branch)
-          oct_copy(at + v * yb, static_cast<const TB*>(p.branch) + row * p.ld_branch + c, tid, n);
+          oct_copy(at + v * yb, static_cast<const TB*>(p.branch) + row * p.ld_branch, c, tid, p.H);
         oct_copy(at + kSteps * yb + v * rb,
-                 static_cast<const TR*>(p.residual) + row * p.ld_residual + c, tid, n);
+                 static_cast<const TR*>(p.residual) + row * p.ld_residual, c, tid, p.H);
       }
     }
     copy_async_commit();
   };
   const long stride = gridDim.x;
   for (int i = 0; i < depth - 1; ++i) fetch(blockIdx.x + i * stride, i);
-  float w_post[kSteps][8], w_pre[kSteps][8];
+  Pair w_post[kSteps][4], w_pre[kSteps][4];
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
     load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
     load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
   }
+  const Pair rscale = pair_of(p.residual_scale, p.residual_scale);
   int slot = 0, sums = 0;  // the row sums' two buffers alternate
   for (long row = blockIdx.x; row < p.T; row += stride) {
+    __syncwarp();  // the slot that is filled now has been read by the whole warp
     fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
     copy_async_wait(depth - 1);
+    __syncwarp();
     const uint32_t at = ring + slot * row_bytes;
     slot = slot + 1 == depth ? 0 : slot + 1;
-    float x[kSteps][8];  // residual_out, unrounded
+    Pair x[kSteps][4];  // residual_out, unrounded
     if (has_branch) {
-      float scale = p.gate_kind == MOE_GATE_TOKEN ? p.gate.at(row) : 1.f;
+      float scale = token ? p.gate.at(row) : 1.f;
       if (post) {
-        float ss[1] = {0.f};
+        Pair acc = 0;
 #pragma unroll
         for (int v = 0; v < kSteps; ++v) {
-          if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+          if (!in[v]) continue;
           Oct<TB> y;
-          oct_read(y, at + v * yb, tid, n);
+          oct_read(y, at + v * yb, tid);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss[0] = fmaf(y.get(j), y.get(j), ss[0]);
+          for (int i = 0; i < 4; ++i) acc = pair_fma(y.pair(i), y.pair(i), acc);
         }
+        float ss[1] = {pair_sum(acc)};
         row_sum<false>(ss, s_sum[sums++ & 1]);
         scale *= rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
       }
+      const Pair sc = pair_of(scale, scale);
       TR* orow = static_cast<TR*>(p.residual_out) + row * p.ld_residual_out;
 #pragma unroll
       for (int v = 0; v < kSteps; ++v) {
-        if (oct_col<true>(v, 0, tid, n) >= p.H) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[v][j] = 0.f;
-          continue;
-        }
+        if (!in[v]) continue;
         Oct<TB> y;
-        Oct<TR> r;
-        oct_read(y, at + v * yb, tid, n);
-        oct_read(r, at + kSteps * yb + v * rb, tid, n);
-        float g[8];
+        Oct<TR> r, o;
+        oct_read(y, at + v * yb, tid);
+        oct_read(r, at + kSteps * yb + v * rb, tid);
+        Pair w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = scale * w_post[v][j];
-        if (p.gate_kind == MOE_GATE_ELEMENT) apply_gate<true>(g, p, row, v, tid, n, 1.f);
+        for (int i = 0; i < 4; ++i) w[i] = pair_mul(sc, w_post[v][i]);
+        if (element) {
+          Pair g[4];
+          load_gate(g, p, row, v, tid, n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.residual_scale, r.get(j), g[j] * y.get(j));
-        store_oct<true>(x[v], orow, v, tid, n, p.H);
+          for (int i = 0; i < 4; ++i) w[i] = pair_mul(w[i], g[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[v][i] = pair_fma(rscale, r.pair(i), pair_mul(w[i], y.pair(i)));
+          o.set_pair(i, x[v][i]);
+        }
+        o.store(orow + oct_col<true>(v, 0, tid, n));
       }
     } else {
 #pragma unroll
       for (int v = 0; v < kSteps; ++v) {
-        const bool in = oct_col<true>(v, 0, tid, n) < p.H;
+        if (!in[v]) continue;
         Oct<TR> r;
-        if (in) oct_read(r, at + kSteps * yb + v * rb, tid, n);
+        oct_read(r, at + kSteps * yb + v * rb, tid);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] = in ? r.get(j) : 0.f;
+        for (int i = 0; i < 4; ++i) x[v][i] = r.pair(i);
       }
     }
-    if (!p.normed) continue;
-    float ss[1] = {0.f};
+    if (!pre) continue;
+    Pair acc = 0;
 #pragma unroll
-    for (int v = 0; v < kSteps; ++v)
+    for (int v = 0; v < kSteps; ++v) {
+      if (!in[v]) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(x[v][j], x[v][j], ss[0]);
+      for (int i = 0; i < 4; ++i) acc = pair_fma(x[v][i], x[v][i], acc);
+    }
+    float ss[1] = {pair_sum(acc)};
     row_sum<false>(ss, s_sum[sums++ & 1]);
     const float rstd = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+    const Pair rs = pair_of(rstd, rstd);
     TB* nrow = static_cast<TB*>(p.normed) + row * p.ld_normed;
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
+      if (!in[v]) continue;
+      Oct<TB> o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[v][j] *= rstd * w_pre[v][j];
-      store_oct<true>(x[v], nrow, v, tid, n, p.H);
+      for (int i = 0; i < 4; ++i) o.set_pair(i, pair_mul(x[v][i], pair_mul(rs, w_pre[v][i])));
+      o.store(nrow + oct_col<true>(v, 0, tid, n));
     }
   }
+  copy_async_wait(0);
 }
 
-template <typename TB, typename TR, int kSteps>
-__global__ void __launch_bounds__(512, 1)
+// kPlain: every input given, no gate or a channel gate.
+template <typename TB, typename TR, int kSteps, bool kPlain>
+__global__ void __launch_bounds__(1024 / kSteps, 1)
 block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   pdl_enter();
   __shared__ float s_sum[2][3 * 32];
   extern __shared__ __align__(16) uint8_t s_rows[];
   const int tid = threadIdx.x, n = blockDim.x;
-  const uint32_t bb = n * 16 * oct_vecs<TB>(), rb = n * 16 * oct_vecs<TR>();  // bytes of a step
+  const uint32_t bb = n * oct_align<TB>(), rb = n * oct_align<TR>();  // bytes of a step
   const uint32_t row_bytes = 2 * kSteps * (bb + rb), ring = smem_u32(s_rows);
   // a row's parts in shared memory
   const uint32_t at_y = 0, at_dn = kSteps * bb, at_r = 2 * kSteps * bb, at_dr = at_r + kSteps * rb;
-  const bool has_branch = p.branch != nullptr, post = p.w_post.p != nullptr,
-             pre = p.d_normed != nullptr, later = p.d_residual_out != nullptr;
-  const bool token = p.gate_kind == MOE_GATE_TOKEN, element = p.gate_kind == MOE_GATE_ELEMENT;
+  const bool has_branch = kPlain || p.branch != nullptr, post = kPlain || p.w_post.p != nullptr;
+  const bool pre = kPlain || p.d_normed != nullptr, later = kPlain || p.d_residual_out != nullptr;
+  const bool token = !kPlain && p.gate_kind == MOE_GATE_TOKEN;
+  const bool element = !kPlain && p.gate_kind == MOE_GATE_ELEMENT;
+  bool in[kSteps];
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) in[v] = oct_col<true>(v, 0, tid, n) < p.H;
   auto fetch = [&](long row, int slot) {
     if (row < p.T) {
       const uint32_t at = ring + slot * row_bytes;
@@ -472,13 +514,12 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
 #pragma unroll
       for (int v = 0; v < kSteps; ++v) {
         const int c = oct_col<true>(v, 0, tid, n);
-        if (c >= p.H) continue;
         if (pre) {
-          oct_copy(at + at_r + v * rb, r + c, tid, n);
-          oct_copy(at + at_dn + v * bb, dn + c, tid, n);
+          oct_copy(at + at_r + v * rb, r, c, tid, p.H);
+          oct_copy(at + at_dn + v * bb, dn, c, tid, p.H);
         }
-        if (has_branch) oct_copy(at + at_y + v * bb, y + c, tid, n);
-        if (later) oct_copy(at + at_dr + v * rb, dr + c, tid, n);
+        if (has_branch) oct_copy(at + at_y + v * bb, y, c, tid, p.H);
+        if (later) oct_copy(at + at_dr + v * rb, dr, c, tid, p.H);
       }
     }
     copy_async_commit();
@@ -486,98 +527,120 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   const long stride = gridDim.x;
   for (int i = 0; i < depth - 1; ++i) fetch(blockIdx.x + i * stride, i);
   // w_pre', and branch_scale * gate (channel) * w_post'
-  float w_pre[kSteps][8], w_post[kSteps][8];
+  Pair w_pre[kSteps][4], w_post[kSteps][4];
+  Pair acc_pre[kSteps][4], acc_post[kSteps][4];
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
     load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
     load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc_pre[v][i] = acc_post[v][i] = 0;
   }
-  float acc_pre[kSteps][8] = {}, acc_post[kSteps][8] = {};
+  const float res_scale = has_branch ? p.residual_scale : 1.f;
+  const Pair rscale = pair_of(res_scale, res_scale);
   int slot = 0, sums = 0;  // the row sums' two buffers alternate
   for (long row = blockIdx.x; row < p.T; row += stride) {
+    __syncwarp();  // the slot that is filled now has been read by the whole warp
     fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
     copy_async_wait(depth - 1);
+    __syncwarp();
     const uint32_t at = ring + slot * row_bytes;
     slot = slot + 1 == depth ? 0 : slot + 1;
-    float s3[3] = {0.f, 0.f, 0.f};  // sum r'^2, sum a r', sum y^2
+    Pair a0 = 0, a1 = 0, a2 = 0;  // sum r'^2, sum a r', sum y^2
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
-      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
+      if (!in[v]) continue;
       if (pre) {
         Oct<TR> r;
         Oct<TB> dn;
-        oct_read(r, at + at_r + v * rb, tid, n);
-        oct_read(dn, at + at_dn + v * bb, tid, n);
+        oct_read(r, at + at_r + v * rb, tid);
+        oct_read(dn, at + at_dn + v * bb, tid);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = r.get(j);
-          s3[0] = fmaf(x, x, s3[0]);
-          s3[1] = fmaf(dn.get(j) * w_pre[v][j], x, s3[1]);
+        for (int i = 0; i < 4; ++i) {
+          a0 = pair_fma(r.pair(i), r.pair(i), a0);
+          a1 = pair_fma(pair_mul(dn.pair(i), w_pre[v][i]), r.pair(i), a1);
         }
       }
       if (post) {
         Oct<TB> y;
-        oct_read(y, at + at_y + v * bb, tid, n);
+        oct_read(y, at + at_y + v * bb, tid);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s3[2] = fmaf(y.get(j), y.get(j), s3[2]);
+        for (int i = 0; i < 4; ++i) a2 = pair_fma(y.pair(i), y.pair(i), a2);
       }
     }
+    float s3[3] = {pair_sum(a0), pair_sum(a1), pair_sum(a2)};
     row_sum<false>(s3, s_sum[sums++ & 1]);
     const float rstd = pre ? rsqrtf(fmaf(s3[0], p.inv_h, p.eps)) : 0.f;
-    const float mean_au = rstd * s3[1] * p.inv_h;
     const float ystd = post ? rsqrtf(fmaf(s3[2], p.inv_h, p.eps)) : 1.f;
+    // g = dr + rstd a - rstd u mean(a u), u = rstd r': the last factor of r'
+    const float kr = -rstd * rstd * (rstd * s3[1] * p.inv_h);
+    const Pair rs = pair_of(rstd, rstd), k2 = pair_of(kr, kr), ys = pair_of(ystd, ystd);
     const float tg = token ? p.gate.at(row) : 1.f;
-    float g[kSteps][8];  // the gradient of residual_out; then c, without the token gate
-    float s1[1] = {0.f};
+    Pair g[kSteps][4];  // c = gradient of v, without the token gate
+    Pair sc = 0;
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
-      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
-      Oct<TR> r, dr;
-      Oct<TB> dn;
-      if (pre) {
-        oct_read(r, at + at_r + v * rb, tid, n);
-        oct_read(dn, at + at_dn + v * bb, tid, n);
-      }
-      if (later) oct_read(dr, at + at_dr + v * rb, tid, n);
-      float o[8];
+      if (!in[v]) continue;
+      const int c = oct_col<true>(v, 0, tid, n);
+      Oct<TR> o;
+      if (later) {
+        Oct<TR> dr;
+        oct_read(dr, at + at_dr + v * rb, tid);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float x = later ? dr.get(j) : 0.f;
-        if (pre) {
-          const float u = r.get(j) * rstd, d = dn.get(j);
-          acc_pre[v][j] = fmaf(d, u, acc_pre[v][j]);
-          x = fmaf(rstd, fmaf(-u, mean_au, d * w_pre[v][j]), x);
-        }
-        g[v][j] = x;
-        o[j] = has_branch ? p.residual_scale * x : x;
+        for (int i = 0; i < 4; ++i) g[v][i] = dr.pair(i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[v][i] = 0;
       }
-      store_oct<true>(o, static_cast<TR*>(p.d_residual) + row * p.ld_residual, v, tid, n, p.H);
+      if (pre) {
+        Oct<TR> r;
+        Oct<TB> dn;
+        oct_read(r, at + at_r + v * rb, tid);
+        oct_read(dn, at + at_dn + v * bb, tid);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const Pair d = pair_mul(dn.pair(i), rs);
+          acc_pre[v][i] = pair_fma(d, r.pair(i), acc_pre[v][i]);
+          g[v][i] = pair_fma(r.pair(i), k2, pair_fma(d, w_pre[v][i], g[v][i]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o.set_pair(i, pair_mul(rscale, g[v][i]));
+      o.store(static_cast<TR*>(p.d_residual) + row * p.ld_residual + c);
       if (!has_branch) continue;
       Oct<TB> y;
-      oct_read(y, at + at_y + v * bb, tid, n);
-      float gate[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) gate[j] = tg;
+      oct_read(y, at + at_y + v * bb, tid);
       if (element) {
-        load_weight8<true>(gate, p.gate, row * p.H, v, tid, n, p.H);
+        Pair gate[4];
+        load_gate(gate, p, row, v, tid, n);
+        float d[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = g[v][j] * (y.get(j) * ystd) * w_post[v][j];
+        for (int i = 0; i < 4; ++i) {
+          const Pair gv = pair_mul(g[v][i], pair_mul(y.pair(i), ys));
+          unpair(pair_mul(gv, w_post[v][i]), d[2 * i], d[2 * i + 1]);
+          acc_post[v][i] = pair_fma(gv, gate[i], acc_post[v][i]);
+          g[v][i] = pair_mul(g[v][i], pair_mul(gate[i], w_post[v][i]));
+          sc = pair_fma(g[v][i], pair_mul(y.pair(i), ys), sc);
+        }
         if (p.w_post.f32)
-          store_oct<true>(o, static_cast<float*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+          store_oct<true>(d, static_cast<float*>(p.d_gate) + row * p.H, v, tid, n, p.H);
         else
-          store_oct<true>(o, static_cast<Bf16*>(p.d_gate) + row * p.H, v, tid, n, p.H);
-      }
+          store_oct<true>(d, static_cast<Bf16*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+      } else {
+        const Pair t = pair_of(tg, tg);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float vj = y.get(j) * ystd;
-        acc_post[v][j] = fmaf(gate[j] * g[v][j], vj, acc_post[v][j]);
-        g[v][j] *= element ? gate[j] * w_post[v][j] : w_post[v][j];
-        s1[0] = fmaf(g[v][j], vj, s1[0]);
+        for (int i = 0; i < 4; ++i) {
+          const Pair vv = pair_mul(y.pair(i), ys);
+          acc_post[v][i] = pair_fma(kPlain ? g[v][i] : pair_mul(t, g[v][i]), vv, acc_post[v][i]);
+          g[v][i] = pair_mul(g[v][i], w_post[v][i]);
+          sc = pair_fma(g[v][i], vv, sc);
+        }
       }
     }
     if (!has_branch) continue;
     float mean_cv = 0.f;
     if (post || token) {
+      float s1[1] = {pair_sum(sc)};
       row_sum<false>(s1, s_sum[sums++ & 1]);
       if (post) mean_cv = s1[0] * p.inv_h;
       if (token && tid == 0) {
@@ -585,16 +648,18 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
         else from_float(static_cast<Bf16*>(p.d_gate)[row], s1[0]);
       }
     }
+    // d_branch = gate ystd (c - v mean(c v)), v = ystd y
+    const float f = tg * ystd, ky = -f * ystd * mean_cv;
+    const Pair fc = pair_of(f, f), fy = pair_of(ky, ky);
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
-      if (oct_col<true>(v, 0, tid, n) >= p.H) continue;
-      Oct<TB> y;
-      oct_read(y, at + at_y + v * bb, tid, n);
-      float o[8];
+      if (!in[v]) continue;
+      Oct<TB> y, o;
+      oct_read(y, at + at_y + v * bb, tid);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        o[j] = tg * ystd * fmaf(-(y.get(j) * ystd), mean_cv, g[v][j]);
-      store_oct<true>(o, static_cast<TB*>(p.d_branch) + row * p.ld_branch, v, tid, n, p.H);
+      for (int i = 0; i < 4; ++i)
+        o.set_pair(i, pair_fma(y.pair(i), fy, pair_mul(g[v][i], fc)));
+      o.store(static_cast<TB*>(p.d_branch) + row * p.ld_branch + oct_col<true>(v, 0, tid, n));
     }
   }
   copy_async_wait(0);
@@ -602,29 +667,33 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.H;
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
+    if (!in[v]) continue;
     const int c = oct_col<true>(v, 0, tid, n);
-    if (c >= p.H) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      part[c + j] = acc_pre[v][j];
-      part[p.H + c + j] = p.branch_scale * acc_post[v][j];
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpair(acc_pre[v][i], lo, hi);
+      reinterpret_cast<float2*>(part + c)[i] = make_float2(lo, hi);
+      unpair(acc_post[v][i], lo, hi);
+      reinterpret_cast<float2*>(part + p.H + c)[i] =
+          make_float2(p.branch_scale * lo, p.branch_scale * hi);
     }
   }
 }
 
-// Sum of the blocks' column sums: 32 columns x 8 runs of blocks per CTA.
-__global__ void __launch_bounds__(256)
+// Sum of the blocks' column sums: 32 columns x 32 runs of blocks per CTA.
+__global__ void __launch_bounds__(1024)
 block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, WeightPtr w_post,
                        WeightPtr gate, int channel_gate, float offset, void* d_w_pre,
                        void* d_w_post, void* d_gate) {
   pdl_enter();
-  __shared__ float s[2][8][32];
+  __shared__ float s[2][32][32];
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f, b = 0.f;
   if (c < H) {
 #pragma unroll 4
-    for (int i = q; i < blocks; i += 8) {
+    for (int i = q; i < blocks; i += 32) {
       const float* row = part + static_cast<long>(i) * 2 * H;
       a += row[c];
       b += row[H + c];
@@ -636,7 +705,7 @@ block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, Weight
   if (q || c >= H) return;
   a = b = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 32; ++i) {
     a += s[0][i][lane];
     b += s[1][i][lane];
   }
@@ -671,11 +740,12 @@ Shape norm_shape(const moe_norm_problem* p, bool bwd, bool wide) {
   if (H <= 256) return {true, false, 1, 256, 2, 0};
   const bool warp = !bwd && H <= 1024;
   if (wide && !warp && H <= 512 * 16 && p->T >= kStreamRows * num_sms()) {
-    Shape s{false, true, 2, ceil_div(ceil_div(H, 16), 32) * 32, 0, 0};
-    s.per_sm = std::max(1, 512 / s.threads);
+    Shape s{false, true, bwd ? 2 : 1, 0, 0, 0};
+    s.threads = ceil_div(ceil_div(H, 8 * s.steps), 32) * 32;
+    s.per_sm = std::max(1, 1024 / s.steps / s.threads);
     const int elt_bytes = (p->branch_dtype == MOE_DTYPE_F32 ? 4 : 2) +
                           (p->residual_dtype == MOE_DTYPE_F32 ? 4 : 2);
-    const int row = s.threads * 16 * elt_bytes * (bwd ? 2 : 1);
+    const int row = s.threads * 8 * s.steps * elt_bytes * (bwd ? 2 : 1);
     s.depth = std::min(kMaxDepth, kStreamBytes / s.per_sm / row);
     if (s.depth >= 2) return s;
   }
@@ -716,13 +786,14 @@ size_t norm_part_bytes(const moe_norm_problem* p) {
 
 constexpr size_t kNormHeader = 256;  // status word
 
-// Collects the pointer checks and whether every row takes 16-byte accesses.
+// Collects the pointer checks and whether every row takes wide accesses.
 struct RowCheck {
   bool ok = true, wide = true;
   void add(const void* p, int dtype, long ld) {
     if (!p) return;
     if (!aligned(p, elt(dtype))) ok = false;
-    if (!aligned(p, 16) || (ld * elt(dtype)) % 16 != 0) wide = false;
+    const int n = 8 * elt(dtype);  // eight elements in one access
+    if (!aligned(p, n) || (ld * elt(dtype)) % n != 0) wide = false;
   }
 };
 
@@ -756,9 +827,17 @@ cudaError_t launch_norm_impl(const NormParams& k, int threads, int blocks, cudaS
 
 template <bool kBwd, typename TB, typename TR>
 cudaError_t launch_norm_stream(const NormParams& k, const Shape& sh, cudaStream_t s) {
-  auto kern = kBwd ? block_norm_bwd_stream_kernel<TB, TR, 2> : block_norm_fwd_stream_kernel<TB, TR, 2>;
-  const size_t smem = static_cast<size_t>(sh.depth) * sh.threads * 16 * (sizeof(TB) + sizeof(TR)) *
-                      (kBwd ? 2 : 1);
+  const bool plain = k.branch && k.w_post.p && k.w_pre.p && (!kBwd || k.d_residual_out) &&
+                     (k.gate_kind == MOE_GATE_NONE || k.gate_kind == MOE_GATE_CHANNEL);
+  void (*kern)(NormParams, int);
+  if constexpr (kBwd)
+    kern = plain ? block_norm_bwd_stream_kernel<TB, TR, 2, true>
+                 : block_norm_bwd_stream_kernel<TB, TR, 2, false>;
+  else
+    kern = plain ? block_norm_fwd_stream_kernel<TB, TR, 1, true>
+                 : block_norm_fwd_stream_kernel<TB, TR, 1, false>;
+  const size_t smem = static_cast<size_t>(sh.depth) * sh.threads * 8 * sh.steps *
+                      (sizeof(TB) + sizeof(TR)) * (kBwd ? 2 : 1);
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kStreamBytes);
   if (err != cudaSuccess) return err;
@@ -918,7 +997,7 @@ extern "C" int moe_block_norm_backward(const moe_norm_problem* p, const void* br
   if (launch_norm<true>(p, k, c.wide, sh, s) != cudaSuccess) return MOE_ERR_CUDA;
   ++launches;
   if (cols) {
-    if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32)), dim3(256), 0, s, 1,
+    if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32)), dim3(1024), 0, s, 1,
                       static_cast<const float*>(k.part), blocks, p->H, k.w_post, k.gate,
                       channel ? 1 : 0, p->weight_offset, d_w_pre, d_w_post, d_gate) != cudaSuccess)
       return MOE_ERR_CUDA;

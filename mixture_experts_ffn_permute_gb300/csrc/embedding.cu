@@ -328,7 +328,8 @@ extern "C" int moe_embedding_forward(const moe_embed_problem* p, const int32_t* 
   if (!aligned(ids, 4) || !aligned(table, elt(p->table_dtype)) ||
       !aligned(out, elt(p->out_dtype)) || !aligned(ws, 256))
     return MOE_ERR_MISALIGNED;
-  const bool wide = p->H % 8 == 0 && aligned(table, 16) && aligned(out, 16);
+  const bool wide = p->H % 8 == 0 && aligned(table, 8 * elt(p->table_dtype)) &&
+                    aligned(out, 8 * elt(p->out_dtype));
   const int slices = ceil_div(p->H, kSlice);
   const cudaError_t err = by_types(p, wide, [&](auto t, auto o, auto w) {
     using TT = decltype(t);
@@ -364,7 +365,8 @@ extern "C" int moe_embedding_backward(const moe_embed_problem* p, const int32_t*
   int32_t* start = reinterpret_cast<int32_t*>(base + L.start);
   float* part = reinterpret_cast<float*>(base + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool wide = p->H % 8 == 0 && aligned(d_table, 16) && aligned(d_out, 16);
+  const bool wide = p->H % 8 == 0 && aligned(d_table, 8 * elt(p->table_dtype)) &&
+                    aligned(d_out, 8 * elt(p->out_dtype));
   const int slices = ceil_div(p->H, kSlice), pieces = pieces_of(p->T);
   const int range = sort_range(p->V);
   const size_t smem = sizeof(int32_t) * kSortWarps * range;

@@ -46,6 +46,51 @@ __device__ __forceinline__ void store_stream16(void* p, uint4 v) {
                : "memory");
 }
 
+// 32 bytes (32-byte aligned): a thread's eight fp32 values in one access, so
+// that a warp's access covers whole sectors.
+__device__ __forceinline__ void load_stream32(float (&f)[8], const float* p) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
+                 "=f"(f[6]), "=f"(f[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store_stream32(float* p, const float (&f)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]),
+               "f"(f[7])
+               : "memory");
+}
+// What eight elements of T in one access need of their address.
+template <typename T>
+__host__ __device__ constexpr int oct_align() { return 8 * static_cast<int>(sizeof(T)); }
+
+// Two fp32 values in one register pair, for the packed fp32 instructions.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float pair_sum(Pair p) {
+  float lo, hi;
+  unpair(p, lo, hi);
+  return lo + hi;
+}
+
 // Eight elements as loaded.
 template <typename T>
 struct Oct;
@@ -55,6 +100,12 @@ struct Oct<Bf16> {
   uint32_t w[4];
   __device__ __forceinline__ float get(int j) const {
     return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+  __device__ __forceinline__ Pair pair(int i) const { return pair_of(bf16_lo(w[i]), bf16_hi(w[i])); }
+  __device__ __forceinline__ void set_pair(int i, Pair p) {
+    float lo, hi;
+    unpair(p, lo, hi);
+    w[i] = pack_bf16(lo, hi);
   }
   __device__ __forceinline__ void load(const Bf16* p) {
     const uint4 v = load_stream16(p);
@@ -77,21 +128,10 @@ template <>
 struct Oct<float> {
   float f[8];
   __device__ __forceinline__ float get(int j) const { return f[j]; }
-  __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 v = load_stream16(p + 4 * h);
-      f[4 * h] = __uint_as_float(v.x), f[4 * h + 1] = __uint_as_float(v.y);
-      f[4 * h + 2] = __uint_as_float(v.z), f[4 * h + 3] = __uint_as_float(v.w);
-    }
-  }
-  __device__ __forceinline__ void store(float* p) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      store_stream16(p + 4 * h,
-                     make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
-                                __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])));
-  }
+  __device__ __forceinline__ Pair pair(int i) const { return pair_of(f[2 * i], f[2 * i + 1]); }
+  __device__ __forceinline__ void set_pair(int i, Pair p) { unpair(p, f[2 * i], f[2 * i + 1]); }
+  __device__ __forceinline__ void load(const float* p) { load_stream32(f, p); }
+  __device__ __forceinline__ void store(float* p) const { store_stream32(p, f); }
   __device__ __forceinline__ void set_bits(int j, float x) { f[j] = x; }
   __device__ __forceinline__ void set(const float (&x)[8]) {
 #pragma unroll
@@ -100,8 +140,8 @@ struct Oct<float> {
 };
 
 // The columns of step v of thread `tid` of `n` threads on a row: kWide, eight
-// neighbours (a 16-byte vector of bf16, two of fp32; the width is a multiple
-// of 8); otherwise eight single columns n apart, so that the threads' single
+// neighbours (one access of 16 bytes of bf16, 32 of fp32; the width is a
+// multiple of 8); otherwise eight single columns n apart, so that the threads' single
 // loads stay coalesced.
 template <bool kWide>
 __device__ __forceinline__ int oct_col(int v, int j, int tid, int n) {
@@ -148,9 +188,14 @@ __device__ __forceinline__ void store_oct(const float (&x)[8], T* row, int v, in
   }
 }
 
-// Copies of a thread's own octets to shared memory and back, for rows read some
-// rows ahead: no other thread touches them, so no barrier is needed.  A step of
-// n threads takes n * 16 bytes (bf16) or two runs of that (fp32).
+// Copies of a warp's octets to shared memory and back, for rows read some rows
+// ahead.  Only the warp's own lanes touch them: after copy_async_wait (and
+// before the next copy to the same place) __syncwarp is barrier enough.  A
+// step of n threads takes n * 16 bytes (bf16) or n * 32 (fp32, where lane l
+// copies the 16-byte pieces l and 32 + l of the warp's 1 KB, so that every
+// copy of a warp is contiguous; bit 3 of a piece's number flips its lowest
+// bit, which keeps the lanes' reads of two neighbouring pieces free of bank
+// conflicts).
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -172,21 +217,29 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t src) {
                : "memory");
   return v;
 }
-template <typename T>
-__host__ __device__ constexpr int oct_vecs() { return static_cast<int>(sizeof(T)) / 2; }  // 16-byte vectors
-template <typename T>
-__device__ __forceinline__ void oct_copy(uint32_t step, const T* src, int tid, int n) {
-#pragma unroll
-  for (int h = 0; h < oct_vecs<T>(); ++h) copy_async16(step + (h * n + tid) * 16, src + 4 * h);
+// row: the row's first element; c: this thread's first column in the step.
+__device__ __forceinline__ void oct_copy(uint32_t step, const Bf16* row, int c, int tid, int H) {
+  if (c < H) copy_async16(step + tid * 16, row + c);
 }
-__device__ __forceinline__ void oct_read(Oct<Bf16>& o, uint32_t step, int tid, int) {
+__device__ __forceinline__ void oct_copy(uint32_t step, const float* row, int c, int tid, int H) {
+  const int lane = tid & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int piece = h * 32 + lane, col = c - lane * 8 + piece * 4;
+    if (col < H)
+      copy_async16(step + (tid - lane) * 32 + (piece ^ ((piece >> 3) & 1)) * 16, row + col);
+  }
+}
+__device__ __forceinline__ void oct_read(Oct<Bf16>& o, uint32_t step, int tid) {
   const uint4 v = load_shared16(step + tid * 16);
   o.w[0] = v.x, o.w[1] = v.y, o.w[2] = v.z, o.w[3] = v.w;
 }
-__device__ __forceinline__ void oct_read(Oct<float>& o, uint32_t step, int tid, int n) {
+__device__ __forceinline__ void oct_read(Oct<float>& o, uint32_t step, int tid) {
+  const int lane = tid & 31;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 v = load_shared16(step + (h * n + tid) * 16);
+    const int piece = 2 * lane + h;
+    const uint4 v = load_shared16(step + (tid - lane) * 32 + (piece ^ ((piece >> 3) & 1)) * 16);
     o.f[4 * h] = __uint_as_float(v.x), o.f[4 * h + 1] = __uint_as_float(v.y);
     o.f[4 * h + 2] = __uint_as_float(v.z), o.f[4 * h + 3] = __uint_as_float(v.w);
   }
