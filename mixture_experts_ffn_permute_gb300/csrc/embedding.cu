@@ -9,14 +9,19 @@
 //      (the base of its part of the sorted list) and those inside, per warp
 //      and id, then places its tokens by a second scan.  A stable counting
 //      sort without a global histogram or any pass over another block's
-//      counts.
-//   2. rows.  One warp per (id, 512 columns) sums the id's tokens and writes
-//      the row: zeros where there is none, which for a large vocabulary is
-//      most of the bytes.  Ids with more than 64 tokens ("heavy") are left
-//      out here; their runs are cut at multiples of 64 sorted positions and
-//      each piece is one warp's item, so that a frequent token does not keep
-//      one warp busy.  The pieces' fp32 sums go to the workspace.
-//   3. join.  Heavy ids: the pieces are added in order.
+//      counts.  The block then knows which of its ids have no token and fills
+//      their rows with zeros, run by run: for a large vocabulary most of the
+//      bytes.
+//   2. rows.  The sorted list is cut into pieces of 8 to 32 tokens, whatever their
+//      ids, one group of threads (8 columns a thread) per piece and 2048
+//      columns: every group has the same work, however the ids are
+//      distributed.  A row whose tokens all lie in the piece is written; the
+//      sums of an id that goes on before or behind it go to the workspace in
+//      fp32.
+//   3. join.  Ids of several pieces: the pieces' sums are added in order.
+// Two forms of 2 that gave ids to warps or groups took 100 and 142 us at
+// T=16384 V=32000 H=4096 bf16 with word frequencies: the latencies of a few
+// tokens an id do not overlap.
 // HBM bound: T rows read, V rows written.
 #include <cuda_runtime.h>
 
@@ -31,10 +36,10 @@
 namespace moe {
 namespace {
 
-constexpr int kSteps = 2;           // octets of a row per lane
+constexpr int kSteps = 2;           // forward: octets of a row per lane
 constexpr int kSlice = 32 * 8 * kSteps;
-constexpr int kWarps = 8;           // per block of the row kernels
-constexpr int kPiece = 64;          // tokens of a heavy id per item
+constexpr int kWarps = 8;           // forward: warps per block
+constexpr int kMinPiece = 8, kMaxPiece = 32;  // sorted positions per piece
 constexpr int kSortWarps = 32;
 constexpr int kMaxRange = 1024;     // ids per sort block (counters in shared memory)
 constexpr size_t kEmbedHeader = 256;
@@ -71,16 +76,32 @@ embed_fwd_kernel(const int32_t* __restrict__ ids, const TT* __restrict__ table,
 }
 
 // ------------------------------------------------------------------ sort
+// Zeros to the n elements from `at` on, by one warp.
+template <typename T>
+__device__ __forceinline__ void fill_zero(T* at, long n, int lane) {
+  constexpr int kPer = 16 / sizeof(T);
+  const long lead = min(
+      n, static_cast<long>(((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / sizeof(T)));
+  const long vecs = (n - lead) / kPer, tail = lead + vecs * kPer;
+  uint4* v = reinterpret_cast<uint4*>(at + lead);
+  for (long i = lane; i < vecs; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+  if (lane < lead) at[lane] = T{};  // fewer than 8 elements on either side
+  if (tail + lane < n) at[tail + lane] = T{};
+}
+
 // Block b: ids [b * range, (b + 1) * range).  Warp w takes the tokens
 // [w * per, (w + 1) * per) in both scans, so its placements keep token order.
 // count [kSortWarps][range] in shared memory.
+template <typename TT>
 __global__ void __launch_bounds__(32 * kSortWarps)
-embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
-                  int32_t* __restrict__ order, int32_t* __restrict__ start, uint32_t* status) {
+embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int range,
+                  int32_t* __restrict__ order, int32_t* __restrict__ sorted_id,
+                  int32_t* __restrict__ start, TT* __restrict__ d_table, uint32_t* status) {
   pdl_enter();
   extern __shared__ int32_t s_count[];
   __shared__ int32_t s_warp[kSortWarps];
   __shared__ int32_t s_below[kSortWarps];
+  __shared__ bool s_empty[kMaxRange];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int v0 = blockIdx.x * range, v1 = min(V, v0 + range), nv = v1 - v0;
   for (int i = threadIdx.x; i < kSortWarps * range; i += 32 * kSortWarps) s_count[i] = 0;
@@ -122,6 +143,7 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
   }
   if (threadIdx.x < nv) {
     start[v0 + threadIdx.x] = base;
+    s_empty[threadIdx.x] = total == 0;
     if (v0 + static_cast<int>(threadIdx.x) == V - 1) start[V] = base + total;
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = s_count[w * range + threadIdx.x];
@@ -143,123 +165,151 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
       __syncwarp(hits);
       if (rank == 0) mine[id - v0] = at + __popc(same);
       order[at + rank] = static_cast<int32_t>(t);
+      sorted_id[at + rank] = id;
     }
     __syncwarp();
+  }
+  // warp w's share of the range's rows: runs of ids without a token
+  const int i0 = static_cast<int>(static_cast<long>(nv) * warp / kSortWarps);
+  const int i1 = static_cast<int>(static_cast<long>(nv) * (warp + 1) / kSortWarps);
+  for (int i = i0; i < i1;) {
+    if (!s_empty[i]) { ++i; continue; }
+    int j = i + 1;
+    while (j < i1 && s_empty[j]) ++j;
+    fill_zero(d_table + (static_cast<long>(v0) + i) * H, static_cast<long>(j - i) * H, lane);
+    i = j;
   }
 }
 
 // ------------------------------------------------------------------ rows
-// Adds the rows of the sorted positions [p0, p1) to acc, in order.
-template <typename TO, bool kWide>
-__device__ __forceinline__ void sum_tokens(float (&acc)[kSteps][8], const int32_t* order, long p0,
-                                           long p1, const TO* d_out, int H, int c0, int n,
-                                           int lane) {
-  for (long p = p0; p < p1; p += 32) {
-    const int m = static_cast<int>(min(32L, p1 - p));
-    const int mine = lane < m ? order[p + lane] : 0;
-#pragma unroll 4
-    for (int i = 0; i < m; ++i) {
-      const long t = __shfl_sync(0xffffffffu, mine, i);
-      const TO* row = d_out + t * H + c0;
-      Oct<TO> x[kSteps];
-#pragma unroll
-      for (int v = 0; v < kSteps; ++v) load_oct<kWide>(x[v], row, v, lane, 32, n);
-#pragma unroll
-      for (int v = 0; v < kSteps; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[v][j] += x[v].get(j);
-    }
+constexpr int kRowThreads = 256;
+constexpr int kRowCols = kRowThreads * 8;  // columns of a block that is one group
+
+// A group's threads: n of them (32 .. 256), 8 columns each from column c0 on.
+struct Group {
+  int index, tid, n, c0, cols;
+  __device__ __forceinline__ Group(int H, int n_) {
+    n = n_;
+    index = threadIdx.x / n;
+    tid = threadIdx.x - index * n;
+    c0 = blockIdx.y * kRowCols;
+    cols = min(kRowCols, H - c0);
   }
+};
+
+// Tokens in flight per thread (single elements take eight loads a token).
+template <typename TO, bool kWide>
+__host__ __device__ constexpr int batch_of() { return !kWide ? 2 : sizeof(TO) == 2 ? 8 : 4; }
+
+template <typename T>
+__device__ __forceinline__ void add_oct(float (&acc)[8], const Oct<T>& x) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] += x.get(j);
 }
 
-// Items [0, pieces * slices): pieces of heavy ids; then V * slices rows.
+// Piece q of the sorted list.  Its first id may have begun before it and its
+// last may go on behind it: their sums go to the slots 2 q (begun before,
+// whether it ends here or not) and 2 q + 1.
 template <typename TT, typename TO, bool kWide>
-__global__ void __launch_bounds__(32 * kWarps)
-embed_rows_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ order,
+__global__ void __launch_bounds__(kRowThreads, 3)
+embed_rows_kernel(const int32_t* __restrict__ order, const int32_t* __restrict__ sorted_id,
                   const int32_t* __restrict__ start, const TO* __restrict__ d_out,
                   TT* __restrict__ d_table, float* __restrict__ part, int V, int H, int pieces,
-                  int slices, float scale) {
+                  int piece, int group_threads, float scale) {
   pdl_enter();
-  long item = static_cast<long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  constexpr int kBatch = batch_of<TO, kWide>();
+  const Group g(H, group_threads);
   const int lane = threadIdx.x & 31;
-  const long q = item / slices;
-  const int c0 = static_cast<int>(item - q * slices) * kSlice, n = min(kSlice, H - c0);
-  if (q < pieces) {
-    // the piece [64 q, 64 q + 64) of the sorted positions touches at most two
-    // heavy ids: the one at its first position (sum in slot 2 q) and another
-    // that starts inside and goes on beyond its end (slot 2 q + 1)
-    const long total = start[V], p0 = q * kPiece, p1 = min(total, p0 + kPiece);
-    if (p0 >= total) return;
-    const int va = ids[order[p0]], vb = ids[order[p1 - 1]];
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int v = h ? vb : va;
-      if (h && vb == va) break;
-      const long s0 = start[v], s1 = start[v + 1];
-      if (s1 - s0 <= kPiece) continue;
-      float acc[kSteps][8] = {};
-      sum_tokens<TO, kWide>(acc, order, max(s0, p0), min(s1, p1), d_out, H, c0, n, lane);
-      float* dst = part + (2 * q + h) * H + c0;
+  const long q = static_cast<long>(blockIdx.x) * (kRowThreads / group_threads) + g.index;
+  const long total = start[V], p0 = q * piece;
+  if (q >= pieces || p0 >= total) return;  // whole warps
+  const int m = static_cast<int>(min(static_cast<long>(piece), total - p0));
+  const int my_t = lane < m ? __ldg(order + p0 + lane) : 0;
+  const int my_v = lane < m ? __ldg(sorted_id + p0 + lane) : -1;
+  const int before = p0 > 0 ? __ldg(sorted_id + p0 - 1) : -1;
+  const int behind = p0 + m < total ? __ldg(sorted_id + p0 + m) : -1;
+  int cur = __shfl_sync(0xffffffffu, my_v, 0);
+  bool begun = before == cur;  // the present id began in an earlier piece
+  float acc[8] = {};
+  auto flush = [&](bool goes_on) {
+    if (begun || goes_on) {
+      float* dst = part + (2 * q + (begun ? 0 : 1)) * H + g.c0;
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u)
+      for (int j = 0; j < 8; ++j) {
+        const int c = oct_col<kWide>(0, j, g.tid, g.n);
+        if (c < g.cols) dst[c] = acc[j];
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = oct_col<kWide>(u, j, lane, 32);
-          if (c < n) dst[c] = acc[u][j];
-        }
+      for (int j = 0; j < 8; ++j) acc[j] *= scale;
+      store_oct<kWide>(acc, d_table + static_cast<long>(cur) * H + g.c0, 0, g.tid, g.n, g.cols);
     }
-    return;
-  }
-  const long v = q - pieces;
-  if (v >= V) return;
-  const long s0 = start[v], s1 = start[v + 1];
-  if (s1 - s0 > kPiece) return;
-  float acc[kSteps][8] = {};
-  sum_tokens<TO, kWide>(acc, order, s0, s1, d_out, H, c0, n, lane);
+  };
+#pragma unroll 1
+  for (int i = 0; i < m; i += kBatch) {
+    Oct<TO> x[kBatch];
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
+      const long t = __shfl_sync(0xffffffffu, my_t, (i + u) & 31);
+      if (i + u < m) load_oct<kWide>(x[u], d_out + t * H + g.c0, 0, g.tid, g.n, g.cols);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[u][j] *= scale;
-    store_oct<kWide>(acc[u], d_table + v * H + c0, u, lane, 32, n);
+    for (int u = 0; u < kBatch; ++u) {
+      const int v = __shfl_sync(0xffffffffu, my_v, (i + u) & 31);
+      if (i + u < m) {
+        if (v != cur) {
+          flush(false);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+          cur = v;
+          begun = false;
+        }
+        add_oct(acc, x[u]);
+      }
+    }
   }
+  flush(behind == cur);
 }
 
-// Piece q: the heavy id that starts in it, if any (there is at most one).
+// The id that starts in piece q and goes on behind it, if there is one.  64
+// threads take 512 columns; the four of them in a block take a quarter of the
+// id's pieces each, so that a frequent id's are not one chain of loads.
+constexpr int kJoinCols = 512, kJoinRuns = 4;
 template <typename TT, bool kWide>
-__global__ void __launch_bounds__(32 * kWarps)
-embed_join_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ order,
-                  const int32_t* __restrict__ start, const float* __restrict__ part,
-                  TT* __restrict__ d_table, int V, int H, int pieces, int slices, float scale) {
+__global__ void __launch_bounds__(64 * kJoinRuns)
+embed_join_kernel(const int32_t* __restrict__ sorted_id, const int32_t* __restrict__ start,
+                  const float* __restrict__ part, TT* __restrict__ d_table, int V, int H,
+                  int piece, float scale) {
   pdl_enter();
-  const long item = static_cast<long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long q = item / slices;
-  const int c0 = static_cast<int>(item - q * slices) * kSlice, n = min(kSlice, H - c0);
-  if (q >= pieces) return;
-  const long total = start[V], p0 = q * kPiece, p1 = min(total, p0 + kPiece);
-  if (p0 >= total) return;
-  const long v = ids[order[p1 - 1]];
-  const long s0 = start[v], s1 = start[v + 1];
-  if (s1 - s0 <= kPiece || s0 < p0) return;
-  float acc[kSteps][8] = {};
+  __shared__ float s_sum[kJoinRuns - 1][8][64];
+  const long q = blockIdx.x;
+  const int c0 = blockIdx.y * kJoinCols, cols = min(kJoinCols, H - c0);
+  const int run = threadIdx.x / 64, tid = threadIdx.x & 63;
+  const long total = start[V], p0 = q * piece, p1 = p0 + piece;
+  if (p1 >= total) return;
+  const long v = __ldg(sorted_id + p1 - 1);
+  if (__ldg(sorted_id + p1) != v || (p0 > 0 && __ldg(sorted_id + p0 - 1) == v)) return;
+  const long n = (start[v + 1] - 1) / piece - q + 1;  // its pieces
+  const long i1 = q + n * (run + 1) / kJoinRuns;
+  float acc[8] = {};
 #pragma unroll 4
-  for (long i = q; i * kPiece < s1; ++i) {
-    // in its first piece the id is at the first position, or it starts inside
-    const float* src = part + (2 * i + (i == q && s0 > p0 ? 1 : 0)) * H + c0;
-    Oct<float> x[kSteps];
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) load_oct<kWide>(x[u], src, u, lane, 32, n);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[u][j] += x[u].get(j);
+  for (long i = q + n * run / kJoinRuns; i < i1; ++i) {
+    Oct<float> x;
+    load_oct<kWide>(x, part + (2 * i + (i == q ? 1 : 0)) * H + c0, 0, tid, 64, cols);
+    add_oct(acc, x);
   }
+  if (run) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[u][j] *= scale;
-    store_oct<kWide>(acc[u], d_table + v * H + c0, u, lane, 32, n);
+    for (int j = 0; j < 8; ++j) s_sum[run - 1][j][tid] = acc[j];
   }
+  __syncthreads();
+  if (run) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    for (int r = 0; r < kJoinRuns - 1; ++r) acc[j] += s_sum[r][j][tid];
+    acc[j] *= scale;
+  }
+  store_oct<kWide>(acc, d_table + v * H + c0, 0, tid, 64, cols);
 }
 
 // ------------------------------------------------------------------ host
@@ -270,19 +320,36 @@ int check_embed(const moe_embed_problem* p) {
   if (!p || p->T < 0 || p->V < 1 || p->H < 1) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(p->table_dtype) || !dtype_ok(p->out_dtype)) return MOE_ERR_INVALID_ARG;
   const long long slices = (p->H + kSlice - 1) / kSlice;
-  // block indices: (rows + pieces) * slices / 8 warps
+  // block indices of the forward: tokens * slices / 8 warps
   if (p->T > (1 << 28) || p->V > (1 << 28) || p->H > (1 << 20) ||
-      (static_cast<long long>(p->V) + p->T) * slices / kWarps >= (1LL << 31) - 2)
+      p->T * slices / kWarps >= (1LL << 31) - 2)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
+// A group's threads: 8 columns each, a power of two of warps.
+int group_threads(int H) {
+  int n = 32;
+  while (n < kRowThreads && n * 8 < H) n *= 2;
+  return n;
+}
+
 // Ids per sort block: as many blocks as SMs while the counters fit.
 int sort_range(int V) { return std::min(kMaxRange, std::max(32, ceil_div(V, num_sms()))); }
-int pieces_of(int T) { return ceil_div(T, kPiece); }
+// Tokens per piece: the most (fewer sums through the workspace) that still
+// gives every SM four blocks.  T=3001 H=1001 fp32: rows 20 us with 32.
+int piece_of(int T, int H) {
+  const int groups = kRowThreads / group_threads(H);
+  int piece = kMaxPiece;
+  while (piece > kMinPiece && static_cast<long>(ceil_div(T, static_cast<long>(piece) * groups)) *
+                                      ceil_div(H, kRowCols) <
+                                  4L * num_sms())
+    piece /= 2;
+  return piece;
+}
 
 struct EmbedLayout {
-  size_t order, start, part, total;
+  size_t order, sorted_id, start, part, total;
 };
 EmbedLayout embed_layout(const moe_embed_problem* p) {
   EmbedLayout L;
@@ -293,8 +360,9 @@ EmbedLayout embed_layout(const moe_embed_problem* p) {
     return at;
   };
   L.order = take(sizeof(int32_t) * static_cast<size_t>(p->T));
+  L.sorted_id = take(sizeof(int32_t) * static_cast<size_t>(p->T));
   L.start = take(sizeof(int32_t) * (static_cast<size_t>(p->V) + 1));
-  L.part = take(sizeof(float) * 2 * static_cast<size_t>(pieces_of(p->T)) * p->H);
+  L.part = take(sizeof(float) * 2 * static_cast<size_t>(ceil_div(p->T, piece_of(p->T, p->H))) * p->H);
   L.total = o;
   return L;
 }
@@ -362,42 +430,46 @@ extern "C" int moe_embedding_backward(const moe_embed_problem* p, const int32_t*
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* order = reinterpret_cast<int32_t*>(base + L.order);
+  int32_t* sorted_id = reinterpret_cast<int32_t*>(base + L.sorted_id);
   int32_t* start = reinterpret_cast<int32_t*>(base + L.start);
   float* part = reinterpret_cast<float*>(base + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = p->H % 8 == 0 && aligned(d_table, 8 * elt(p->table_dtype)) &&
                     aligned(d_out, 8 * elt(p->out_dtype));
-  const int slices = ceil_div(p->H, kSlice), pieces = pieces_of(p->T);
+  const int group = group_threads(p->H), piece = piece_of(p->T, p->H);
+  const int pieces = ceil_div(p->T, piece);
   const int range = sort_range(p->V);
   const size_t smem = sizeof(int32_t) * kSortWarps * range;
   set_last_launch_count(0);
-  if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(int32_t) * kSortWarps * kMaxRange)) !=
-          cudaSuccess ||
-      launch_kernel(embed_sort_kernel, dim3(ceil_div(p->V, range)), dim3(32 * kSortWarps), smem, s,
-                    1, ids, p->T, p->V, range, order, start, static_cast<uint32_t*>(ws)) !=
-          cudaSuccess)
-    return MOE_ERR_CUDA;
-  int launches = 1;
+  int launches = 0;
   const cudaError_t err = by_types(p, wide, [&](auto t, auto o, auto w) {
     using TT = decltype(t);
     using TO = decltype(o);
     constexpr bool kWide = decltype(w)::value;
-    cudaError_t e = launch_kernel(
-        embed_rows_kernel<TT, TO, kWide>,
-        dim3(blocks_of((static_cast<long>(p->V) + pieces) * slices)), dim3(32 * kWarps), 0, s, 1,
-        ids, static_cast<const int32_t*>(order), static_cast<const int32_t*>(start),
-        static_cast<const TO*>(d_out), static_cast<TT*>(d_table), part, p->V, p->H, pieces, slices,
-        p->scale);
+    cudaError_t e = cudaFuncSetAttribute(
+        embed_sort_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(sizeof(int32_t) * kSortWarps * kMaxRange));
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(embed_sort_kernel<TT>, dim3(ceil_div(p->V, range)), dim3(32 * kSortWarps),
+                      smem, s, 1, ids, p->T, p->V, p->H, range, order, sorted_id, start,
+                      static_cast<TT*>(d_table), static_cast<uint32_t*>(ws));
     if (e != cudaSuccess) return e;
     ++launches;
-    if (pieces < 2) return e;  // an id has more than 64 tokens only if there are more
+    if (pieces == 0) return e;
+    e = launch_kernel(embed_rows_kernel<TT, TO, kWide>,
+                      dim3(ceil_div(pieces, kRowThreads / group), ceil_div(p->H, kRowCols)),
+                      dim3(kRowThreads), 0, s, 1, static_cast<const int32_t*>(order),
+                      static_cast<const int32_t*>(sorted_id), static_cast<const int32_t*>(start),
+                      static_cast<const TO*>(d_out), static_cast<TT*>(d_table), part, p->V, p->H,
+                      pieces, piece, group, p->scale);
+    if (e != cudaSuccess) return e;
     ++launches;
-    return launch_kernel(embed_join_kernel<TT, kWide>,
-                         dim3(blocks_of(static_cast<long>(pieces) * slices)), dim3(32 * kWarps), 0,
-                         s, 1, ids, static_cast<const int32_t*>(order),
+    if (pieces == 1) return e;  // nothing goes on into another piece
+    ++launches;
+    return launch_kernel(embed_join_kernel<TT, kWide>, dim3(pieces, ceil_div(p->H, kJoinCols)),
+                         dim3(64 * kJoinRuns), 0, s, 1, static_cast<const int32_t*>(sorted_id),
                          static_cast<const int32_t*>(start), static_cast<const float*>(part),
-                         static_cast<TT*>(d_table), p->V, p->H, pieces, slices, p->scale);
+                         static_cast<TT*>(d_table), p->V, p->H, piece, p->scale);
   });
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   set_last_launch_count(launches);

@@ -32,9 +32,9 @@ constexpr int kClipUnroll = 4;       // 16-byte loads in flight per thread
 constexpr int kClipBlocksPerSm = 8;  // 2048 threads
 constexpr int kMaxClipBlocks = 2048; // per launch; bounds the workspace
 constexpr size_t kClipHeader = 256;
-// Tables by capacity: the small one fits the first 4 KB of parameters.
-constexpr int kSmallTable = 96;
-constexpr int kLargeTable = 768;
+// Tables by capacity: parameters are copied with every launch, so a short list
+// takes a short table.
+constexpr int kSmallTable = 64, kMiddleTable = 256, kLargeTable = 1024;
 
 template <int kCap>
 struct GradTable {
@@ -44,7 +44,7 @@ struct GradTable {
   void* out[kCap];
   long numel[kCap];      // sign bit: fp32
 };
-static_assert(sizeof(GradTable<kLargeTable>) < 32000, "kernel parameters");
+static_assert(sizeof(GradTable<kLargeTable>) <= 32000, "kernel parameters");
 
 struct Chunk {
   const uint8_t* grad;  // first element
@@ -262,6 +262,7 @@ template <int kCap>
 int run_clip(int n, const moe_grad_tensor* g, float grad_scale, float max_norm, float eps,
              float* norm_out, double* part, cudaStream_t s) {
   GradTable<kCap> t;
+  fill_table(t, g, 0);
   int launches = 0, n_part = 0;
   for (int i = 0; i < n; i += kCap) {
     fill_table(t, g + i, std::min(kCap, n - i));
@@ -275,7 +276,7 @@ int run_clip(int n, const moe_grad_tensor* g, float grad_scale, float max_norm, 
   // the last table first: its tensors were read last.  One launch at least,
   // for the norm.
   for (int i = n ? (n - 1) / kCap * kCap : 0; i >= 0; i -= kCap) {
-    fill_table(t, g + i, std::min(kCap, n - i));
+    if (n > kCap) fill_table(t, g + i, std::min(kCap, n - i));  // else it still holds them
     if (launch_kernel(grad_scale_kernel<kCap>, dim3(clip_blocks(t.chunk0[t.n])),
                       dim3(kClipThreads), 0, s, 1, t, static_cast<const double*>(part), n_part,
                       grad_scale, max_norm, eps, launches == (n + kCap - 1) / kCap ? norm_out
@@ -295,7 +296,7 @@ using namespace moe;
 
 extern "C" size_t moe_clip_workspace_size(int32_t n) {
   if (n < 0 || n > MOE_MAX_GRAD_TENSORS) return 0;
-  const int tables = n <= kSmallTable ? 1 : (n + kLargeTable - 1) / kLargeTable;
+  const int tables = std::max(1, ceil_div(n, kLargeTable));
   return kClipHeader + sizeof(double) * kMaxClipBlocks * static_cast<size_t>(tables);
 }
 
@@ -325,5 +326,7 @@ extern "C" int moe_clip_grad_norm(int32_t n, const moe_grad_tensor* tensors, flo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return n <= kSmallTable
              ? run_clip<kSmallTable>(n, tensors, grad_scale, max_norm, eps, norm_out, part, s)
+         : n <= kMiddleTable
+             ? run_clip<kMiddleTable>(n, tensors, grad_scale, max_norm, eps, norm_out, part, s)
              : run_clip<kLargeTable>(n, tensors, grad_scale, max_norm, eps, norm_out, part, s);
 }

@@ -102,6 +102,35 @@ def test_backward_widths(H):
     check_backward(ids_of(400, 37, "mixed"), 37, H, BF, BF)
 
 
+@pytest.mark.parametrize("H", [40, 248, 256, 264, 513, 1024, 1025, 2047, 2048, 2049, 2056, 4104])
+def test_groups_and_column_blocks(H):
+    """Every group size (32 to 256 threads) and several column blocks, with long, short and
+    empty runs of ids."""
+    for V, T, kind in ((1000, 300, "uniform"), (37, 600, "mixed"), (600, 900, "few")):
+        check_backward(ids_of(T, V, kind, H), V, H, BF, F32)
+        check_backward(ids_of(T, V, kind, H), V, H, F32, BF)
+
+
+def test_unaligned_rows():
+    """A table and gradients that start off a 16-byte boundary."""
+    for shift in (1, 3):
+        ids = ids_of(500, 90, "mixed")
+        d = torch.randn(500 * 64 + shift, device=DEV).to(BF)[shift:].view(500, 64)
+        full = torch.full((90 * 64 + 16,), float("nan"), dtype=BF, device=DEV)
+        t = full[shift:shift + 90 * 64].view(90, 64)
+        p = moe.EmbedProblem.make(500, 90, 64, BF, BF)
+        moe.embedding_backward(p, ids.to(DEV), d, t, moe.alloc_embedding_workspace(p))
+        ok = ids >= 0
+        want = torch.zeros(90, 64, dtype=torch.float64).index_add_(
+            0, ids[ok].long(), d.double().cpu()[ok])
+        err = (t.double().cpu() - want).abs()
+        assert (err <= 2.0 ** -8 * want.abs() + 1e-3).all()
+        assert torch.isnan(full[:shift]).all() and torch.isnan(full[shift + 90 * 64:]).all()
+        out = torch.empty(500 * 64 + shift, dtype=BF, device=DEV)[shift:].view(500, 64)
+        moe.embedding_forward(p, ids.to(DEV), t, out)
+        assert torch.equal(out[ok.to(DEV)], t[ids[ok].long().to(DEV)])
+
+
 def test_runs_round_the_piece_boundaries():
     """Runs of 64, 65 and more tokens that start at, before and after multiples of 64."""
     for lead in (0, 1, 63, 64, 65):

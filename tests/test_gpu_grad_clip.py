@@ -79,6 +79,12 @@ def test_many_tensors(n):
     check(tensors(sizes, [BF if i % 3 else F32 for i in range(n)]), 2.0)
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 255, 256, 257, 1023, 1024, 1025, 2050])
+def test_table_sizes(n):
+    sizes = [1 + (41 * i) % 900 for i in range(n)]
+    check(tensors(sizes, [F32 if i % 3 else BF for i in range(n)]), 2.0, scale=0.25)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_every_alignment(dtype):
     """Views at every element offset, and outputs whose 16-byte boundaries lie elsewhere."""
