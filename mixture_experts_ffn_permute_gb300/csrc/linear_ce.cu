@@ -38,7 +38,8 @@
 // other accumulator.
 //
 // Warp roles (one CTA per SM, tiles dealt to the pairs in a fixed order):
-//   warp 0     TMA producer: 3 stages of 32 KB of A and up to 32 KB of B per CTA
+//   warp 0     TMA producer: 3 stages of 32 KB of A and 32 KB of B per CTA, up to 8
+//              where few rows or narrow tiles make them smaller
 //   warp 1     TMEM allocation, MMA issue (the leader CTA's)
 //   warps 2..  epilogue, thread = row of the tile; two accumulators of 256
 //              columns, so it overlaps the next mainloop; bf16 tiles leave
@@ -63,16 +64,14 @@ namespace {
 constexpr int kTileM = 256;  // rows of a pair tile, 128 per CTA
 constexpr int kTileN = 256;  // columns at most
 constexpr int kTileK = 128;  // one stage
-constexpr int kStagesCe = 3;
+constexpr int kMaxStages = 8;
 constexpr uint32_t kPlane = 128 * 64 * 2;            // 128 rows x 64 columns, 16 KB
-constexpr uint32_t kABytesCe = 2 * kPlane;
-constexpr uint32_t kBBytesCe = 2 * kPlane;
-constexpr uint32_t kStageCe = kABytesCe + kBBytesCe;
+constexpr uint32_t kRingCe = 3 * 4 * kPlane;         // 3 full stages, more of smaller ones
 constexpr int kPromote = 8;  // forward: stages per accumulation in TMEM (K = 1024)
 constexpr uint32_t kStagingBox = 32 * 128;           // 32 rows x 64 bf16
 constexpr int kStagingBuffers = 2;
 constexpr uint32_t kStagingCe = 4 * kStagingBuffers * kStagingBox;
-constexpr size_t kSmemCe = 1024 + kStagesCe * kStageCe + kStagingCe + 256;
+constexpr size_t kSmemCe = 1024 + kRingCe + kStagingCe + 256;
 static_assert(kSmemCe <= 232448, "shared memory budget");
 constexpr int kGroupM = 8;  // m-tiles whose sweep over the n-tiles shares B tiles in L2
 constexpr float kLog2e = 1.4426950408889634f;
@@ -111,6 +110,8 @@ struct CeParams {
   float* acc;           // kProducts: dx in fp32 [T, N]
   const float* unit;    // kGrad, kProducts: s, the unit of G
   uint32_t* status;
+  int stages;               // of the ring
+  uint32_t a_stage, b_stage;  // bytes of a stage's operands in one CTA
 };
 
 struct CeMaps {
@@ -185,11 +186,13 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = smem;
-  uint8_t* sB = sA + kStagesCe * kABytesCe;
-  uint8_t* s_out = sB + kStagesCe * kBBytesCe;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + kStagingCe);
-  uint64_t* empty = full + kStagesCe;
-  uint64_t* tfull = empty + kStagesCe;
+  uint8_t* sB = sA + p.stages * p.a_stage;
+  uint8_t* s_out = smem + kRingCe;
+  const int n_stages = p.stages;
+  const uint32_t a_stage = p.a_stage, b_stage = p.b_stage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + kStagingCe);  // past the forward's ring
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -199,7 +202,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStagesCe; ++s) {
+    for (int s = 0; s < n_stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -245,7 +248,9 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const int col0 = n * g.n_step + static_cast<int>(rank) * half;
         const bool a_mn = g.a_mn, b_mn = g.b_mn, a_planes = g.a_planes, b_planes = g.b_planes;
         const uint32_t a_plane = static_cast<uint32_t>(g.a_rows) * 128, b_plane = half * 128;
-        // one CTA's rows may hold the whole of a small M
+        // one CTA's rows may hold the whole of a small M (the MMA then reads
+        // whatever the shared memory behind them holds: rows of the
+        // accumulator that nobody reads)
         const bool a_load = rank == 0 || g.M > 128;
         const uint32_t bytes = (g.M > 128 ? 4 : 2) * a_plane + 4 * b_plane;
         const int ksteps = g.ksteps;
@@ -257,8 +262,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = pair::mapa(smem_u32(&full[stage]), 0);
-          uint8_t* a = sA + stage * kABytesCe;
-          uint8_t* b = sB + stage * kBBytesCe;
+          uint8_t* a = sA + stage * a_stage;
+          uint8_t* b = sB + stage * b_stage;
           const int k0 = kb * kTileK;
           if (a_load) {
             const int c = a_mn ? row0 : k0, r = a_mn ? k0 : row0;
@@ -278,17 +283,17 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           }
           ++issued;
           if (++kb == ksteps) kb = 0;
-          if (++stage == kStagesCe) { stage = 0; phase ^= 1; }
+          if (++stage == n_stages) { stage = 0; phase ^= 1; }
         }
         if (!ok) { *abort_flag = 1; break; }
       }
       // no bulk copy left in flight: the last fill of every stage has landed
       // (a pair's copies complete on the leader's barriers; the final cluster
       // barrier keeps the peer's shared memory until then)
-      for (int i = 1; leader && i <= kStagesCe && i <= issued; ++i) {
+      for (int i = 1; leader && i <= n_stages && i <= issued; ++i) {
         int s = stage - i;
         uint32_t ph = phase;
-        if (s < 0) { s += kStagesCe; ph ^= 1; }
+        if (s < 0) { s += n_stages; ph ^= 1; }
         mbar_wait(&full[s], ph, p.status);
       }
     }
@@ -323,8 +328,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           for (int kb = k0; kb < k1; ++kb) {
             if (!mbar_wait(&full[stage], phase, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t a = smem_u32(sA + stage * kABytesCe);
-            const uint32_t b = smem_u32(sB + stage * kBBytesCe);
+            const uint32_t a = smem_u32(sA + stage * a_stage);
+            const uint32_t b = smem_u32(sB + stage * b_stage);
             const uint64_t ad = a_mn ? mn_desc(a) : sw128_kmajor_desc(a);
             const uint64_t bd = b_mn ? mn_desc(b) : sw128_kmajor_desc(b);
 #pragma unroll
@@ -332,7 +337,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
               pair::mma(d_tmem, ad + (kk & 3) * as + (kk >> 2) * a4,
                         bd + (kk & 3) * bs + (kk >> 2) * b4, idesc, kb > k0 || kk != 0);
             pair::commit_both(&empty[stage]);
-            if (++stage == kStagesCe) { stage = 0; phase ^= 1; }
+            if (++stage == n_stages) { stage = 0; phase ^= 1; }
           }
           if (ok) pair::commit_both(&tfull[buf]);
         }
@@ -552,13 +557,13 @@ ce_unit_kernel(const float* __restrict__ d_loss, const int32_t* __restrict__ lab
 }
 
 // lse and loss of every token from its tiles' (max, sum), in tile order: 32
-// tokens x 8 runs of tiles per block.
-__global__ void __launch_bounds__(256)
+// tokens x 32 runs of tiles per block.
+__global__ void __launch_bounds__(1024)
 ce_join_kernel(const float2* __restrict__ part, const float* __restrict__ label_logit,
                const int32_t* __restrict__ labels, int T, int V, int tiles,
                float* __restrict__ loss, float* __restrict__ lse, uint32_t* status) {
   pdl_enter();
-  __shared__ float2 s[8][32];
+  __shared__ float2 s[32][32];
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int t = blockIdx.x * 32 + lane;
   float m = -INFINITY, sum = 0.f;
@@ -569,7 +574,7 @@ ce_join_kernel(const float2* __restrict__ part, const float* __restrict__ label_
     m = cm;
   };
   if (t < T) {
-    const int per = (tiles + 7) / 8, i1 = min(tiles, (q + 1) * per);
+    const int per = (tiles + 31) / 32, i1 = min(tiles, (q + 1) * per);
 #pragma unroll 8
     for (int i = q * per; i < i1; ++i) add(part[static_cast<long>(i) * T + t]);
   }
@@ -578,12 +583,27 @@ ce_join_kernel(const float2* __restrict__ part, const float* __restrict__ label_
   if (q || t >= T) return;
   m = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) add(s[i][lane]);
+  for (int i = 0; i < 32; ++i) add(s[i][lane]);
   const float l = (m + log2f(sum)) * kLn2;
   lse[t] = l;
   const int id = labels[t];
   if (id >= V) record_status(status, kStatusIndex);
   loss[t] = id >= 0 && id < V ? l - label_logit[t] : 0.f;
+}
+
+// dst [rows, cols] = src [rows, H], zeros behind it: rows of whole planes.  H
+// and cols multiples of 8.
+__global__ void __launch_bounds__(256)
+ce_pad_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, long rows, int h_vecs,
+              int col_vecs) {
+  pdl_enter();
+  const long total = rows * col_vecs, step = static_cast<long>(gridDim.x) * 256;
+#pragma unroll 4
+  for (long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
+    const long r = i / col_vecs;
+    const int c = static_cast<int>(i - r * col_vecs);
+    dst[i] = c < h_vecs ? __ldg(src + r * h_vecs + c) : make_uint4(0, 0, 0, 0);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -680,8 +700,17 @@ bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const 
 }
 
 template <CeMode kMode>
-cudaError_t launch_ce(const CeMaps& m0, const CeMaps& m1, const CeParams& p, cudaStream_t s) {
+cudaError_t launch_ce(const CeMaps& m0, const CeMaps& m1, CeParams& p, cudaStream_t s) {
   auto kern = linear_ce_kernel<kMode>;
+  p.a_stage = p.b_stage = 0;
+  for (const Gemm& g : p.g) {
+    if (g.tiles() == 0) continue;
+    p.a_stage = std::max(p.a_stage, static_cast<uint32_t>(g.a_rows) * 256);
+    p.b_stage = std::max(p.b_stage, static_cast<uint32_t>(g.n_step) * 128);
+  }
+  // the forward has no staging for output tiles: its ring takes that room too
+  const uint32_t ring = kRingCe + (kMode == CeMode::kLse ? kStagingCe : 0);
+  p.stages = std::min<int>(kMaxStages, ring / (p.a_stage + p.b_stage));
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemCe));
   if (err != cudaSuccess) return err;
@@ -716,10 +745,25 @@ int check_ce(const moe_ce_problem* p) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Rows whose length is not a multiple of 64 start off the lines that the copies
+// move, and every segment of theirs takes a line more.  With several m-tiles,
+// where W is read from L2 again and again, x and W are copied once to rows of
+// whole planes: T=777 H=1000 V=50021 forward 144 us against 92 us for H=1024
+// rows, T=4096 437 us against 252; the copy takes 30 us there.
+bool padded(const moe_ce_problem* p) { return p->H % 64 != 0 && p->T > kTileM; }
+int padded_width(const moe_ce_problem* p) { return ceil_div(p->H, 64) * 64; }
+
+size_t ce_pad_bytes(const moe_ce_problem* p, long w_rows) {
+  return padded(p) ? up(2 * static_cast<size_t>(p->T) * padded_width(p)) +
+                         up(2 * static_cast<size_t>(w_rows) * padded_width(p))
+                   : 0;
+}
+
 size_t ce_forward_bytes(const moe_ce_problem* p) {
   const int n = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
   const size_t T = static_cast<size_t>(p->T);
-  return kCeHeader + up(sizeof(float2) * T * 2 * ceil_div(p->V, n)) + up(sizeof(float) * T);
+  return kCeHeader + up(sizeof(float2) * T * 2 * ceil_div(p->V, n)) + up(sizeof(float) * T) +
+         ce_pad_bytes(p, p->V);
 }
 
 // Vocabulary rows per piece (a multiple of the tile), pieces of equal size.
@@ -733,7 +777,8 @@ int piece_rows(const moe_ce_problem* p) {
 size_t ce_backward_bytes(const moe_ce_problem* p) {
   const size_t T = static_cast<size_t>(p->T);
   const int rows = piece_rows(p);
-  return kCeHeader + up(2 * T * rows) + (rows < p->V ? up(sizeof(float) * T * p->H) : 0);
+  return kCeHeader + up(2 * T * rows) + (rows < p->V ? up(sizeof(float) * T * p->H) : 0) +
+         ce_pad_bytes(p, std::min(rows, p->V));
 }
 
 bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -746,6 +791,21 @@ int check_ce_tensors(const void* x, const void* w, const int32_t* labels, const 
       !aligned(loss, 4) || !aligned(ws, 256))
     return MOE_ERR_MISALIGNED;
   return MOE_OK;
+}
+
+// A [rows, H] matrix as the GEMMs read it: itself, or its padded copy at `copy`
+// (one launch).
+cudaError_t operand(Matrix* m, const moe_ce_problem* p, const void* src, long rows, void* copy,
+                    cudaStream_t s, int* launches) {
+  *m = {src, rows, p->H, p->H};
+  if (!padded(p)) return cudaSuccess;
+  const int cols = padded_width(p);
+  *m = {copy, rows, cols, cols};
+  ++*launches;
+  const long blocks = std::min<long>(8L * num_sms(), (rows * (cols / 8) + 255) / 256);
+  return launch_kernel(ce_pad_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, 1,
+                       static_cast<const uint4*>(src), static_cast<uint4*>(copy), rows, p->H / 8,
+                       cols / 8);
 }
 
 }  // namespace
@@ -774,24 +834,30 @@ extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, con
   const int n_step = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
   uint8_t* base = static_cast<uint8_t*>(ws) + kCeHeader;
   CeParams k{};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  const size_t n_part = up(sizeof(float2) * static_cast<size_t>(p->T) * 2 * ceil_div(p->V, n_step));
+  uint8_t* pad = base + n_part + up(sizeof(float) * static_cast<size_t>(p->T));
+  Matrix xm, wm;
+  if (operand(&xm, p, x, p->T, pad, s, &launches) != cudaSuccess ||
+      operand(&wm, p, w, p->V, pad + up(2 * static_cast<size_t>(p->T) * padded_width(p)), s,
+              &launches) != cudaSuccess)
+    return MOE_ERR_CUDA;
   CeMaps m{};
-  if (!make_gemm(&k.g[0], &m, p->T, p->V, p->H, n_step, {x, p->T, p->H, p->H}, false,
-                 {w, p->V, p->H, p->H}, false))
+  if (!make_gemm(&k.g[0], &m, p->T, p->V, xm.cols, n_step, xm, false, wm, false))
     return MOE_ERR_CUDA;
   k.labels = labels;
   k.V = p->V;
   k.scale = p->logit_scale;
   k.part = reinterpret_cast<float2*>(base);
-  k.label_logit = reinterpret_cast<float*>(
-      base + up(sizeof(float2) * static_cast<size_t>(p->T) * 2 * k.g[0].n_tiles));
+  k.label_logit = reinterpret_cast<float*>(base + n_part);
   k.status = static_cast<uint32_t*>(ws);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_ce<CeMode::kLse>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
-  if (launch_kernel(ce_join_kernel, dim3(ceil_div(p->T, 32)), dim3(256), 0, s, 1,
+  if (launch_kernel(ce_join_kernel, dim3(ceil_div(p->T, 32)), dim3(1024), 0, s, 1,
                     static_cast<const float2*>(k.part), static_cast<const float*>(k.label_logit),
                     labels, p->T, p->V, 2 * k.g[0].n_tiles, loss, lse, k.status) != cudaSuccess)
     return MOE_ERR_CUDA;
-  set_last_launch_count(2);
+  set_last_launch_count(launches + 2);
   return MOE_OK;
 }
 
@@ -828,7 +894,11 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
   k.lse = lse;
   k.d_loss = d_loss;
   k.d_lse = d_lse;
-  k.acc = reinterpret_cast<float*>(base + up(2 * static_cast<size_t>(p->T) * rows));
+  const size_t n_grad = up(2 * static_cast<size_t>(p->T) * rows);
+  k.acc = reinterpret_cast<float*>(base + n_grad);
+  uint8_t* pad = base + n_grad +
+                 (pieces > 1 ? up(sizeof(float) * static_cast<size_t>(p->T) * p->H) : 0);
+  uint8_t* pad_w = pad + up(2 * static_cast<size_t>(p->T) * padded_width(p));
   k.status = static_cast<uint32_t*>(ws);
   float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kUnitOffset);
   k.unit = unit;
@@ -836,18 +906,20 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
                     unit) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++launches;
+  Matrix xm, wm;
+  if (operand(&xm, p, x, p->T, pad, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
   for (int i = 0; i < pieces; ++i) {
     const int v0 = i * rows, nv = std::min(rows, p->V - v0);
     const uint8_t* wp = static_cast<const uint8_t*>(w) + 2 * static_cast<size_t>(v0) * p->H;
     uint8_t* dwp = static_cast<uint8_t*>(dw) + 2 * static_cast<size_t>(v0) * p->H;
     k.v0 = v0;
     const int n_step = tile_columns(ceil_div(p->T, kTileM), nv, kUnitGrad);
-    const Matrix xm{x, p->T, p->H, p->H}, wm{wp, nv, p->H, p->H};
+    if (operand(&wm, p, wp, nv, pad_w, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
     // padded to whole planes: the epilogue writes zeros there
     const Matrix gm{grad, p->T, ceil_div(nv, 64) * 64L, rows};
     CeMaps m{}, m1{};
     k.g[1] = Gemm{};
-    if (!make_gemm(&k.g[0], &m, p->T, nv, p->H, n_step, xm, false, wm, false) ||
+    if (!make_gemm(&k.g[0], &m, p->T, nv, xm.cols, n_step, xm, false, wm, false) ||
         !make_map(&m.out, grad, p->T, gm.cols, rows, 32))
       return MOE_ERR_CUDA;
     if (launch_ce<CeMode::kGrad>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
