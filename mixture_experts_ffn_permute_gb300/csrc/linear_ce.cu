@@ -85,8 +85,13 @@ struct Gemm {
   bool a_mn, b_mn;            // operand stored [K, M] (resp. [K, N]): read MN-major
   bool a_planes, b_planes;    // one copy per stage (row length a multiple of 64)
   int a_rows;                 // K-major A: rows per CTA that are loaded (128, fewer for small M)
-  bool add, keep;             // fp32 accumulation over launches: add acc, keep it in acc
-  __host__ __device__ int tiles() const { return m_tiles * n_tiles; }
+  int splits;                 // of K: each is a tile of its own with its own sums in acc
+  bool add, keep;             // fp32 sums: add to acc, leave them in acc (else bf16 out)
+  float* acc;                 // [splits][M][N]
+  __host__ __device__ int tiles() const { return m_tiles * n_tiles * splits; }
+  __host__ __device__ int k_begin(int split) const {
+    return static_cast<int>(static_cast<long>(ksteps) * split / splits);
+  }
 };
 
 enum class CeMode : int { kLse = 0, kGrad = 1, kProducts = 2 };
@@ -107,7 +112,6 @@ struct CeParams {
   const float* lse;     // kGrad
   const float* d_loss;
   const float* d_lse;   // or NULL
-  float* acc;           // kProducts: dx in fp32 [T, N]
   const float* unit;    // kGrad, kProducts: s, the unit of G
   uint32_t* status;
   int stages;               // of the ring
@@ -136,8 +140,11 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Tile `i` of a GEMM: groups of kGroupM m-tiles sweep the n-tiles.
-__device__ __forceinline__ void tile_of(const Gemm& g, int i, int& m, int& n) {
+// Tile `i` of a GEMM: split by split, groups of kGroupM m-tiles sweep the
+// n-tiles.
+__device__ __forceinline__ void tile_of(const Gemm& g, int i, int& m, int& n, int& split) {
+  split = i / (g.m_tiles * g.n_tiles);
+  i -= split * (g.m_tiles * g.n_tiles);
   const int per = kGroupM * g.n_tiles;
   const int grp = i / per, within = i - grp * per;
   const int size = min(kGroupM, g.m_tiles - grp * kGroupM);
@@ -157,7 +164,9 @@ struct Deal {
     tiles1 = p.g[1].tiles();
     rem = tiles0 % pairs;
     mine0 = tiles0 / pairs + (pair < rem ? 1 : 0);
-    lead = rem ? (p.g[0].ksteps + p.g[1].ksteps / 2) / max(1, p.g[1].ksteps) : 0;
+    const int k0 = p.g[0].ksteps / max(1, p.g[0].splits);
+    const int k1 = max(1, p.g[1].ksteps / max(1, p.g[1].splits));
+    lead = rem ? (k0 + k1 / 2) / k1 : 0;
   }
   // tile number `i` of this pair: false past the last; `second`: of g[1]
   __device__ __forceinline__ bool at(int i, int& tile, bool& second) const {
@@ -228,7 +237,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   // nothing above touches global memory
   pdl_enter();
   const Deal deal(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
-  int tile, m, n;
+  int tile, m, n, split;
   bool two;
 
   if (warp == 0) {
@@ -242,7 +251,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         if (*abort_flag) break;
         const Gemm& g = p.g[two];
         const CeMaps& maps = two ? m1 : m0;
-        tile_of(g, tile, m, n);
+        tile_of(g, tile, m, n, split);
         const int row0 = m * kTileM + static_cast<int>(rank) * 128;
         const int half = g.n_step / 2;
         const int col0 = n * g.n_step + static_cast<int>(rank) * half;
@@ -253,12 +262,12 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         // accumulator that nobody reads)
         const bool a_load = rank == 0 || g.M > 128;
         const uint32_t bytes = (g.M > 128 ? 4 : 2) * a_plane + 4 * b_plane;
-        const int ksteps = g.ksteps;
+        const int k_first = g.k_begin(split), k_last = g.k_begin(split + 1);
         // with one m-tile every pair reads the same A: each starts elsewhere in
         // K, so that they do not all ask for the same lines at once
-        int kb = g.m_tiles == 1 ? deal.pair % ksteps : 0;
+        int kb = k_first + (g.m_tiles == 1 ? deal.pair % (k_last - k_first) : 0);
         bool ok = true;
-        for (int j = 0; j < ksteps; ++j) {
+        for (int j = k_first; j < k_last; ++j) {
           if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = pair::mapa(smem_u32(&full[stage]), 0);
@@ -282,7 +291,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             pair::tma_load(b + b_plane, &maps.b, c + 64, r, bar, pol);
           }
           ++issued;
-          if (++kb == ksteps) kb = 0;
+          if (++kb == k_last) kb = k_first;
           if (++stage == n_stages) { stage = 0; phase ^= 1; }
         }
         if (!ok) { *abort_flag = 1; break; }
@@ -308,7 +317,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         if (*abort_flag) break;
         const Gemm& g = p.g[two];
         const bool a_mn = g.a_mn, b_mn = g.b_mn;
-        const int ksteps = g.ksteps;
+        split = tile / (g.m_tiles * g.n_tiles);
+        const int ksteps = g.k_begin(split + 1) - g.k_begin(split);
         const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(g.n_step)) |
                                (static_cast<uint32_t>(a_mn) << 15) |
                                (static_cast<uint32_t>(b_mn) << 16);
@@ -372,7 +382,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     for (int i = 0; go && deal.at(i, tile, two); ++i) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
       const Gemm& g = p.g[two];
-      tile_of(g, tile, m, n);
+      tile_of(g, tile, m, n, split);
       const int wrow0 = m * kTileM + static_cast<int>(rank) * 128 + quad * 32;
       const int row = wrow0 + lane;
       const bool row_ok = row < g.M, warp_ok = wrow0 < g.M;
@@ -448,7 +458,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const bool f32_only = kMode == CeMode::kProducts && g.keep;
         float* acc = nullptr;
         if (kMode == CeMode::kProducts && (g.add || g.keep))
-          acc = p.acc + static_cast<long>(row) * g.N + col0;
+          acc = g.acc + (static_cast<long>(split) * g.M + row) * g.N + col0;
         const CUtensorMap* out = two ? &m1.out : &m0.out;
         const float S = kMode == CeMode::kProducts ? p.scale * __ldg(p.unit) : 1.f;
 #pragma unroll 1
@@ -591,6 +601,28 @@ ce_join_kernel(const float2* __restrict__ part, const float* __restrict__ label_
   loss[t] = id >= 0 && id < V ? l - label_logit[t] : 0.f;
 }
 
+// out [n] bf16 = scale * unit * the sum of the splits' fp32 sums, in order; n a
+// multiple of 8.
+__global__ void __launch_bounds__(256)
+ce_split_join_kernel(const float* __restrict__ acc, int splits, long n, float scale,
+                     const float* __restrict__ unit, uint4* __restrict__ out) {
+  pdl_enter();
+  const float f = scale * *unit;
+  const long step = static_cast<long>(gridDim.x) * 256;
+  for (long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; i < n / 8; i += step) {
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4* q = reinterpret_cast<const float4*>(acc + s * n) + 2 * i;
+      const float4 a = __ldg(q), b = __ldg(q + 1);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    out[i] = make_uint4(pack_bf16(f * v[0], f * v[1]), pack_bf16(f * v[2], f * v[3]),
+                        pack_bf16(f * v[4], f * v[5]), pack_bf16(f * v[6], f * v[7]));
+  }
+}
+
 // dst [rows, cols] = src [rows, H], zeros behind it: rows of whole planes.  H
 // and cols multiples of 8.
 __global__ void __launch_bounds__(256)
@@ -686,6 +718,7 @@ bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const 
   g->n_tiles = ceil_div(N, n_step);
   g->ksteps = ceil_div(K, kTileK);
   g->n_step = n_step;
+  g->splits = 1;
   g->a_mn = a_mn;
   g->b_mn = b_mn;
   g->a_planes = a.cols % 64 == 0;
@@ -774,11 +807,50 @@ int piece_rows(const moe_ce_problem* p) {
   return ceil_div(ceil_div(p->V, pieces), kTileM) * kTileM;
 }
 
-size_t ce_backward_bytes(const moe_ce_problem* p) {
-  const size_t T = static_cast<size_t>(p->T);
+// Splits of the two products of a piece.  A tile with few others and a long K
+// (dx for few tokens, dW for a small vocabulary) would keep one CTA pair busy
+// long after the rest have finished: K is cut so that no tile takes more than
+// half of a pair's share of the launch, into parts of eight stages at least.
+// T=777 H=1000 V=50021: dx is 16 tiles of 391 stages, and both products took
+// 270 us unsplit.
+struct Splits {
+  int dx, dw;
+};
+Splits splits_of(const moe_ce_problem* p, int rows) {
+  const long cols = ceil_div(p->H, kTileN), pairs = std::max(1, num_sms() / 2);
+  const long nv = std::min(rows, p->V);
+  const long t0 = ceil_div(p->T, kTileM) * cols, k0 = ceil_div(nv, kTileK);
+  const long t1 = ceil_div(nv, kTileM) * cols, k1 = ceil_div(p->T, kTileK);
+  const long share = std::max(1L, (t0 * k0 + t1 * k1) / pairs);
+  auto cut = [&](long k) {
+    return static_cast<int>(std::max(1L, std::min((2 * k + share - 1) / share, k / 8)));
+  };
+  return {cut(k0), cut(k1)};
+}
+
+// The backward's workspace past the header.
+struct BackwardLayout {
+  size_t grad, dx, dw, pad_x, pad_w, total;
+};
+BackwardLayout backward_layout(const moe_ce_problem* p) {
+  const size_t T = static_cast<size_t>(p->T), H = static_cast<size_t>(p->H);
   const int rows = piece_rows(p);
-  return kCeHeader + up(2 * T * rows) + (rows < p->V ? up(sizeof(float) * T * p->H) : 0) +
-         ce_pad_bytes(p, std::min(rows, p->V));
+  const size_t nv = static_cast<size_t>(std::min(rows, p->V));
+  const Splits sp = splits_of(p, rows);
+  BackwardLayout L;
+  size_t o = kCeHeader;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up(bytes);
+    return at;
+  };
+  L.grad = take(2 * T * rows);
+  L.dx = take(sizeof(float) * T * H * (sp.dx > 1 ? sp.dx : rows < p->V ? 1 : 0));
+  L.dw = take(sizeof(float) * nv * H * (sp.dw > 1 ? sp.dw : 0));
+  L.pad_x = take(padded(p) ? 2 * T * padded_width(p) : 0);
+  L.pad_w = take(padded(p) ? 2 * nv * padded_width(p) : 0);
+  L.total = o;
+  return L;
 }
 
 bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -808,6 +880,14 @@ cudaError_t operand(Matrix* m, const moe_ce_problem* p, const void* src, long ro
                        cols / 8);
 }
 
+cudaError_t join_splits(const float* acc, int splits, long n, float scale, const float* unit,
+                        void* out, cudaStream_t s, int* launches) {
+  ++*launches;
+  const long blocks = std::min<long>(8L * num_sms(), (n / 8 + 255) / 256);
+  return launch_kernel(ce_split_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                       1, acc, splits, n, scale, unit, static_cast<uint4*>(out));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -818,7 +898,7 @@ extern "C" size_t moe_linear_ce_workspace_size(const moe_ce_problem* p) {
 }
 
 extern "C" size_t moe_linear_ce_backward_workspace_size(const moe_ce_problem* p) {
-  return check_ce(p) == MOE_OK ? std::max(ce_forward_bytes(p), ce_backward_bytes(p)) : 0;
+  return check_ce(p) == MOE_OK ? std::max(ce_forward_bytes(p), backward_layout(p).total) : 0;
 }
 
 extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, const void* w,
@@ -882,11 +962,15 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
   if (rc != MOE_OK) return rc;
   if (!dx) return MOE_ERR_INVALID_ARG;
   if (!aligned(dx, 16) || !aligned(d_lse, 4)) return MOE_ERR_MISALIGNED;
-  if (ws_bytes < ce_backward_bytes(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const BackwardLayout L = backward_layout(p);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const int rows = piece_rows(p);
   const int pieces = ceil_div(p->V, rows);
-  uint8_t* base = static_cast<uint8_t*>(ws) + kCeHeader;
-  void* grad = base;  // [T, rows] bf16
+  const Splits sp = splits_of(p, rows);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  void* grad = base + L.grad;  // [T, rows] bf16
+  float* acc_dx = reinterpret_cast<float*>(base + L.dx);
+  float* acc_dw = reinterpret_cast<float*>(base + L.dw);
   CeParams k{};
   k.labels = labels;
   k.V = p->V;
@@ -894,11 +978,6 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
   k.lse = lse;
   k.d_loss = d_loss;
   k.d_lse = d_lse;
-  const size_t n_grad = up(2 * static_cast<size_t>(p->T) * rows);
-  k.acc = reinterpret_cast<float*>(base + n_grad);
-  uint8_t* pad = base + n_grad +
-                 (pieces > 1 ? up(sizeof(float) * static_cast<size_t>(p->T) * p->H) : 0);
-  uint8_t* pad_w = pad + up(2 * static_cast<size_t>(p->T) * padded_width(p));
   k.status = static_cast<uint32_t*>(ws);
   float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kUnitOffset);
   k.unit = unit;
@@ -907,14 +986,14 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
     return MOE_ERR_CUDA;
   ++launches;
   Matrix xm, wm;
-  if (operand(&xm, p, x, p->T, pad, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
+  if (operand(&xm, p, x, p->T, base + L.pad_x, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
   for (int i = 0; i < pieces; ++i) {
     const int v0 = i * rows, nv = std::min(rows, p->V - v0);
     const uint8_t* wp = static_cast<const uint8_t*>(w) + 2 * static_cast<size_t>(v0) * p->H;
     uint8_t* dwp = static_cast<uint8_t*>(dw) + 2 * static_cast<size_t>(v0) * p->H;
     k.v0 = v0;
     const int n_step = tile_columns(ceil_div(p->T, kTileM), nv, kUnitGrad);
-    if (operand(&wm, p, wp, nv, pad_w, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
+    if (operand(&wm, p, wp, nv, base + L.pad_w, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
     // padded to whole planes: the epilogue writes zeros there
     const Matrix gm{grad, p->T, ceil_div(nv, 64) * 64L, rows};
     CeMaps m{}, m1{};
@@ -928,11 +1007,24 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
         !make_gemm(&k.g[1], &m1, nv, p->H, p->T, kTileN, gm, true, xm, true) ||
         !make_map(&m1.out, dwp, nv, p->H, p->H, 32))
       return MOE_ERR_CUDA;
+    // a short last piece may have fewer stages than there are splits: it adds
+    // to the first ones' sums
+    k.g[0].splits = std::min(sp.dx, k.g[0].ksteps);
+    k.g[0].acc = acc_dx;
     k.g[0].add = i > 0;
-    k.g[0].keep = i + 1 < pieces;
+    k.g[0].keep = sp.dx > 1 || i + 1 < pieces;
+    k.g[1].splits = sp.dw;
+    k.g[1].acc = acc_dw;
+    k.g[1].keep = sp.dw > 1;
     if (launch_ce<CeMode::kProducts>(m, m1, k, s) != cudaSuccess) return MOE_ERR_CUDA;
     launches += 2;
+    if (sp.dw > 1 && join_splits(acc_dw, sp.dw, static_cast<long>(nv) * p->H, p->logit_scale, unit,
+                                 dwp, s, &launches) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
+  if (sp.dx > 1 && join_splits(acc_dx, sp.dx, static_cast<long>(p->T) * p->H, p->logit_scale, unit,
+                               dx, s, &launches) != cudaSuccess)
+    return MOE_ERR_CUDA;
   set_last_launch_count(launches);
   return MOE_OK;
 }

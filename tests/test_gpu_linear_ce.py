@@ -117,6 +117,20 @@ def test_several_pieces():
     check(8200, 264, 9000, seed=3, use_d_lse=True)
 
 
+@pytest.mark.parametrize("T,H,V", [(3, 64, 60000), (200, 1000, 50021), (300, 2056, 33000),
+                                   (6000, 128, 700), (9000, 72, 300), (2500, 512, 2500)])
+def test_products_split_along_k(T, H, V):
+    """dx of few tokens sums over a large vocabulary, dW of a small vocabulary over many
+    tokens: both cut into parts that are joined."""
+    check(T, H, V, use_d_lse=T % 2 == 0)
+
+
+def test_split_products_in_several_pieces():
+    """dx split in every piece, the last piece shorter than the others (one stage of it)."""
+    check(16500, 64, 4097, seed=4)
+    check(16400, 64, 61441, seed=5)
+
+
 @pytest.mark.parametrize("scale", [0.25, -1.5, 8.0])
 def test_logit_scale_and_lse_gradient(scale):
     check(100, 128, 700, scale=scale, use_d_lse=True)
