@@ -8,6 +8,12 @@
 // last and still is in L2.  HBM bound: the norm is needed before the first
 // output, so the tensors are read twice beyond what L2 keeps (129 MB).
 //
+// For few bytes the launches' latencies count: the second kernel reads its first
+// chunk before it waits for the first kernel (the gradients were complete
+// before that one began), and a chunk's tensor is found by a hint.  150 tensors
+// of 5 MB took 14.3 us with a binary search over the table, whose dependent
+// misses in the constant cache were most of it, and no early read.
+//
 // The tensors' table travels in the kernel parameters (no copy to the device,
 // nothing to go stale in a captured graph).  Chunks start at 16-byte
 // boundaries of the gradient: a tensor's leading elements before the first
@@ -28,7 +34,7 @@ namespace {
 
 constexpr int kChunkBytes = 32768;
 constexpr int kClipThreads = 256;
-constexpr int kClipUnroll = 4;       // 16-byte loads in flight per thread
+constexpr int kClipVecs = kChunkBytes / 16 / kClipThreads;  // per thread and chunk, all in flight
 constexpr int kClipBlocksPerSm = 8;  // 2048 threads
 constexpr int kMaxClipBlocks = 2048; // per launch; bounds the workspace
 constexpr size_t kClipHeader = 256;
@@ -36,10 +42,13 @@ constexpr size_t kClipHeader = 256;
 // takes a short table.
 constexpr int kSmallTable = 64, kMiddleTable = 256, kLargeTable = 1024;
 
+constexpr int kHints = 256;
 template <int kCap>
 struct GradTable {
   int n;
-  int chunk0[kCap + 1];  // first chunk of each tensor
+  int hint_shift;
+  uint16_t hint[kHints];  // the tensor of chunk i << hint_shift
+  int chunk0[kCap + 1];   // first chunk of each tensor
   const void* grad[kCap];
   void* out[kCap];
   long numel[kCap];      // sign bit: fp32
@@ -56,11 +65,8 @@ struct Chunk {
 
 template <int kCap>
 __device__ __forceinline__ Chunk chunk_at(const GradTable<kCap>& t, int c) {
-  int lo = 0, hi = t.n - 1;  // the last tensor whose first chunk is <= c
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.chunk0[mid] <= c) lo = mid; else hi = mid - 1;
-  }
+  int lo = t.hint[c >> t.hint_shift];  // at or before the last tensor whose first chunk is <= c
+  while (t.chunk0[lo + 1] <= c) ++lo;
   Chunk k;
   k.f32 = t.numel[lo] < 0;
   const long numel = t.numel[lo] & 0x7fffffffffffffffL;
@@ -110,58 +116,77 @@ __device__ __forceinline__ double square16_f64(uint4 v) {
   return s;
 }
 
+// What a thread takes of a chunk: every kClipThreads-th 16-byte vector behind
+// the leading elements, and one of the few elements round the vectors.
+struct Part {
+  uint4 x[kClipVecs];
+  int vecs;    // of the chunk
+  int single;  // index of the element, or -1
+  __device__ __forceinline__ void load(const Chunk& c) {
+    const int size = c.f32 ? 4 : 2, per = 16 / size;
+    vecs = static_cast<int>((c.n - c.lead) / per);
+    const uint4* v = reinterpret_cast<const uint4*>(c.grad + static_cast<long>(c.lead) * size);
+#pragma unroll
+    for (int u = 0; u < kClipVecs; ++u) {
+      const int i = u * kClipThreads + threadIdx.x;
+      if (i < vecs) x[u] = v[i];
+    }
+    const int tail = c.lead + vecs * per + static_cast<int>(threadIdx.x) - 32;
+    single = static_cast<int>(threadIdx.x) < c.lead       ? static_cast<int>(threadIdx.x)
+             : threadIdx.x >= 32 && tail < c.n ? tail
+                                               : -1;
+  }
+};
+
 // This thread's part of a chunk's sum of squares.
 template <bool kF32>
-__device__ __forceinline__ double chunk_squares(const Chunk& c) {
+__device__ __forceinline__ double part_squares(const Chunk& c, const Part& p) {
   using T = typename std::conditional<kF32, float, Bf16>::type;
-  constexpr int kPer = 16 / sizeof(T);
-  const T* g = reinterpret_cast<const T*>(c.grad);
-  const long vecs = (c.n - c.lead) / kPer;
-  const uint4* v = reinterpret_cast<const uint4*>(g + c.lead);
-  const long tail = c.lead + vecs * kPer;
   float s = 0.f;
-  long i = threadIdx.x;
-  for (; i + (kClipUnroll - 1) * kClipThreads < vecs; i += kClipUnroll * kClipThreads) {
-    uint4 x[kClipUnroll];
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) x[u] = load16(v + i + u * kClipThreads);
-#pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) s += square16<kF32>(x[u]);
-  }
-  for (; i < vecs; i += kClipThreads) s += square16<kF32>(load16(v + i));
-  // the elements round the vectors: fewer than 8 on either side
-  float e = 0.f;
-  if (threadIdx.x < c.lead) e = to_float(g[threadIdx.x]);
-  else if (threadIdx.x >= 32 && tail + (threadIdx.x - 32) < c.n)
-    e = to_float(g[tail + threadIdx.x - 32]);
+  for (int u = 0; u < kClipVecs; ++u)
+    if (u * kClipThreads + static_cast<int>(threadIdx.x) < p.vecs) s += square16<kF32>(p.x[u]);
+  const float e = p.single >= 0 ? to_float(reinterpret_cast<const T*>(c.grad)[p.single]) : 0.f;
   s = fmaf(e, e, s);
   if (s == 0.f || (s >= 0x1p-80f && s < __int_as_float(0x7f800000))) return s;
   double d = static_cast<double>(e) * e;  // out of fp32's comfortable range: again in fp64
-  for (i = threadIdx.x; i < vecs; i += kClipThreads) d += square16_f64<kF32>(load16(v + i));
+#pragma unroll 1
+  for (int i = threadIdx.x; i < p.vecs; i += kClipThreads)
+    d += square16_f64<kF32>(reinterpret_cast<const uint4*>(
+        c.grad + static_cast<long>(c.lead) * sizeof(T))[i]);
   return d;
 }
 
+// The block's sum, in thread 0 (fp64 is slow here: no thread does more of it
+// than it has to).
 __device__ __forceinline__ double block_sum(double x, double* s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
   __syncthreads();
-  x = 0.;
+  if (threadIdx.x < 32) {
+    x = threadIdx.x < kClipThreads / 32 ? s[threadIdx.x] : 0.;
 #pragma unroll
-  for (int i = 0; i < kClipThreads / 32; ++i) x += s[i];
+    for (int o = kClipThreads / 64; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  }
   return x;
 }
 
 template <int kCap>
 __global__ void __launch_bounds__(kClipThreads)
 grad_norm_kernel(const __grid_constant__ GradTable<kCap> t, double* __restrict__ part) {
-  pdl_enter();
   __shared__ double s[kClipThreads / 32];
   const int chunks = t.chunk0[t.n];
   double sum = 0.;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Chunk k = chunk_at(t, c);
-    sum += k.f32 ? chunk_squares<true>(k) : chunk_squares<false>(k);
+  int c = blockIdx.x;
+  Chunk k;
+  if (c < chunks) k = chunk_at(t, c);  // parameters only
+  pdl_enter();
+  for (; c < chunks; c += gridDim.x) {
+    if (c != static_cast<int>(blockIdx.x)) k = chunk_at(t, c);
+    Part x;
+    x.load(k);
+    sum += k.f32 ? part_squares<true>(k, x) : part_squares<false>(k, x);
   }
   sum = block_sum(sum, s);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
@@ -178,9 +203,8 @@ __device__ __forceinline__ uint4 scale16(uint4 v, float f) {
 }
 
 template <bool kF32>
-__device__ __forceinline__ void chunk_scale(const Chunk& c, float f) {
+__device__ __forceinline__ void part_scale(const Chunk& c, const Part& p, float f) {
   using T = typename std::conditional<kF32, float, Bf16>::type;
-  constexpr int kPer = 16 / sizeof(T);
   const T* g = reinterpret_cast<const T*>(c.grad);
   T* o = reinterpret_cast<T*>(c.out);
   if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
@@ -188,47 +212,57 @@ __device__ __forceinline__ void chunk_scale(const Chunk& c, float f) {
     for (long i = threadIdx.x; i < c.n; i += kClipThreads) from_float(o[i], to_float(g[i]) * f);
     return;
   }
-  const long vecs = (c.n - c.lead) / kPer;
-  const uint4* v = reinterpret_cast<const uint4*>(g + c.lead);
   uint4* w = reinterpret_cast<uint4*>(o + c.lead);
-  const long tail = c.lead + vecs * kPer;
-  long i = threadIdx.x;
-  for (; i + (kClipUnroll - 1) * kClipThreads < vecs; i += kClipUnroll * kClipThreads) {
-    uint4 x[kClipUnroll];
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) x[u] = load16(v + i + u * kClipThreads);
-#pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) __stcs(w + i + u * kClipThreads, scale16<kF32>(x[u], f));
+  for (int u = 0; u < kClipVecs; ++u) {
+    const int i = u * kClipThreads + threadIdx.x;
+    if (i < p.vecs) __stcs(w + i, scale16<kF32>(p.x[u], f));
   }
-  for (; i < vecs; i += kClipThreads) __stcs(w + i, scale16<kF32>(load16(v + i), f));
-  if (threadIdx.x < c.lead) from_float(o[threadIdx.x], to_float(g[threadIdx.x]) * f);
-  else if (threadIdx.x >= 32 && tail + (threadIdx.x - 32) < c.n)
-    from_float(o[tail + threadIdx.x - 32], to_float(g[tail + threadIdx.x - 32]) * f);
+  if (p.single >= 0) from_float(o[p.single], to_float(g[p.single]) * f);
 }
 
 template <int kCap>
 __global__ void __launch_bounds__(kClipThreads)
 grad_scale_kernel(const __grid_constant__ GradTable<kCap> t, const double* __restrict__ part,
                   int n_part, float grad_scale, float max_norm, float eps, float* norm_out) {
-  pdl_enter();
   __shared__ double s[kClipThreads / 32];
+  __shared__ float s_factor;
+  const int chunks = t.chunk0[t.n];
+  int c = chunks - 1 - static_cast<int>(blockIdx.x);
+  Chunk k;
+  Part x;
+  // The first chunk ahead of the wait: the kernel before this one only read
+  // the gradients, and began when whatever wrote them was complete.
+  if (c >= 0) {
+    k = chunk_at(t, c);
+    x.load(k);
+  }
+  pdl_enter();
   double sum = 0.;
   for (int i = threadIdx.x; i < n_part; i += kClipThreads) sum += part[i];
   sum = block_sum(sum, s);
-  const float norm = static_cast<float>(fabs(static_cast<double>(grad_scale)) * sqrt(sum));
-  float coef = max_norm / (norm + eps);
-  if (coef >= 1.f) coef = 1.f;  // a NaN stays
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
-    norm_out[0] = norm;
-    norm_out[1] = coef;
+  if (threadIdx.x == 0) {
+    const float norm = static_cast<float>(fabs(static_cast<double>(grad_scale)) * sqrt(sum));
+    float coef = max_norm / (norm + eps);
+    if (coef >= 1.f) coef = 1.f;  // a NaN stays
+    if (norm_out && blockIdx.x == 0) {
+      norm_out[0] = norm;
+      norm_out[1] = coef;
+    }
+    s_factor = grad_scale * coef;
   }
-  const float f = grad_scale * coef;
-  const int chunks = t.chunk0[t.n];
-  for (int c = chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
-    const Chunk k = chunk_at(t, c);
-    if (!k.out || (f == 1.f && k.out == k.grad)) continue;
-    if (k.f32) chunk_scale<true>(k, f);
-    else chunk_scale<false>(k, f);
+  __syncthreads();
+  const float f = s_factor;
+  while (c >= 0) {
+    if (k.out && !(f == 1.f && k.out == k.grad)) {
+      if (k.f32) part_scale<true>(k, x, f);
+      else part_scale<false>(k, x, f);
+    }
+    c -= gridDim.x;
+    if (c >= 0) {
+      k = chunk_at(t, c);
+      x.load(k);
+    }
   }
 }
 
@@ -252,6 +286,15 @@ void fill_table(GradTable<kCap>& t, const moe_grad_tensor* g, int n) {
                                     1, (g[i].numel - lead + per - 1) / per));
   }
   t.chunk0[n] = chunks;
+  t.hint_shift = 0;
+  while ((chunks >> t.hint_shift) >= kHints) ++t.hint_shift;
+  int owner = 0;
+  for (int i = 0; i < kHints; ++i) {
+    const long c = static_cast<long>(i) << t.hint_shift;
+    if (c >= chunks) break;
+    while (t.chunk0[owner + 1] <= c) ++owner;
+    t.hint[i] = static_cast<uint16_t>(owner);
+  }
 }
 
 int clip_blocks(int chunks) {
