@@ -9,15 +9,15 @@
 //      (the base of its part of the sorted list) and those inside, per warp
 //      and id, then places its tokens by a second scan.  A stable counting
 //      sort without a global histogram or any pass over another block's
-//      counts.  The block then knows which of its ids have no token and fills
-//      their rows with zeros, run by run: for a large vocabulary most of the
-//      bytes.
+//      counts.
 //   2. rows.  The sorted list is cut into pieces of 8 to 32 tokens, whatever their
 //      ids, one group of threads (8 columns a thread) per piece and 2048
 //      columns: every group has the same work, however the ids are
 //      distributed.  A row whose tokens all lie in the piece is written; the
 //      sums of an id that goes on before or behind it go to the workspace in
-//      fp32.
+//      fp32.  Among these blocks are those that fill the rows of ids without
+//      a token, run by run (for a large vocabulary most of the bytes): they
+//      keep HBM busy while the others wait for their loads.
 //   3. join.  Ids of several pieces: the pieces' sums are added in order.
 // Two forms of 2 that gave ids to warps or groups took 100 and 142 us at
 // T=16384 V=32000 H=4096 bf16 with word frequencies: the latencies of a few
@@ -76,32 +76,17 @@ embed_fwd_kernel(const int32_t* __restrict__ ids, const TT* __restrict__ table,
 }
 
 // ------------------------------------------------------------------ sort
-// Zeros to the n elements from `at` on, by one warp.
-template <typename T>
-__device__ __forceinline__ void fill_zero(T* at, long n, int lane) {
-  constexpr int kPer = 16 / sizeof(T);
-  const long lead = min(
-      n, static_cast<long>(((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / sizeof(T)));
-  const long vecs = (n - lead) / kPer, tail = lead + vecs * kPer;
-  uint4* v = reinterpret_cast<uint4*>(at + lead);
-  for (long i = lane; i < vecs; i += 32) v[i] = make_uint4(0, 0, 0, 0);
-  if (lane < lead) at[lane] = T{};  // fewer than 8 elements on either side
-  if (tail + lane < n) at[tail + lane] = T{};
-}
-
 // Block b: ids [b * range, (b + 1) * range).  Warp w takes the tokens
 // [w * per, (w + 1) * per) in both scans, so its placements keep token order.
 // count [kSortWarps][range] in shared memory.
-template <typename TT>
 __global__ void __launch_bounds__(32 * kSortWarps)
-embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int range,
+embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
                   int32_t* __restrict__ order, int32_t* __restrict__ sorted_id,
-                  int32_t* __restrict__ start, TT* __restrict__ d_table, uint32_t* status) {
+                  int32_t* __restrict__ start, uint32_t* status) {
   pdl_enter();
   extern __shared__ int32_t s_count[];
   __shared__ int32_t s_warp[kSortWarps];
   __shared__ int32_t s_below[kSortWarps];
-  __shared__ bool s_empty[kMaxRange];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int v0 = blockIdx.x * range, v1 = min(V, v0 + range), nv = v1 - v0;
   for (int i = threadIdx.x; i < kSortWarps * range; i += 32 * kSortWarps) s_count[i] = 0;
@@ -143,7 +128,6 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int rang
   }
   if (threadIdx.x < nv) {
     start[v0 + threadIdx.x] = base;
-    s_empty[threadIdx.x] = total == 0;
     if (v0 + static_cast<int>(threadIdx.x) == V - 1) start[V] = base + total;
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = s_count[w * range + threadIdx.x];
@@ -168,16 +152,6 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int rang
       sorted_id[at + rank] = id;
     }
     __syncwarp();
-  }
-  // warp w's share of the range's rows: runs of ids without a token
-  const int i0 = static_cast<int>(static_cast<long>(nv) * warp / kSortWarps);
-  const int i1 = static_cast<int>(static_cast<long>(nv) * (warp + 1) / kSortWarps);
-  for (int i = i0; i < i1;) {
-    if (!s_empty[i]) { ++i; continue; }
-    int j = i + 1;
-    while (j < i1 && s_empty[j]) ++j;
-    fill_zero(d_table + (static_cast<long>(v0) + i) * H, static_cast<long>(j - i) * H, lane);
-    i = j;
   }
 }
 
@@ -207,20 +181,56 @@ __device__ __forceinline__ void add_oct(float (&acc)[8], const Oct<T>& x) {
   for (int j = 0; j < 8; ++j) acc[j] += x.get(j);
 }
 
+// Zeros to the n elements from `at` on, by one warp.
+template <typename T>
+__device__ __forceinline__ void fill_zero(T* at, long n, int lane) {
+  constexpr int kPer = 16 / sizeof(T);
+  const long lead = min(
+      n, static_cast<long>(((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / sizeof(T)));
+  const long vecs = (n - lead) / kPer, tail = lead + vecs * kPer;
+  uint4* v = reinterpret_cast<uint4*>(at + lead);
+  for (long i = lane; i < vecs; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+  if (lane < lead) at[lane] = T{};  // fewer than 8 elements on either side
+  if (tail + lane < n) at[tail + lane] = T{};
+}
+
+// The rows of the ids [v0, v0 + kFillIds) that have no token, by one warp.
+constexpr int kFillIds = 8;
+template <typename TT>
+__device__ __forceinline__ void fill_rows(const int32_t* start, TT* d_table, long v0, int V, int H,
+                                          int lane) {
+  const int n = static_cast<int>(max(0L, min(static_cast<long>(kFillIds), V - v0)));
+  const bool empty = lane < n && __ldg(start + v0 + lane) == __ldg(start + v0 + lane + 1);
+  unsigned mask = __ballot_sync(0xffffffffu, empty);
+  while (mask) {
+    const int i = __ffs(mask) - 1, len = __ffs(~(mask >> i)) - 1;
+    fill_zero(d_table + (v0 + i) * H, static_cast<long>(len) * H, lane);
+    mask &= ~(((1u << len) - 1) << i);
+  }
+}
+
 // Piece q of the sorted list.  Its first id may have begun before it and its
 // last may go on behind it: their sums go to the slots 2 q (begun before,
-// whether it ends here or not) and 2 q + 1.
+// whether it ends here or not) and 2 q + 1.  Of the grid's columns of
+// blocks, piece_blocks take pieces and the others fill.
 template <typename TT, typename TO, bool kWide>
 __global__ void __launch_bounds__(kRowThreads, 3)
 embed_rows_kernel(const int32_t* __restrict__ order, const int32_t* __restrict__ sorted_id,
                   const int32_t* __restrict__ start, const TO* __restrict__ d_out,
                   TT* __restrict__ d_table, float* __restrict__ part, int V, int H, int pieces,
-                  int piece, int group_threads, float scale) {
+                  int piece, int group_threads, int piece_blocks, float scale) {
   pdl_enter();
   constexpr int kBatch = batch_of<TO, kWide>();
-  const Group g(H, group_threads);
   const int lane = threadIdx.x & 31;
-  const long q = static_cast<long>(blockIdx.x) * (kRowThreads / group_threads) + g.index;
+  // the two kinds of blocks in proportion, so that both are under way throughout
+  const long pb = static_cast<long>(blockIdx.x) * piece_blocks / gridDim.x;
+  if (static_cast<long>(blockIdx.x + 1) * piece_blocks / gridDim.x == pb) {
+    const long b = (blockIdx.x - pb) * gridDim.y + blockIdx.y;
+    fill_rows(start, d_table, (b * (kRowThreads / 32) + (threadIdx.x >> 5)) * kFillIds, V, H, lane);
+    return;
+  }
+  const Group g(H, group_threads);
+  const long q = pb * (kRowThreads / group_threads) + g.index;
   const long total = start[V], p0 = q * piece;
   if (q >= pieces || p0 >= total) return;  // whole warps
   const int m = static_cast<int>(min(static_cast<long>(piece), total - p0));
@@ -447,24 +457,26 @@ extern "C" int moe_embedding_backward(const moe_embed_problem* p, const int32_t*
     using TO = decltype(o);
     constexpr bool kWide = decltype(w)::value;
     cudaError_t e = cudaFuncSetAttribute(
-        embed_sort_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
         static_cast<int>(sizeof(int32_t) * kSortWarps * kMaxRange));
     if (e != cudaSuccess) return e;
-    e = launch_kernel(embed_sort_kernel<TT>, dim3(ceil_div(p->V, range)), dim3(32 * kSortWarps),
-                      smem, s, 1, ids, p->T, p->V, p->H, range, order, sorted_id, start,
-                      static_cast<TT*>(d_table), static_cast<uint32_t*>(ws));
+    e = launch_kernel(embed_sort_kernel, dim3(ceil_div(p->V, range)), dim3(32 * kSortWarps), smem,
+                      s, 1, ids, p->T, p->V, range, order, sorted_id, start,
+                      static_cast<uint32_t*>(ws));
     if (e != cudaSuccess) return e;
     ++launches;
-    if (pieces == 0) return e;
+    const int piece_blocks = ceil_div(pieces, kRowThreads / group);
+    const int col_blocks = ceil_div(p->H, kRowCols);
+    const int fill_blocks = ceil_div(p->V, static_cast<long>(kRowThreads / 32 * kFillIds));
     e = launch_kernel(embed_rows_kernel<TT, TO, kWide>,
-                      dim3(ceil_div(pieces, kRowThreads / group), ceil_div(p->H, kRowCols)),
+                      dim3(piece_blocks + ceil_div(fill_blocks, col_blocks), col_blocks),
                       dim3(kRowThreads), 0, s, 1, static_cast<const int32_t*>(order),
                       static_cast<const int32_t*>(sorted_id), static_cast<const int32_t*>(start),
                       static_cast<const TO*>(d_out), static_cast<TT*>(d_table), part, p->V, p->H,
-                      pieces, piece, group, p->scale);
+                      pieces, piece, group, piece_blocks, p->scale);
     if (e != cudaSuccess) return e;
     ++launches;
-    if (pieces == 1) return e;  // nothing goes on into another piece
+    if (pieces <= 1) return e;  // nothing goes on into another piece
     ++launches;
     return launch_kernel(embed_join_kernel<TT, kWide>, dim3(pieces, ceil_div(p->H, kJoinCols)),
                          dim3(64 * kJoinRuns), 0, s, 1, static_cast<const int32_t*>(sorted_id),
