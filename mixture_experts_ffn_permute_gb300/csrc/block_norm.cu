@@ -43,7 +43,8 @@ struct NormParams {
   void* d_residual;
   void* d_branch;
   void* d_gate;  // token and element gates
-  float* part;   // backward: [blocks][2][H] column sums (w_pre, w_post)
+  float* part;   // backward: [blocks][2][part_ld] column sums (w_pre, w_post)
+  int part_ld;   // H, or (flat rows, whose column c lies at c + shift) with room for that
   long ld_branch, ld_residual, ld_residual_out, ld_normed;
   int T, H, gate_kind;
   float eps, offset, residual_scale, branch_scale, inv_h;
@@ -283,7 +284,7 @@ block_norm_bwd_kernel(const NormParams p) {
     }
   }
   if (!p.part) return;
-  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.H;
+  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.part_ld;  // ld = H here
   if (kWarp) {
 #pragma unroll
     for (int v = 0; v < kSteps; ++v)
@@ -317,24 +318,95 @@ block_norm_bwd_kernel(const NormParams p) {
 }
 
 // ------------------------------------------------------------------ streamed rows
-// The same rows and sums for many rows of wide accesses: a block stays on its
-// SM, keeps its columns' weights in registers and copies the rows to come into
-// shared memory (cp.async, every warp its own octets) while it works on the
-// present one, so that the two row sums' barriers do not leave HBM idle.  The
+// The same rows and sums by blocks that stay on their SM: a block keeps its
+// columns' weights in registers and copies the rows to come into shared memory
+// (cp.async; rows of wide accesses: every warp its own octets) while it works
+// on the present one, so that the two row sums' barriers do not leave HBM
+// idle.  The
 // phases read their octets from shared memory again rather than hold them,
 // and compute in packed pairs of fp32: the backward is otherwise bound by the
 // issue of instructions (70 a element of a first version took it to 63 us at
 // T=4096 H=4096 bf16).
 constexpr int kMaxDepth = 4;  // rows in shared memory, the present one among them
 
+// One tensor's part of a row in shared memory.
+template <typename T, int kSteps>
+__host__ __device__ constexpr uint32_t slot_bytes(int n) {
+  return static_cast<uint32_t>(kSteps * n * oct_align<T>());
+}
+
+// The two forms of the rows.  kWide: every row starts on an octet (any row
+// stride).  Otherwise the rows are dense, of any width, and taken as octets of
+// the whole tensor (rowwise.cuh); the blocks' row stride is a multiple of 8, so
+// that a block's shift, and with it the columns of a thread, stays the same.
+template <bool kWide>
+__device__ __forceinline__ int first_col(int v, int tid, int n, int shift) {
+  return (v * n + tid) * 8 - (kWide ? 0 : shift);
+}
+template <bool kWide>
+__device__ __forceinline__ int row_shift(int H) {
+  return kWide ? 0 : static_cast<int>(static_cast<long>(blockIdx.x) * H & 7);
+}
+
+template <typename T, int kSteps, bool kWide>
+struct Rows {
+  const T* base;
+  long ld;
+  __device__ __forceinline__ void copy(uint32_t slot, long r, const NormParams& p, int tid, int n,
+                                       int shift) const {
+    const T* row = base + r * ld;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v) {
+      const uint32_t step = slot + v * n * oct_align<T>();
+      const int c = first_col<kWide>(v, tid, n, shift);
+      if (kWide) oct_copy(step, row, c, tid, p.H);
+      else flat_copy(step, row, c, tid, p.H, base + static_cast<long>(p.T) * p.H);
+    }
+  }
+  // for a step inside the row
+  __device__ __forceinline__ void read(Oct<T>& o, uint32_t slot, int v, int tid, int n, int H,
+                                       int shift) const {
+    oct_read(o, slot + v * n * oct_align<T>(), tid);
+    if (!kWide) {
+      const int c = first_col<kWide>(v, tid, n, shift);
+      if (!oct_whole(c, H)) oct_mask(o, c, H);
+    }
+  }
+};
+template <bool kWide, typename T>
+__device__ __forceinline__ void store_pairs(const Pair (&x)[4], T* row, int c, int H) {
+  if (kWide || oct_whole(c, H)) {
+    Oct<T> o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.set_pair(i, x[i]);
+    o.store(row + c);
+  } else {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= 0 && c + j < H) from_float(row[c + j], f[j]);
+  }
+}
+// Makes the present row readable and starts the copy of the row that takes the
+// place of the one before it.
+template <typename F>
+__device__ __forceinline__ void next_row(int depth, F&& fetch_next) {
+  __syncwarp();  // the slot that is filled now has been read by the whole warp
+  fetch_next();
+  copy_async_wait(depth - 1);
+  __syncwarp();
+}
+
 // scale * (weight + offset), times the gate's channel where that is its kind,
 // of this thread's columns
+template <bool kWide>
 __device__ __forceinline__ void load_weights(Pair (&w)[4], const NormParams& p,
-                                             const WeightPtr& ptr, bool gated, float scale, int v,
-                                             int tid, int n) {
+                                             const WeightPtr& ptr, bool gated, float scale, int c) {
   float x[8];
   if (ptr.p) {
-    load_weight8<true>(x, ptr, 0, v, tid, n, p.H);
+    load_weight_cols(x, ptr, 0, c, p.H, kWide);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = scale * (x[j] + p.offset);
   } else {
@@ -343,7 +415,7 @@ __device__ __forceinline__ void load_weights(Pair (&w)[4], const NormParams& p,
   }
   if (gated && p.gate_kind == MOE_GATE_CHANNEL) {
     float g[8];
-    load_weight8<true>(g, p.gate, 0, v, tid, n, p.H);
+    load_weight_cols(g, p.gate, 0, c, p.H, kWide);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= g[j];
   }
@@ -351,43 +423,39 @@ __device__ __forceinline__ void load_weights(Pair (&w)[4], const NormParams& p,
   for (int i = 0; i < 4; ++i) w[i] = pair_of(x[2 * i], x[2 * i + 1]);
 }
 
-__device__ __forceinline__ void load_gate(Pair (&w)[4], const NormParams& p, long row, int v,
-                                          int tid, int n) {
+__device__ __forceinline__ void load_gate(Pair (&w)[4], const NormParams& p, long row, int c) {
   float x[8];
-  load_weight8<true>(x, p.gate, row * p.H, v, tid, n, p.H);
+  load_weight_cols(x, p.gate, row * p.H, c, p.H, true);  // octets of the tensor in both forms
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pair_of(x[2 * i], x[2 * i + 1]);
 }
 
 // kPlain: branch, w_post and w_pre given, no gate or a channel gate; the
 // general form decides by the row.
-template <typename TB, typename TR, int kSteps, bool kPlain>
+template <typename TB, typename TR, int kSteps, bool kPlain, bool kWide>
 __global__ void __launch_bounds__(1024 / kSteps, 1)
 block_norm_fwd_stream_kernel(const NormParams p, int depth) {
   pdl_enter();
   __shared__ float s_sum[2][32];
   extern __shared__ __align__(16) uint8_t s_rows[];
   const int tid = threadIdx.x, n = blockDim.x;
-  const uint32_t yb = n * oct_align<TB>(), rb = n * oct_align<TR>();  // bytes of a step
-  const uint32_t row_bytes = kSteps * (yb + rb), ring = smem_u32(s_rows);
+  const uint32_t at_r = slot_bytes<TB, kSteps>(n);
+  const uint32_t row_bytes = at_r + slot_bytes<TR, kSteps>(n), ring = smem_u32(s_rows);
+  const Rows<TB, kSteps, kWide> rows_y{static_cast<const TB*>(p.branch), p.ld_branch};
+  const Rows<TR, kSteps, kWide> rows_r{static_cast<const TR*>(p.residual), p.ld_residual};
   const bool has_branch = kPlain || p.branch != nullptr;
   const bool post = kPlain || p.w_post.p != nullptr, pre = kPlain || p.normed != nullptr;
   const bool token = !kPlain && p.gate_kind == MOE_GATE_TOKEN;
   const bool element = !kPlain && p.gate_kind == MOE_GATE_ELEMENT;
-  bool in[kSteps];
+  const int shift = row_shift<kWide>(p.H);
+  bool in[kSteps];  // steps inside the row
 #pragma unroll
-  for (int v = 0; v < kSteps; ++v) in[v] = oct_col<true>(v, 0, tid, n) < p.H;
+  for (int v = 0; v < kSteps; ++v) in[v] = oct_inside(first_col<kWide>(v, tid, n, shift), p.H);
   auto fetch = [&](long row, int slot) {
     if (row < p.T) {
       const uint32_t at = ring + slot * row_bytes;
-#pragma unroll
-      for (int v = 0; v < kSteps; ++v) {
-        const int c = oct_col<true>(v, 0, tid, n);
-        if (has_branch)
-          oct_copy(at + v * yb, static_cast<const TB*>(p.branch) + row * p.ld_branch, c, tid, p.H);
-        oct_copy(at + kSteps * yb + v * rb,
-                 static_cast<const TR*>(p.residual) + row * p.ld_residual, c, tid, p.H);
-      }
+      if (has_branch) rows_y.copy(at, row, p, tid, n, shift);
+      rows_r.copy(at + at_r, row, p, tid, n, shift);
     }
     copy_async_commit();
   };
@@ -396,16 +464,16 @@ block_norm_fwd_stream_kernel(const NormParams p, int depth) {
   Pair w_post[kSteps][4], w_pre[kSteps][4];
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
-    load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
-    load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
+    load_weights<kWide>(w_post[v], p, p.w_post, true, p.branch_scale,
+                        first_col<kWide>(v, tid, n, shift));
+    load_weights<kWide>(w_pre[v], p, p.w_pre, false, 1.f, first_col<kWide>(v, tid, n, shift));
   }
   const Pair rscale = pair_of(p.residual_scale, p.residual_scale);
   int slot = 0, sums = 0;  // the row sums' two buffers alternate
   for (long row = blockIdx.x; row < p.T; row += stride) {
-    __syncwarp();  // the slot that is filled now has been read by the whole warp
-    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
-    copy_async_wait(depth - 1);
-    __syncwarp();
+    next_row(depth, [&]() {
+      fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    });
     const uint32_t at = ring + slot * row_bytes;
     slot = slot + 1 == depth ? 0 : slot + 1;
     Pair x[kSteps][4];  // residual_out, unrounded
@@ -417,7 +485,7 @@ block_norm_fwd_stream_kernel(const NormParams p, int depth) {
         for (int v = 0; v < kSteps; ++v) {
           if (!in[v]) continue;
           Oct<TB> y;
-          oct_read(y, at + v * yb, tid);
+          rows_y.read(y, at, v, tid, n, p.H, shift);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc = pair_fma(y.pair(i), y.pair(i), acc);
         }
@@ -431,31 +499,30 @@ block_norm_fwd_stream_kernel(const NormParams p, int depth) {
       for (int v = 0; v < kSteps; ++v) {
         if (!in[v]) continue;
         Oct<TB> y;
-        Oct<TR> r, o;
-        oct_read(y, at + v * yb, tid);
-        oct_read(r, at + kSteps * yb + v * rb, tid);
+        Oct<TR> r;
+        rows_y.read(y, at, v, tid, n, p.H, shift);
+        rows_r.read(r, at + at_r, v, tid, n, p.H, shift);
         Pair w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = pair_mul(sc, w_post[v][i]);
         if (element) {
           Pair g[4];
-          load_gate(g, p, row, v, tid, n);
+          load_gate(g, p, row, first_col<kWide>(v, tid, n, shift));
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = pair_mul(w[i], g[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[v][i] = pair_fma(rscale, r.pair(i), pair_mul(w[i], y.pair(i)));
-          o.set_pair(i, x[v][i]);
         }
-        o.store(orow + oct_col<true>(v, 0, tid, n));
+        store_pairs<kWide>(x[v], orow, first_col<kWide>(v, tid, n, shift), p.H);
       }
     } else {
 #pragma unroll
       for (int v = 0; v < kSteps; ++v) {
         if (!in[v]) continue;
         Oct<TR> r;
-        oct_read(r, at + kSteps * yb + v * rb, tid);
+        rows_r.read(r, at + at_r, v, tid, n, p.H, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[v][i] = r.pair(i);
       }
@@ -476,51 +543,49 @@ block_norm_fwd_stream_kernel(const NormParams p, int depth) {
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
       if (!in[v]) continue;
-      Oct<TB> o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o.set_pair(i, pair_mul(x[v][i], pair_mul(rs, w_pre[v][i])));
-      o.store(nrow + oct_col<true>(v, 0, tid, n));
+      for (int i = 0; i < 4; ++i) x[v][i] = pair_mul(x[v][i], pair_mul(rs, w_pre[v][i]));
+      store_pairs<kWide>(x[v], nrow, first_col<kWide>(v, tid, n, shift), p.H);
     }
   }
   copy_async_wait(0);
 }
 
 // kPlain: every input given, no gate or a channel gate.
-template <typename TB, typename TR, int kSteps, bool kPlain>
+template <typename TB, typename TR, int kSteps, bool kPlain, bool kWide>
 __global__ void __launch_bounds__(1024 / kSteps, 1)
 block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   pdl_enter();
   __shared__ float s_sum[2][3 * 32];
   extern __shared__ __align__(16) uint8_t s_rows[];
   const int tid = threadIdx.x, n = blockDim.x;
-  const uint32_t bb = n * oct_align<TB>(), rb = n * oct_align<TR>();  // bytes of a step
-  const uint32_t row_bytes = 2 * kSteps * (bb + rb), ring = smem_u32(s_rows);
+  const uint32_t bb = slot_bytes<TB, kSteps>(n);
+  const uint32_t rb = slot_bytes<TR, kSteps>(n);
+  const uint32_t row_bytes = 2 * (bb + rb), ring = smem_u32(s_rows);
   // a row's parts in shared memory
-  const uint32_t at_y = 0, at_dn = kSteps * bb, at_r = 2 * kSteps * bb, at_dr = at_r + kSteps * rb;
+  const uint32_t at_y = 0, at_dn = bb, at_r = 2 * bb, at_dr = at_r + rb;
+  const Rows<TB, kSteps, kWide> rows_y{static_cast<const TB*>(p.branch), p.ld_branch};
+  const Rows<TB, kSteps, kWide> rows_dn{static_cast<const TB*>(p.d_normed), p.ld_normed};
+  const Rows<TR, kSteps, kWide> rows_r{static_cast<const TR*>(p.residual), p.ld_residual_out};
+  const Rows<TR, kSteps, kWide> rows_dr{static_cast<const TR*>(p.d_residual_out),
+                                        p.ld_residual_out};
   const bool has_branch = kPlain || p.branch != nullptr, post = kPlain || p.w_post.p != nullptr;
   const bool pre = kPlain || p.d_normed != nullptr, later = kPlain || p.d_residual_out != nullptr;
   const bool token = !kPlain && p.gate_kind == MOE_GATE_TOKEN;
   const bool element = !kPlain && p.gate_kind == MOE_GATE_ELEMENT;
-  bool in[kSteps];
+  const int shift = row_shift<kWide>(p.H);
+  bool in[kSteps];  // steps inside the row
 #pragma unroll
-  for (int v = 0; v < kSteps; ++v) in[v] = oct_col<true>(v, 0, tid, n) < p.H;
+  for (int v = 0; v < kSteps; ++v) in[v] = oct_inside(first_col<kWide>(v, tid, n, shift), p.H);
   auto fetch = [&](long row, int slot) {
     if (row < p.T) {
       const uint32_t at = ring + slot * row_bytes;
-      const TB* y = static_cast<const TB*>(p.branch) + row * p.ld_branch;
-      const TB* dn = static_cast<const TB*>(p.d_normed) + row * p.ld_normed;
-      const TR* r = static_cast<const TR*>(p.residual) + row * p.ld_residual_out;
-      const TR* dr = static_cast<const TR*>(p.d_residual_out) + row * p.ld_residual_out;
-#pragma unroll
-      for (int v = 0; v < kSteps; ++v) {
-        const int c = oct_col<true>(v, 0, tid, n);
-        if (pre) {
-          oct_copy(at + at_r + v * rb, r, c, tid, p.H);
-          oct_copy(at + at_dn + v * bb, dn, c, tid, p.H);
-        }
-        if (has_branch) oct_copy(at + at_y + v * bb, y, c, tid, p.H);
-        if (later) oct_copy(at + at_dr + v * rb, dr, c, tid, p.H);
+      if (pre) {
+        rows_r.copy(at + at_r, row, p, tid, n, shift);
+        rows_dn.copy(at + at_dn, row, p, tid, n, shift);
       }
+      if (has_branch) rows_y.copy(at + at_y, row, p, tid, n, shift);
+      if (later) rows_dr.copy(at + at_dr, row, p, tid, n, shift);
     }
     copy_async_commit();
   };
@@ -531,8 +596,9 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   Pair acc_pre[kSteps][4], acc_post[kSteps][4];
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
-    load_weights(w_pre[v], p, p.w_pre, false, 1.f, v, tid, n);
-    load_weights(w_post[v], p, p.w_post, true, p.branch_scale, v, tid, n);
+    load_weights<kWide>(w_pre[v], p, p.w_pre, false, 1.f, first_col<kWide>(v, tid, n, shift));
+    load_weights<kWide>(w_post[v], p, p.w_post, true, p.branch_scale,
+                        first_col<kWide>(v, tid, n, shift));
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc_pre[v][i] = acc_post[v][i] = 0;
   }
@@ -540,10 +606,9 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
   const Pair rscale = pair_of(res_scale, res_scale);
   int slot = 0, sums = 0;  // the row sums' two buffers alternate
   for (long row = blockIdx.x; row < p.T; row += stride) {
-    __syncwarp();  // the slot that is filled now has been read by the whole warp
-    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
-    copy_async_wait(depth - 1);
-    __syncwarp();
+    next_row(depth, [&]() {
+      fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    });
     const uint32_t at = ring + slot * row_bytes;
     slot = slot + 1 == depth ? 0 : slot + 1;
     Pair a0 = 0, a1 = 0, a2 = 0;  // sum r'^2, sum a r', sum y^2
@@ -553,8 +618,8 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
       if (pre) {
         Oct<TR> r;
         Oct<TB> dn;
-        oct_read(r, at + at_r + v * rb, tid);
-        oct_read(dn, at + at_dn + v * bb, tid);
+        rows_r.read(r, at + at_r, v, tid, n, p.H, shift);
+        rows_dn.read(dn, at + at_dn, v, tid, n, p.H, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           a0 = pair_fma(r.pair(i), r.pair(i), a0);
@@ -563,7 +628,7 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
       }
       if (post) {
         Oct<TB> y;
-        oct_read(y, at + at_y + v * bb, tid);
+        rows_y.read(y, at + at_y, v, tid, n, p.H, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a2 = pair_fma(y.pair(i), y.pair(i), a2);
       }
@@ -581,11 +646,10 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
       if (!in[v]) continue;
-      const int c = oct_col<true>(v, 0, tid, n);
-      Oct<TR> o;
+      const int c = first_col<kWide>(v, tid, n, shift);
       if (later) {
         Oct<TR> dr;
-        oct_read(dr, at + at_dr + v * rb, tid);
+        rows_dr.read(dr, at + at_dr, v, tid, n, p.H, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[v][i] = dr.pair(i);
       } else {
@@ -595,8 +659,8 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
       if (pre) {
         Oct<TR> r;
         Oct<TB> dn;
-        oct_read(r, at + at_r + v * rb, tid);
-        oct_read(dn, at + at_dn + v * bb, tid);
+        rows_r.read(r, at + at_r, v, tid, n, p.H, shift);
+        rows_dn.read(dn, at + at_dn, v, tid, n, p.H, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const Pair d = pair_mul(dn.pair(i), rs);
@@ -604,28 +668,29 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
           g[v][i] = pair_fma(r.pair(i), k2, pair_fma(d, w_pre[v][i], g[v][i]));
         }
       }
+      Pair o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o.set_pair(i, pair_mul(rscale, g[v][i]));
-      o.store(static_cast<TR*>(p.d_residual) + row * p.ld_residual + c);
+      for (int i = 0; i < 4; ++i) o[i] = pair_mul(rscale, g[v][i]);
+      store_pairs<kWide>(o, static_cast<TR*>(p.d_residual) + row * p.ld_residual, c, p.H);
       if (!has_branch) continue;
       Oct<TB> y;
-      oct_read(y, at + at_y + v * bb, tid);
+      rows_y.read(y, at + at_y, v, tid, n, p.H, shift);
       if (element) {
         Pair gate[4];
-        load_gate(gate, p, row, v, tid, n);
-        float d[8];
+        load_gate(gate, p, row, c);
+        Pair dg[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const Pair gv = pair_mul(g[v][i], pair_mul(y.pair(i), ys));
-          unpair(pair_mul(gv, w_post[v][i]), d[2 * i], d[2 * i + 1]);
+          dg[i] = pair_mul(gv, w_post[v][i]);
           acc_post[v][i] = pair_fma(gv, gate[i], acc_post[v][i]);
           g[v][i] = pair_mul(g[v][i], pair_mul(gate[i], w_post[v][i]));
           sc = pair_fma(g[v][i], pair_mul(y.pair(i), ys), sc);
         }
         if (p.w_post.f32)
-          store_oct<true>(d, static_cast<float*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+          store_pairs<kWide>(dg, static_cast<float*>(p.d_gate) + row * p.H, c, p.H);
         else
-          store_oct<true>(d, static_cast<Bf16*>(p.d_gate) + row * p.H, v, tid, n, p.H);
+          store_pairs<kWide>(dg, static_cast<Bf16*>(p.d_gate) + row * p.H, c, p.H);
       } else {
         const Pair t = pair_of(tg, tg);
 #pragma unroll
@@ -654,111 +719,129 @@ block_norm_bwd_stream_kernel(const NormParams p, int depth) {
 #pragma unroll
     for (int v = 0; v < kSteps; ++v) {
       if (!in[v]) continue;
-      Oct<TB> y, o;
-      oct_read(y, at + at_y + v * bb, tid);
+      Oct<TB> y;
+      Pair o[4];
+      rows_y.read(y, at + at_y, v, tid, n, p.H, shift);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o.set_pair(i, pair_fma(y.pair(i), fy, pair_mul(g[v][i], fc)));
-      o.store(static_cast<TB*>(p.d_branch) + row * p.ld_branch + oct_col<true>(v, 0, tid, n));
+        o[i] = pair_fma(y.pair(i), fy, pair_mul(g[v][i], fc));
+      store_pairs<kWide>(o, static_cast<TB*>(p.d_branch) + row * p.ld_branch,
+                         first_col<kWide>(v, tid, n, shift), p.H);
     }
   }
   copy_async_wait(0);
   if (!p.part) return;
-  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.H;
+  // octets again: what a flat row's first and last ones hold outside it is not read
+  float* part = p.part + static_cast<long>(blockIdx.x) * 2 * p.part_ld;
 #pragma unroll
   for (int v = 0; v < kSteps; ++v) {
     if (!in[v]) continue;
-    const int c = oct_col<true>(v, 0, tid, n);
+    float* at = part + (v * n + tid) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      unpair(acc_pre[v][i], lo, hi);
-      reinterpret_cast<float2*>(part + c)[i] = make_float2(lo, hi);
-      unpair(acc_post[v][i], lo, hi);
-      reinterpret_cast<float2*>(part + p.H + c)[i] =
-          make_float2(p.branch_scale * lo, p.branch_scale * hi);
+    for (int i = 0; i < 4; i += 2) {
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        unpair(acc_pre[v][i + j], a[2 * j], a[2 * j + 1]);
+        unpair(acc_post[v][i + j], b[2 * j], b[2 * j + 1]);
+      }
+      reinterpret_cast<float4*>(at)[i / 2] = make_float4(a[0], a[1], a[2], a[3]);
+      reinterpret_cast<float4*>(at + p.part_ld)[i / 2] =
+          make_float4(p.branch_scale * b[0], p.branch_scale * b[1], p.branch_scale * b[2],
+                      p.branch_scale * b[3]);
     }
   }
 }
 
-// Sum of the blocks' column sums: 32 columns x 32 runs of blocks per CTA.
+// Sum of the blocks' column sums: 32 columns of w_pre's (blockIdx.y 0) or w_post's
+// x 32 runs of blocks per CTA.
 __global__ void __launch_bounds__(1024)
-block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, WeightPtr w_post,
-                       WeightPtr gate, int channel_gate, float offset, void* d_w_pre,
-                       void* d_w_post, void* d_gate) {
+block_norm_cols_kernel(const float* __restrict__ part, int blocks, int H, int ld, int flat,
+                       WeightPtr w_post, WeightPtr gate, int channel_gate, float offset,
+                       void* d_w_pre, void* d_w_post, void* d_gate) {
   pdl_enter();
-  __shared__ float s[2][32][32];
+  __shared__ float s[32][32];
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float a = 0.f, b = 0.f;
+  float a = 0.f;
   if (c < H) {
-#pragma unroll 4
+    const float* at = part + static_cast<long>(blockIdx.y) * ld + c;
+#pragma unroll 8
     for (int i = q; i < blocks; i += 32) {
-      const float* row = part + static_cast<long>(i) * 2 * H;
-      a += row[c];
-      b += row[H + c];
+      const int shift = flat ? static_cast<int>(static_cast<long>(i) * H & 7) : 0;
+      a += at[static_cast<long>(i) * 2 * ld + shift];
     }
   }
-  s[0][q][lane] = a;
-  s[1][q][lane] = b;
+  s[q][lane] = a;
   __syncthreads();
   if (q || c >= H) return;
-  a = b = 0.f;
+  a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    a += s[0][i][lane];
-    b += s[1][i][lane];
-  }
+  for (int i = 0; i < 32; ++i) a += s[i][lane];
   auto put = [&](void* d, float x) {
     if (!d) return;
     if (w_post.f32) static_cast<float*>(d)[c] = x;
     else from_float(static_cast<Bf16*>(d)[c], x);
   };
-  put(d_w_pre, a);
-  put(d_w_post, channel_gate ? gate.at(c) * b : b);
-  if (channel_gate) put(d_gate, (w_post.p ? w_post.at(c) + offset : 1.f) * b);
+  if (blockIdx.y == 0) {
+    put(d_w_pre, a);
+  } else {
+    put(d_w_post, channel_gate ? gate.at(c) * a : a);
+    if (channel_gate) put(d_gate, (w_post.p ? w_post.at(c) + offset : 1.f) * a);
+  }
 }
 
-// Threads and row mapping.  The forward gives a row to a warp up to 1024
-// columns (32 per lane: the row sums then need no barrier), the backward up to
-// 256 (its column sums would not fit the registers of more); wider rows take
-// a block of one step (8 columns) a thread up to 512 threads, else two steps.
-//
-// The streamed form takes rows of 16-byte accesses that a block would take,
-// up to 8192 columns, two steps a thread, where every SM has several rows to
-// work on and the ring holds at least two rows.  512 threads an SM in either
-// form: the backward's registers allow no more.
+// How a tensor's rows lie: every row on an octet; dense, the first one on an
+// octet; or anyhow.
+enum class Lay { kWide, kFlat, kAny };
+
+// Threads and row mapping.
+//   - A warp takes a row up to 1024 columns in the forward (32 per lane: the row
+//     sums then need no barrier), up to 256 in the backward (its column sums
+//     would not fit the registers of more).
+//   - Wider rows take a block.  Streamed (wide or flat rows up to 8192 columns):
+//     8 columns a thread in the forward, 16 in the backward, whose registers
+//     allow 512 threads an SM; all rows of the backward, and of the forward
+//     where every SM has several rows to work on.
+//   - Otherwise, 8 columns a thread up to 512 threads, else 16.
 struct Shape {
   bool warp, stream;
   int steps, threads, per_sm, depth;
 };
-constexpr int kStreamRows = 4;            // rows per SM from which rows are streamed
+constexpr int kStreamRows = 4;            // rows per SM from which the forward streams
 constexpr int kStreamBytes = 200 * 1024;  // shared memory of an SM for the rings
+constexpr int kFwdSteps = 1, kBwdSteps = 2;
 
-Shape norm_shape(const moe_norm_problem* p, bool bwd, bool wide) {
+Shape norm_shape(const moe_norm_problem* p, bool bwd, Lay lay) {
   const int H = p->H;
   if (H <= 256) return {true, false, 1, 256, 2, 0};
-  const bool warp = !bwd && H <= 1024;
-  if (wide && !warp && H <= 512 * 16 && p->T >= kStreamRows * num_sms()) {
-    Shape s{false, true, bwd ? 2 : 1, 0, 0, 0};
-    s.threads = ceil_div(ceil_div(H, 8 * s.steps), 32) * 32;
+  if (!bwd && H <= 1024) return {true, false, H <= 512 ? 2 : 4, 256, 0, 0};
+  const int span = H + (lay == Lay::kFlat ? 7 : 0);  // columns with the shift
+  if (lay != Lay::kAny && span <= 512 * 16 && (bwd || p->T >= kStreamRows * num_sms())) {
+    Shape s{false, true, bwd ? kBwdSteps : kFwdSteps, 0, 0, 0};
+    s.threads = ceil_div(ceil_div(span, 8 * s.steps), 32) * 32;
     s.per_sm = std::max(1, 1024 / s.steps / s.threads);
-    const int elt_bytes = (p->branch_dtype == MOE_DTYPE_F32 ? 4 : 2) +
-                          (p->residual_dtype == MOE_DTYPE_F32 ? 4 : 2);
-    const int row = s.threads * 8 * s.steps * elt_bytes * (bwd ? 2 : 1);
-    s.depth = std::min(kMaxDepth, kStreamBytes / s.per_sm / row);
-    if (s.depth >= 2) return s;
+    auto slot = [&](int dtype) {
+      return static_cast<int>(dtype == MOE_DTYPE_F32 ? slot_bytes<float, 1>(s.threads)
+                                                     : slot_bytes<Bf16, 1>(s.threads)) *
+             s.steps;
+    };
+    const int row = (slot(p->branch_dtype) + slot(p->residual_dtype)) * (bwd ? 2 : 1);
+    s.depth = std::max(1, std::min(kMaxDepth, kStreamBytes / s.per_sm / row));
+    return s;
   }
-  if (warp) return {true, false, H <= 512 ? 2 : 4, 256, 0, 0};
   const int steps = H <= 512 * 8 ? 1 : 2;
   const int threads = ceil_div(ceil_div(H, 8 * steps), 32) * 32;
   return {false, false, steps, threads, std::max(1, 512 / threads), 0};
 }
 
-// Blocks of the backward: what the SMs hold at once, and no more than one for
-// a row (eight rows for the warp form).
-int norm_blocks(int T, const Shape& s) {
-  return std::max(1, std::min(num_sms() * s.per_sm, s.warp ? ceil_div(T, 8) : T));
+// Blocks that stay: what the SMs hold at once, and no more than one for two rows
+// (every block leaves column sums to be added) but where that leaves SMs
+// without one, and eight rows for the warp form; a multiple of 8 for flat rows.
+int norm_blocks(int T, const Shape& s, Lay lay) {
+  const int rows = s.warp ? ceil_div(T, 8) : std::max(std::min(T, num_sms()), ceil_div(T, 2));
+  const int most = std::max(1, std::min(num_sms() * s.per_sm, rows));
+  return s.stream && lay == Lay::kFlat ? std::max(8, most / 8 * 8) : most;
 }
 
 int elt(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
@@ -777,23 +860,31 @@ int check_norm(const moe_norm_problem* p) {
   return MOE_OK;
 }
 
+int part_ld(int H, Lay lay) { return lay == Lay::kFlat ? ceil_div(H + 7, 8) * 8 : H; }
+
 size_t norm_part_bytes(const moe_norm_problem* p) {
-  // whichever form the tensors' alignment calls for
-  return sizeof(float) * 2 * static_cast<size_t>(p->H) *
-         std::max(norm_blocks(p->T, norm_shape(p, true, true)),
-                  norm_blocks(p->T, norm_shape(p, true, false)));
+  int blocks = 0;  // whichever form the tensors' alignment calls for
+  for (const Lay lay : {Lay::kWide, Lay::kFlat, Lay::kAny})
+    blocks = std::max(blocks, norm_blocks(p->T, norm_shape(p, true, lay), lay));
+  return sizeof(float) * 2 * static_cast<size_t>(part_ld(p->H, Lay::kFlat)) * blocks;
 }
 
 constexpr size_t kNormHeader = 256;  // status word
 
-// Collects the pointer checks and whether every row takes wide accesses.
+// Collects the pointer checks and how the rows lie.
 struct RowCheck {
-  bool ok = true, wide = true;
+  bool ok = true, octets = true, dense = true, wide;
+  int H;
+  explicit RowCheck(int h) : wide(h % 8 == 0), H(h) {}
   void add(const void* p, int dtype, long ld) {
     if (!p) return;
     if (!aligned(p, elt(dtype))) ok = false;
-    const int n = 8 * elt(dtype);  // eight elements in one access
-    if (!aligned(p, n) || (ld * elt(dtype)) % n != 0) wide = false;
+    if (!aligned(p, 8 * elt(dtype))) octets = false;  // eight elements in one access
+    if (ld % 8 != 0) wide = false;
+    if (ld != H) dense = false;
+  }
+  Lay lay() const {
+    return octets && wide ? Lay::kWide : octets && dense ? Lay::kFlat : Lay::kAny;
   }
 };
 
@@ -825,55 +916,59 @@ cudaError_t launch_norm_impl(const NormParams& k, int threads, int blocks, cudaS
                          dim3(blocks), dim3(threads), 0, s, 1, k);
 }
 
-template <bool kBwd, typename TB, typename TR>
-cudaError_t launch_norm_stream(const NormParams& k, const Shape& sh, cudaStream_t s) {
+template <bool kBwd, typename TB, typename TR, bool kWide>
+cudaError_t launch_norm_stream(const NormParams& k, const Shape& sh, int blocks, cudaStream_t s) {
   const bool plain = k.branch && k.w_post.p && k.w_pre.p && (!kBwd || k.d_residual_out) &&
                      (k.gate_kind == MOE_GATE_NONE || k.gate_kind == MOE_GATE_CHANNEL);
+  constexpr int kSteps = kBwd ? kBwdSteps : kFwdSteps;
   void (*kern)(NormParams, int);
   if constexpr (kBwd)
-    kern = plain ? block_norm_bwd_stream_kernel<TB, TR, 2, true>
-                 : block_norm_bwd_stream_kernel<TB, TR, 2, false>;
+    kern = plain ? block_norm_bwd_stream_kernel<TB, TR, kSteps, true, kWide>
+                 : block_norm_bwd_stream_kernel<TB, TR, kSteps, false, kWide>;
   else
-    kern = plain ? block_norm_fwd_stream_kernel<TB, TR, 1, true>
-                 : block_norm_fwd_stream_kernel<TB, TR, 1, false>;
-  const size_t smem = static_cast<size_t>(sh.depth) * sh.threads * 8 * sh.steps *
-                      (sizeof(TB) + sizeof(TR)) * (kBwd ? 2 : 1);
+    kern = plain ? block_norm_fwd_stream_kernel<TB, TR, kSteps, true, kWide>
+                 : block_norm_fwd_stream_kernel<TB, TR, kSteps, false, kWide>;
+  const size_t smem = static_cast<size_t>(sh.depth) * (kBwd ? 2 : 1) *
+                      (slot_bytes<TB, kSteps>(sh.threads) + slot_bytes<TR, kSteps>(sh.threads));
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kStreamBytes);
   if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(norm_blocks(k.T, sh)), dim3(sh.threads), smem, s, 1, k, sh.depth);
+  return launch_kernel(kern, dim3(blocks), dim3(sh.threads), smem, s, 1, k, sh.depth);
 }
 
-template <bool kBwd, typename TB, typename TR, bool kWide>
-cudaError_t launch_norm_shape(const NormParams& k, const Shape& sh, cudaStream_t s) {
+template <bool kBwd, typename TB, typename TR>
+cudaError_t launch_norm_shape(const NormParams& k, Lay lay, const Shape& sh, int blocks,
+                              cudaStream_t s) {
   const int n = sh.threads;
-  const int blocks = kBwd ? norm_blocks(k.T, sh) : sh.warp ? ceil_div(k.T, 8) : k.T;
-  if constexpr (kWide)
-    if (sh.stream) return launch_norm_stream<kBwd, TB, TR>(k, sh, s);
-  if (sh.warp) {
-    if (sh.steps == 1) return launch_norm_impl<kBwd, TB, TR, 1, 256, true, kWide>(k, n, blocks, s);
+  if (sh.stream)
+    return lay == Lay::kWide ? launch_norm_stream<kBwd, TB, TR, true>(k, sh, blocks, s)
+                             : launch_norm_stream<kBwd, TB, TR, false>(k, sh, blocks, s);
+  auto go = [&](auto w) {
+    constexpr bool kWide = decltype(w)::value;
+    if (sh.warp && sh.steps == 1)
+      return launch_norm_impl<kBwd, TB, TR, 1, 256, true, kWide>(k, n, blocks, s);
     if constexpr (!kBwd)
-      return sh.steps == 2 ? launch_norm_impl<kBwd, TB, TR, 2, 256, true, kWide>(k, n, blocks, s)
-                           : launch_norm_impl<kBwd, TB, TR, 4, 256, true, kWide>(k, n, blocks, s);
-  }
-  return sh.steps == 1 ? launch_norm_impl<kBwd, TB, TR, 1, 512, false, kWide>(k, n, blocks, s)
-         : n <= 512    ? launch_norm_impl<kBwd, TB, TR, 2, 512, false, kWide>(k, n, blocks, s)
-                       : launch_norm_impl<kBwd, TB, TR, 2, 1024, false, kWide>(k, n, blocks, s);
+      if (sh.warp)
+        return sh.steps == 2 ? launch_norm_impl<kBwd, TB, TR, 2, 256, true, kWide>(k, n, blocks, s)
+                             : launch_norm_impl<kBwd, TB, TR, 4, 256, true, kWide>(k, n, blocks, s);
+    if constexpr (!kBwd || !kWide) {  // the backward streams these where the rows are wide
+      if (sh.steps == 1) return launch_norm_impl<kBwd, TB, TR, 1, 512, false, kWide>(k, n, blocks, s);
+      if (n <= 512) return launch_norm_impl<kBwd, TB, TR, 2, 512, false, kWide>(k, n, blocks, s);
+    }
+    return launch_norm_impl<kBwd, TB, TR, 2, 1024, false, kWide>(k, n, blocks, s);
+  };
+  return lay == Lay::kWide ? go(std::true_type{}) : go(std::false_type{});
 }
 
 template <bool kBwd>
-cudaError_t launch_norm(const moe_norm_problem* p, const NormParams& k, bool wide, const Shape& sh,
-                        cudaStream_t s) {
+cudaError_t launch_norm(const moe_norm_problem* p, const NormParams& k, Lay lay, const Shape& sh,
+                        int blocks, cudaStream_t s) {
   const bool bf = p->branch_dtype == MOE_DTYPE_BF16, rf = p->residual_dtype == MOE_DTYPE_BF16;
-  auto go = [&](auto w) {
-    constexpr bool kWide = decltype(w)::value;
-    if (bf)
-      return rf ? launch_norm_shape<kBwd, Bf16, Bf16, kWide>(k, sh, s)
-                : launch_norm_shape<kBwd, Bf16, float, kWide>(k, sh, s);
-    return rf ? launch_norm_shape<kBwd, float, Bf16, kWide>(k, sh, s)
-              : launch_norm_shape<kBwd, float, float, kWide>(k, sh, s);
-  };
-  return wide ? go(std::true_type{}) : go(std::false_type{});
+  if (bf)
+    return rf ? launch_norm_shape<kBwd, Bf16, Bf16>(k, lay, sh, blocks, s)
+              : launch_norm_shape<kBwd, Bf16, float>(k, lay, sh, blocks, s);
+  return rf ? launch_norm_shape<kBwd, float, Bf16>(k, lay, sh, blocks, s)
+            : launch_norm_shape<kBwd, float, float>(k, lay, sh, blocks, s);
 }
 
 }  // namespace
@@ -897,8 +992,7 @@ extern "C" int moe_block_norm_forward(const moe_norm_problem* p, const void* bra
   if (!has_branch && !normed) return MOE_ERR_INVALID_ARG;
   NormParams k = norm_params(p);
   if (residual_out == residual && k.ld_residual != k.ld_residual_out) return MOE_ERR_INVALID_ARG;
-  RowCheck c;
-  c.wide = p->H % 8 == 0;
+  RowCheck c(p->H);
   c.add(branch, p->branch_dtype, k.ld_branch);
   c.add(normed, p->branch_dtype, k.ld_normed);
   c.add(residual, p->residual_dtype, k.ld_residual);
@@ -915,8 +1009,12 @@ extern "C" int moe_block_norm_forward(const moe_norm_problem* p, const void* bra
   k.gate = {gate, wf};
   k.residual_out = residual_out;
   k.normed = normed;
-  if (launch_norm<false>(p, k, c.wide, norm_shape(p, false, c.wide),
-                         static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  const Shape sh = norm_shape(p, false, c.lay());
+  const int blocks = sh.stream ? norm_blocks(p->T, sh, c.lay())
+                     : sh.warp ? ceil_div(p->T, 8)
+                               : p->T;
+  if (launch_norm<false>(p, k, c.lay(), sh, blocks, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
     return MOE_ERR_CUDA;
   set_last_launch_count(1);
   return MOE_OK;
@@ -968,8 +1066,7 @@ extern "C" int moe_block_norm_backward(const moe_norm_problem* p, const void* br
   NormParams k = norm_params(p);
   if (d_residual == d_residual_out && k.ld_residual != k.ld_residual_out)
     return MOE_ERR_INVALID_ARG;
-  RowCheck c;
-  c.wide = p->H % 8 == 0;
+  RowCheck c(p->H);
   c.add(branch, p->branch_dtype, k.ld_branch);
   c.add(d_branch, p->branch_dtype, k.ld_branch);
   c.add(d_normed, p->branch_dtype, k.ld_normed);
@@ -992,14 +1089,16 @@ extern "C" int moe_block_norm_backward(const moe_norm_problem* p, const void* br
   k.d_gate = d_gate;
   const bool cols = pre || w_post || channel;
   k.part = cols ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kNormHeader) : nullptr;
-  const Shape sh = norm_shape(p, true, c.wide);
-  const int blocks = norm_blocks(p->T, sh);
-  if (launch_norm<true>(p, k, c.wide, sh, s) != cudaSuccess) return MOE_ERR_CUDA;
+  const Shape sh = norm_shape(p, true, c.lay());
+  const int blocks = norm_blocks(p->T, sh, c.lay());
+  k.part_ld = part_ld(p->H, sh.stream ? c.lay() : Lay::kAny);
+  if (launch_norm<true>(p, k, c.lay(), sh, blocks, s) != cudaSuccess) return MOE_ERR_CUDA;
   ++launches;
   if (cols) {
-    if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32)), dim3(1024), 0, s, 1,
-                      static_cast<const float*>(k.part), blocks, p->H, k.w_post, k.gate,
-                      channel ? 1 : 0, p->weight_offset, d_w_pre, d_w_post, d_gate) != cudaSuccess)
+    const int flat = sh.stream && c.lay() == Lay::kFlat;
+    if (launch_kernel(block_norm_cols_kernel, dim3(ceil_div(p->H, 32), 2), dim3(1024), 0, s, 1,
+                      static_cast<const float*>(k.part), blocks, p->H, k.part_ld, flat, k.w_post,
+                      k.gate, channel ? 1 : 0, p->weight_offset, d_w_pre, d_w_post, d_gate) != cudaSuccess)
       return MOE_ERR_CUDA;
     ++launches;
   }

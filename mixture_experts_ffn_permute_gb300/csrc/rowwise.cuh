@@ -245,6 +245,57 @@ __device__ __forceinline__ void oct_read(Oct<float>& o, uint32_t step, int tid) 
   }
 }
 
+// Dense rows of any width: row r of [T, H] is the elements [r H, (r + 1) H) of one
+// sequence, and the octets are the sequence's, so that every access is wide and
+// aligned.  Octet k of the row starts at column 8 k - shift, shift = r H mod 8;
+// a row's first and last octets hold elements of the rows beside it, which are
+// masked after a read and left alone by a write.
+__device__ __forceinline__ bool oct_whole(int c, int H) { return c >= 0 && c + 8 <= H; }
+__device__ __forceinline__ bool oct_inside(int c, int H) { return c + 8 > 0 && c < H; }
+__device__ __forceinline__ void oct_mask(Oct<Bf16>& o, int c, int H) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < 0 || c + j >= H) o.w[j >> 1] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+}
+__device__ __forceinline__ void oct_mask(Oct<float>& o, int c, int H) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < 0 || c + j >= H) o.f[j] = 0.f;
+}
+// m elements of the row from column c on (the first of them may lie before it,
+// and the last behind the tensor's end: those are not copied) to shared memory.
+template <typename T>
+__device__ __forceinline__ void flat_piece(uint32_t dst, const T* row, int c, int m, int H,
+                                           const T* end) {
+  if (c + m <= 0 || c >= H) return;
+  if (row + c + m <= end) {
+    copy_async16(dst, row + c);
+    return;
+  }
+  for (int j = 0; j < m && c + j < H; ++j) {
+    if (c + j < 0) continue;
+    const uint32_t at = dst + j * static_cast<int>(sizeof(T));
+    if constexpr (sizeof(T) == 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(row[c + j].bits) : "memory");
+    else
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(row[c + j]) : "memory");
+  }
+}
+__device__ __forceinline__ void flat_copy(uint32_t step, const Bf16* row, int c, int tid, int H,
+                                          const Bf16* end) {
+  flat_piece(step + tid * 16, row, c, 8, H, end);
+}
+__device__ __forceinline__ void flat_copy(uint32_t step, const float* row, int c, int tid, int H,
+                                          const float* end) {
+  const int lane = tid & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // the layout of oct_copy
+    const int piece = h * 32 + lane;
+    flat_piece(step + (tid - lane) * 32 + (piece ^ ((piece >> 3) & 1)) * 16, row,
+               c - lane * 8 + piece * 4, 4, H, end);
+  }
+}
+
 // A weight vector whose type is known at run time only (bf16 or fp32).
 struct WeightPtr {
   const void* p;
@@ -282,6 +333,18 @@ __device__ __forceinline__ void load_weight8(float (&x)[8], const WeightPtr& w, 
       x[j] = c < H ? w.at(at0 + c) : 0.f;
     }
   }
+}
+
+// The weights at0 + [c, c + 8); zeros outside the row.  wide: a whole octet is
+// aligned.
+__device__ __forceinline__ void load_weight_cols(float (&x)[8], const WeightPtr& w, long at0,
+                                                 int c, int H, bool wide) {
+  if (wide && oct_whole(c, H)) {
+    load_weight8<true>(x, w, at0 + c, 0, 0, 1, 8);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = c + j >= 0 && c + j < H ? w.at(at0 + c + j) : 0.f;
 }
 
 // Sums over the threads of one row, every thread getting the totals.  kWarp:

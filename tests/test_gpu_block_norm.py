@@ -214,12 +214,56 @@ def test_streamed_rows(tb, tr, H):
     check(700, H, tb, tr, BF, "token", ld=H + 8)
 
 
+# rows that do not start on 16 bytes: dense ones are streamed as octets of the whole tensor
+@pytest.mark.parametrize("H", [257, 566, 1025, 1254, 2047, 5897, 8191])
+@pytest.mark.parametrize("tb,tr", list(itertools.product((BF, F32), repeat=2)))
+def test_streamed_narrow_rows(tb, tr, H):
+    check(613, H, tb, tr, F32, "channel", off=0.5)
+    check(1, H, tb, tr, BF, "element")
+    check(620, H, tb, tr, BF, "token", ld=H + 5)
+
+
+@pytest.mark.parametrize("shift,H", [(0, 1031), (0, 1026), (8, 1029), (1, 1032), (2, 1031),
+                                     (3, 1032), (5, 1032), (7, 1032)])
+def test_rows_of_a_shifted_tensor(shift, H):
+    """The tensors start `shift` elements behind a 32-byte boundary and end where the last eight
+    elements' place is not whole; what lies round them is NaN and stays."""
+    T = 701
+    s = inputs(T, H, BF, F32, F32, "channel")
+    p = problem(T, H, BF, F32, F32, "channel", 0.0, 0.9, 0.5)
+    whole = {}
+
+    def put(name, t):
+        whole[name] = torch.full((T * H + 16,), float("nan"), dtype=t.dtype, device=DEV)
+        view = whole[name][shift:shift + T * H].view(T, H)
+        return view.copy_(t)
+
+    d = {k: put(k, v) if v.dim() == 2 else v.to(DEV) for k, v in s.items()}
+    o = {k: put("o" + k, torch.zeros_like(s[k])) for k in ("branch", "residual")}
+    out, n = put("out", torch.zeros_like(s["residual"])), put("n", torch.zeros_like(s["branch"]))
+    kw = dict(branch=d["branch"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"])
+    moe.block_norm_forward(p, d["residual"], residual_out=out, normed=n, **kw)
+    want, mag, nw, n_mag = ref_forward(s, "channel", 0.0, 0.9, 0.5)
+    close(out, want, mag, F32)
+    close(n, nw, n_mag, BF)
+    w = {k: torch.empty_like(d[k]) for k in ("w_post", "gate", "w_pre")}
+    moe.block_norm_backward(p, d["residual"], o["residual"], moe.alloc_block_norm_workspace(p),
+                            d_normed=d["d_normed"], d_residual_out=d["d_residual_out"],
+                            d_branch=o["branch"], **kw, **{"d_" + k: v for k, v in w.items()})
+    for k, (want, mag) in ref_backward(s, "channel", 0.0, 0.9, 0.5).items():
+        got = o[k] if k in o else w[k]
+        close(got, want, mag, got.dtype, sums=T if want.dim() == 1 else 1)
+    for name, t in whole.items():
+        assert torch.isnan(t[:shift]).all() and torch.isnan(t[shift + T * H:]).all(), name
+
+
 @pytest.mark.parametrize("kind", ["none", "token", "element"])
 @pytest.mark.parametrize("post,pre,later", [(False, True, True), (True, False, True),
                                             (True, True, False), (False, False, True)])
 def test_streamed_rows_with_parts_left_out(kind, post, pre, later):
     check(1300, 1288, BF, F32, F32, kind, post=post, pre=pre, later=later)
     check(1300, 1288, BF, BF, F32, kind, post=post, pre=pre, later=later)
+    check(650, 1291, BF, F32, F32, kind, post=post, pre=pre, later=later)
 
 
 @pytest.mark.parametrize("kind", ["none", "channel", "token", "element"])
