@@ -778,12 +778,14 @@ int check_ce(const moe_ce_problem* p) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Rows whose length is not a multiple of 64 start off the lines that the copies
-// move, and every segment of theirs takes a line more.  With several m-tiles,
-// where W is read from L2 again and again, x and W are copied once to rows of
-// whole planes: T=777 H=1000 V=50021 forward 144 us against 92 us for H=1024
-// rows, T=4096 437 us against 252; the copy takes 30 us there.
-bool padded(const moe_ce_problem* p) { return p->H % 64 != 0 && p->T > kTileM; }
+// Rows whose length is not a multiple of 16 start off the 32-byte sectors, and
+// the copies move a sector more with every 128 bytes of theirs.  From three
+// m-tiles on, where W is read from L2 again and again, x and W are copied once
+// to rows of whole planes.  Both directions with / without the copy, V=50021:
+// H=1000 T=777 354 / 429 us, T=1024 395 / 471, T=600 298 / 321, T=300 257 / 255,
+// T=64 208 / 155; H=1008, whose rows start on sectors: T=600 297 / 257,
+// T=2048 641 / 620, T=4096 1178 / 1226.
+bool padded(const moe_ce_problem* p) { return p->H % 16 != 0 && p->T > 2 * kTileM; }
 int padded_width(const moe_ce_problem* p) { return ceil_div(p->H, 64) * 64; }
 
 size_t ce_pad_bytes(const moe_ce_problem* p, long w_rows) {
