@@ -79,7 +79,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // One GEMM: C[M, N] = A B^T over K, by pair tiles.
 struct Gemm {
-  int m_tiles, n_tiles, ksteps;  // ksteps: stages of 128
+  int m_tiles, n_tiles, ksteps;  // ksteps: stages of k_step
+  int k_step;                 // 128, or (both operands MN-major) K's even share
   int n_step;                 // columns per tile (a multiple of 32, <= 256)
   int M, N;                   // extents (rows and columns beyond are not written)
   bool a_mn, b_mn;            // operand stored [K, M] (resp. [K, N]): read MN-major
@@ -128,12 +129,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Descriptor of an MN-major operand: planes of 64 columns x 128 K rows with the
-// 128-byte swizzle; leading offset = the next 64 columns (one plane), stride
-// offset = 8 K rows.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
+// Descriptor of an MN-major operand: planes of 64 columns x k_step K rows with
+// the 128-byte swizzle; leading offset = the next 64 columns (one plane),
+// stride offset = 8 K rows.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr, int k_step) {
   return sw128_kmajor_desc(smem_addr) ^ (static_cast<uint64_t>(1u) << 16) ^
-         (static_cast<uint64_t>(kPlane >> 4) << 16);
+         (static_cast<uint64_t>(k_step * 8) << 16);
 }
 
 __device__ __forceinline__ void fence_async_shared() {
@@ -256,7 +257,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const int half = g.n_step / 2;
         const int col0 = n * g.n_step + static_cast<int>(rank) * half;
         const bool a_mn = g.a_mn, b_mn = g.b_mn, a_planes = g.a_planes, b_planes = g.b_planes;
-        const uint32_t a_plane = static_cast<uint32_t>(g.a_rows) * 128, b_plane = half * 128;
+        const uint32_t a_plane = static_cast<uint32_t>(a_mn ? g.k_step : g.a_rows) * 128;
+        const uint32_t b_plane = static_cast<uint32_t>(b_mn ? g.k_step : half) * 128;
         // one CTA's rows may hold the whole of a small M (the MMA then reads
         // whatever the shared memory behind them holds: rows of the
         // accumulator that nobody reads)
@@ -273,7 +275,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           const uint32_t bar = pair::mapa(smem_u32(&full[stage]), 0);
           uint8_t* a = sA + stage * a_stage;
           uint8_t* b = sB + stage * b_stage;
-          const int k0 = kb * kTileK;
+          const int k0 = kb * g.k_step;
           if (a_load) {
             const int c = a_mn ? row0 : k0, r = a_mn ? k0 : row0;
             if (a_planes) {
@@ -318,7 +320,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const Gemm& g = p.g[two];
         const bool a_mn = g.a_mn, b_mn = g.b_mn;
         split = tile / (g.m_tiles * g.n_tiles);
-        const int ksteps = g.k_begin(split + 1) - g.k_begin(split);
+        const int ksteps = g.k_begin(split + 1) - g.k_begin(split), k_step = g.k_step;
         const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(g.n_step)) |
                                (static_cast<uint32_t>(a_mn) << 15) |
                                (static_cast<uint32_t>(b_mn) << 16);
@@ -340,12 +342,14 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             tc_fence_after();
             const uint32_t a = smem_u32(sA + stage * a_stage);
             const uint32_t b = smem_u32(sB + stage * b_stage);
-            const uint64_t ad = a_mn ? mn_desc(a) : sw128_kmajor_desc(a);
-            const uint64_t bd = b_mn ? mn_desc(b) : sw128_kmajor_desc(b);
+            const uint64_t ad = a_mn ? mn_desc(a, k_step) : sw128_kmajor_desc(a);
+            const uint64_t bd = b_mn ? mn_desc(b, k_step) : sw128_kmajor_desc(b);
 #pragma unroll
-            for (int kk = 0; kk < kTileK / 16; ++kk)
+            for (int kk = 0; kk < kTileK / 16; ++kk) {
+              if (kk * 16 >= k_step) break;
               pair::mma(d_tmem, ad + (kk & 3) * as + (kk >> 2) * a4,
                         bd + (kk & 3) * bs + (kk >> 2) * b4, idesc, kb > k0 || kk != 0);
+            }
             pair::commit_both(&empty[stage]);
             if (++stage == n_stages) { stage = 0; phase ^= 1; }
           }
@@ -717,6 +721,10 @@ bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const 
   g->m_tiles = ceil_div(M, kTileM);
   g->n_tiles = ceil_div(N, n_step);
   g->ksteps = ceil_div(K, kTileK);
+  // A stage of MN-major operands can have any multiple of 16 along K: stages of
+  // equal depth leave no last one whose rows are mostly filled with zeros,
+  // which copies slowly.
+  g->k_step = a_mn && b_mn ? ceil_div(ceil_div(K, g->ksteps), 16) * 16 : kTileK;
   g->n_step = n_step;
   g->splits = 1;
   g->a_mn = a_mn;
@@ -728,8 +736,8 @@ bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const 
     return planes ? make_planes(m, x.p, x.rows, x.cols, x.ld, rows)
                   : make_map(m, x.p, x.rows, x.cols, x.ld, rows);
   };
-  return make(&maps->a, a, g->a_planes, g->a_rows) &&
-         make(&maps->b, b, g->b_planes, b_mn ? kTileK : n_step / 2);
+  return make(&maps->a, a, g->a_planes, a_mn ? g->k_step : g->a_rows) &&
+         make(&maps->b, b, g->b_planes, b_mn ? g->k_step : n_step / 2);
 }
 
 template <CeMode kMode>
