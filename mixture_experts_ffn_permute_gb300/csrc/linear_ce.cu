@@ -90,8 +90,9 @@ struct Gemm {
   bool add, keep;             // fp32 sums: add to acc, leave them in acc (else bf16 out)
   float* acc;                 // [splits][M][N]
   __host__ __device__ int tiles() const { return m_tiles * n_tiles * splits; }
+  // first stage of a split (splits are at most twice the CTA pairs: no overflow)
   __host__ __device__ int k_begin(int split) const {
-    return static_cast<int>(static_cast<long>(ksteps) * split / splits);
+    return splits == 1 ? split * ksteps : ksteps * split / splits;
   }
 };
 
@@ -144,8 +145,16 @@ __device__ __forceinline__ void fence_async_shared() {
 // Tile `i` of a GEMM: split by split, groups of kGroupM m-tiles sweep the
 // n-tiles.
 __device__ __forceinline__ void tile_of(const Gemm& g, int i, int& m, int& n, int& split) {
-  split = i / (g.m_tiles * g.n_tiles);
-  i -= split * (g.m_tiles * g.n_tiles);
+  split = 0;
+  if (g.splits > 1) {
+    split = i / (g.m_tiles * g.n_tiles);
+    i -= split * (g.m_tiles * g.n_tiles);
+  }
+  if (g.m_tiles == 1) {
+    m = 0;
+    n = i;
+    return;
+  }
   const int per = kGroupM * g.n_tiles;
   const int grp = i / per, within = i - grp * per;
   const int size = min(kGroupM, g.m_tiles - grp * kGroupM);
@@ -158,16 +167,18 @@ __device__ __forceinline__ void tile_of(const Gemm& g, int i, int& m, int& n, in
 // first `lead` tiles of g[1] while the others finish, the rest round-robin.
 struct Deal {
   int pair, pairs, mine0, rem, tiles0, tiles1, lead;
-  __device__ __forceinline__ Deal(const CeParams& p, int pair_, int pairs_) {
+  __device__ __forceinline__ Deal(const CeParams& p, int pair_, int pairs_, bool both) {
     pair = pair_;
     pairs = pairs_;
     tiles0 = p.g[0].tiles();
-    tiles1 = p.g[1].tiles();
+    tiles1 = both ? p.g[1].tiles() : 0;
     rem = tiles0 % pairs;
     mine0 = tiles0 / pairs + (pair < rem ? 1 : 0);
+    lead = 0;
+    if (!both) return;
     const int k0 = p.g[0].ksteps / max(1, p.g[0].splits);
     const int k1 = max(1, p.g[1].ksteps / max(1, p.g[1].splits));
-    lead = rem ? (k0 + k1 / 2) / k1 : 0;
+    if (rem) lead = (k0 + k1 / 2) / k1;
   }
   // tile number `i` of this pair: false past the last; `second`: of g[1]
   __device__ __forceinline__ bool at(int i, int& tile, bool& second) const {
@@ -176,6 +187,7 @@ struct Deal {
       tile = i * pairs + pair;
       return true;
     }
+    if (tiles1 == 0) return false;
     int j = i - mine0;
     if (pair >= rem) {
       if (j < lead) {
@@ -218,7 +230,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * 32 * epi_warps<kMode>());
+      mbar_init(&tempty[b], 2 * epi_warps<kMode>());  // one arrival per epilogue warp
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -237,7 +249,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
 
   // nothing above touches global memory
   pdl_enter();
-  const Deal deal(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
+  const Deal deal(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1),
+                  kMode == CeMode::kProducts);
   int tile, m, n, split;
   bool two;
 
@@ -267,7 +280,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const int k_first = g.k_begin(split), k_last = g.k_begin(split + 1);
         // with one m-tile every pair reads the same A: each starts elsewhere in
         // K, so that they do not all ask for the same lines at once
-        int kb = k_first + (g.m_tiles == 1 ? deal.pair % (k_last - k_first) : 0);
+        int kb = k_first;
+        if (g.m_tiles == 1) kb += deal.pair % (k_last - k_first);
         bool ok = true;
         for (int j = k_first; j < k_last; ++j) {
           if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
@@ -319,7 +333,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         if (*abort_flag) break;
         const Gemm& g = p.g[two];
         const bool a_mn = g.a_mn, b_mn = g.b_mn;
-        split = tile / (g.m_tiles * g.n_tiles);
+        split = g.splits > 1 ? tile / (g.m_tiles * g.n_tiles) : 0;
         const int ksteps = g.k_begin(split + 1) - g.k_begin(split), k_step = g.k_step;
         const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(g.n_step)) |
                                (static_cast<uint32_t>(a_mn) << 15) |
@@ -380,7 +394,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     // it has been read (the leader's barrier of this accumulator)
     auto release = [&]() {
       tc_fence_before();
-      pair::arrive_remote(tempty_leader + (seg & 1) * 8);
+      __syncwarp();
+      if (lane == 0) pair::arrive_remote(tempty_leader + (seg & 1) * 8);
       ++seg;
     };
     for (int i = 0; go && deal.at(i, tile, two); ++i) {
@@ -411,20 +426,26 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
       if (kMode == CeMode::kLse) {
         // this warp's half of the columns, up to 128 of a row per thread
         const int half = (warp - 2) >> 2, c0 = half * 128;
-        float z[4][32];
+        uint32_t z[4][32];  // fp32
         for (int k0 = 0; k0 < g.ksteps; k0 += kPromote) {
           if (!wait_full()) break;
           const uint32_t t_lane = t_quad + (seg & 1) * kTileN + c0;
+          if (warp_ok) {
+            __syncwarp();
+            if (k0 == 0) {  // all at once (columns past the tile's are not used)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (warp_ok && c0 + 32 * q < ncols) {
-              uint32_t a[32];
-              __syncwarp();
-              tmem_ld_32x32b_x32(t_lane + 32 * q, a);
+              for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_lane + 32 * q, z[q]);
               tmem_ld_wait();
+            } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                z[q][j] = k0 ? z[q][j] + __uint_as_float(a[j]) : __uint_as_float(a[j]);
+              for (int q = 0; q < 4; ++q) {
+                uint32_t a[32];
+                tmem_ld_32x32b_x32(t_lane + 32 * q, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  z[q][j] = __float_as_uint(__uint_as_float(z[q][j]) + __uint_as_float(a[j]));
+              }
             }
           }
           release();
@@ -438,21 +459,22 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
           if (label >= c && label < c + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c + j == label) p.label_logit[row] = p.scale * z[q][j];
+              if (c + j == label) p.label_logit[row] = p.scale * __uint_as_float(z[q][j]);
           }
-          float cm = mx;
+          // four chains each for the maximum and the sum
+          float v[32], cm[4] = {mx, mx, mx, mx}, s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            z[q][j] = j < left ? c2 * z[q][j] : -INFINITY;
-            cm = fmaxf(cm, z[q][j]);
+            v[j] = j < left ? c2 * __uint_as_float(z[q][j]) : -INFINITY;
+            cm[j & 3] = fmaxf(cm[j & 3], v[j]);
           }
+          const float m4 = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
           // ordinary rows: one rescaling a chunk; all -inf so far: the sum stays 0
-          if (cm != -INFINITY) {
-            float s = 0.f;
+          if (m4 != -INFINITY) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s += ex2(z[q][j] - cm);
-            sum = fmaf(sum, ex2(mx - cm), s);
-            mx = cm;
+            for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(v[j] - m4);
+            sum = fmaf(sum, ex2(mx - m4), (s4[0] + s4[1]) + (s4[2] + s4[3]));
+            mx = m4;
           }
         }
         if (row_ok) p.part[static_cast<long>(2 * n + half) * g.M + row] = make_float2(mx, sum);
@@ -472,16 +494,17 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             if (lane == 0) bulk_wait_group_read<kStagingBuffers - 1>();
             __syncwarp();
           }
+          __syncwarp();
+          uint32_t a[2][32];
+          tmem_ld_32x32b_x32(t_lane + c, a[0]);
+          tmem_ld_32x32b_x32(t_lane + c + 32, a[1]);
+          tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int cc = c + 32 * h;
-            __syncwarp();
-            uint32_t a[32];
-            tmem_ld_32x32b_x32(t_lane + cc, a);
-            tmem_ld_wait();
             float v[32];
 #pragma unroll
-            for (int i2 = 0; i2 < 32; ++i2) v[i2] = __uint_as_float(a[i2]);
+            for (int i2 = 0; i2 < 32; ++i2) v[i2] = __uint_as_float(a[h][i2]);
             if (kMode == CeMode::kGrad) {
               // columns past the vocabulary, up to the store's 64: zeros, which
               // the products read along K
