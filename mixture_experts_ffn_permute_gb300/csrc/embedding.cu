@@ -76,6 +76,15 @@ embed_fwd_kernel(const int32_t* __restrict__ ids, const TT* __restrict__ table,
 }
 
 // ------------------------------------------------------------------ sort
+// The ids of a lane's next kSortBatch tokens (32 apart; -1 past the end), all
+// under way at once.
+constexpr int kSortBatch = 8;
+__device__ __forceinline__ void load_ids(int (&id)[kSortBatch], const int32_t* ids, long t,
+                                         long end) {
+#pragma unroll
+  for (int u = 0; u < kSortBatch; ++u) id[u] = t + 32 * u < end ? __ldg(ids + t + 32 * u) : -1;
+}
+
 // Block b: ids [b * range, (b + 1) * range).  Warp w takes the tokens
 // [w * per, (w + 1) * per) in both scans, so its placements keep token order.
 // count [kSortWarps][range] in shared memory.
@@ -97,12 +106,15 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
   int32_t* mine = s_count + warp * range;
   int below = 0;
   bool bad = false;
-#pragma unroll 4
-  for (long t = t0 + lane; t < t1; t += 32) {
-    const int id = __ldg(ids + t);
-    below += id >= 0 && id < v0;
-    bad |= id >= V;
-    if (id >= v0 && id < v1) atomicAdd(&mine[id - v0], 1);  // integers: any order
+  for (long tb = t0; tb < t1; tb += 32 * kSortBatch) {
+    int id[kSortBatch];
+    load_ids(id, ids, tb + lane, t1);
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u) {
+      below += id[u] >= 0 && id[u] < v0;
+      bad |= id[u] >= V;
+      if (id[u] >= v0 && id[u] < v1) atomicAdd(&mine[id[u] - v0], 1);  // integers: any order
+    }
   }
   if (blockIdx.x == 0 && bad) record_status(status, kStatusIndex);
 #pragma unroll
@@ -136,22 +148,25 @@ embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int range,
     }
   }
   __syncthreads();
-  for (long tb = t0; tb < t1; tb += 32) {  // the whole warp stays together
-    const long t = tb + lane;
-    const int id = t < t1 ? __ldg(ids + t) : -1;
-    const bool hit = id >= v0 && id < v1;
-    const unsigned hits = __ballot_sync(0xffffffffu, hit);
-    if (!hits) continue;
-    if (hit) {
-      const unsigned same = __match_any_sync(hits, id);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      const int at = mine[id - v0];
-      __syncwarp(hits);
-      if (rank == 0) mine[id - v0] = at + __popc(same);
-      order[at + rank] = static_cast<int32_t>(t);
-      sorted_id[at + rank] = id;
+  for (long tb = t0; tb < t1; tb += 32 * kSortBatch) {  // the whole warp stays together
+    int id[kSortBatch];
+    load_ids(id, ids, tb + lane, t1);
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u) {
+      const bool hit = id[u] >= v0 && id[u] < v1;
+      const unsigned hits = __ballot_sync(0xffffffffu, hit);
+      if (!hits) continue;
+      if (hit) {
+        const unsigned same = __match_any_sync(hits, id[u]);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        const int at = mine[id[u] - v0];
+        __syncwarp(hits);
+        if (rank == 0) mine[id[u] - v0] = at + __popc(same);
+        order[at + rank] = static_cast<int32_t>(tb + 32 * u + lane);
+        sorted_id[at + rank] = id[u];
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
