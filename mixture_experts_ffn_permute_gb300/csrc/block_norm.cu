@@ -812,6 +812,10 @@ constexpr int kStreamRows = 4;            // rows per SM from which the forward 
 constexpr int kStreamBytes = 200 * 1024;  // shared memory of an SM for the rings
 constexpr int kFwdSteps = 1, kBwdSteps = 2;
 
+// Blocks that T rows are worth: every block of the backward leaves column sums
+// to be added, so one for two rows but where that leaves SMs without one.
+int stay_rows(int T) { return std::max(std::min(T, num_sms()), ceil_div(T, 2)); }
+
 Shape norm_shape(const moe_norm_problem* p, bool bwd, Lay lay) {
   const int H = p->H;
   if (H <= 256) return {true, false, 1, 256, 2, 0};
@@ -827,7 +831,13 @@ Shape norm_shape(const moe_norm_problem* p, bool bwd, Lay lay) {
              s.steps;
     };
     const int row = (slot(p->branch_dtype) + slot(p->residual_dtype)) * (bwd ? 2 : 1);
-    s.depth = std::max(1, std::min(kMaxDepth, kStreamBytes / s.per_sm / row));
+    // two rows in the ring at least, with fewer blocks an SM if need be, but two
+    // (fp32 backward: T=4096 H=2048 42.5 us with four blocks of one row, 39.7
+    // with three of two; T=8192 H=4096 129 us with two of one, 139 with one of
+    // three)
+    s.per_sm = std::max(std::min(s.per_sm, 2), std::min(s.per_sm, kStreamBytes / (2 * row)));
+    const int used = std::max(1, std::min(s.per_sm, ceil_div(stay_rows(p->T), num_sms())));
+    s.depth = std::max(1, std::min(kMaxDepth, kStreamBytes / used / row));
     return s;
   }
   const int steps = H <= 512 * 8 ? 1 : 2;
@@ -835,11 +845,10 @@ Shape norm_shape(const moe_norm_problem* p, bool bwd, Lay lay) {
   return {false, false, steps, threads, std::max(1, 512 / threads), 0};
 }
 
-// Blocks that stay: what the SMs hold at once, and no more than one for two rows
-// (every block leaves column sums to be added) but where that leaves SMs
-// without one, and eight rows for the warp form; a multiple of 8 for flat rows.
+// Blocks that stay: what the SMs hold at once, and no more than the rows are
+// worth (eight rows a block for the warp form); a multiple of 8 for flat rows.
 int norm_blocks(int T, const Shape& s, Lay lay) {
-  const int rows = s.warp ? ceil_div(T, 8) : std::max(std::min(T, num_sms()), ceil_div(T, 2));
+  const int rows = s.warp ? ceil_div(T, 8) : stay_rows(T);
   const int most = std::max(1, std::min(num_sms() * s.per_sm, rows));
   return s.stream && lay == Lay::kFlat ? std::max(8, most / 8 * 8) : most;
 }
