@@ -22,7 +22,9 @@
 // Two forms of 2 that gave ids to warps or groups took 100 and 142 us at
 // T=16384 V=32000 H=4096 bf16 with word frequencies: the latencies of a few
 // tokens an id do not overlap.
-// HBM bound: T rows read, V rows written.
+// HBM bound: T rows read, V rows written.  T=16384 V=32000 H=4096 bf16 with word
+// frequencies: 85 us (396 MB; 58 at HBM rate), of which the sort takes 10 and
+// the join 10; T=3001 V=50021 H=1001 fp32 45 us (212 MB; 31).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -345,8 +347,9 @@ int check_embed(const moe_embed_problem* p) {
   if (!p || p->T < 0 || p->V < 1 || p->H < 1) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(p->table_dtype) || !dtype_ok(p->out_dtype)) return MOE_ERR_INVALID_ARG;
   const long long slices = (p->H + kSlice - 1) / kSlice;
-  // block indices of the forward: tokens * slices / 8 warps
+  // a table no GPU holds; block indices of the forward: tokens * slices / 8 warps
   if (p->T > (1 << 28) || p->V > (1 << 28) || p->H > (1 << 20) ||
+      static_cast<long long>(p->V) * p->H > (1LL << 42) ||
       p->T * slices / kWarps >= (1LL << 31) - 2)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;

@@ -11,8 +11,10 @@
 // For few bytes the launches' latencies count: the second kernel reads its first
 // chunk before it waits for the first kernel (the gradients were complete
 // before that one began), and a chunk's tensor is found by a hint.  150 tensors
-// of 5 MB took 14.3 us with a binary search over the table, whose dependent
-// misses in the constant cache were most of it, and no early read.
+// of 5 MB take 6.9 us in a captured graph; with a binary search over the table,
+// whose dependent misses in the constant cache cost most, no early read and
+// fp64 in every thread they took 14.3.  1.2 GB of bf16 gradients take 0.55 ms:
+// the norm at 6.9 TB/s, the scaling (read and write) at 6.5.
 //
 // The tensors' table travels in the kernel parameters (no copy to the device,
 // nothing to go stale in a captured graph).  Chunks start at 16-byte
