@@ -80,6 +80,7 @@ constexpr int kStagingBuffers = 2;
 constexpr uint32_t kStagingCe = 4 * kStagingBuffers * kStagingBox;
 constexpr size_t kSmemCe = 1024 + kRingCe + kStagingCe + 256;
 static_assert(kSmemCe <= 232448, "shared memory budget");
+static_assert((2 * kMaxStages + 5) * 8 + 8 + 4 * 4 <= 256, "barrier area");
 constexpr int kGroupM = 8;  // m-tiles whose sweep over the n-tiles shares B tiles in L2
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -121,7 +122,8 @@ struct CeParams {
   const float* lse;     // kGrad
   const float* d_loss;
   const float* d_lse;   // or NULL
-  const float* unit;    // kGrad, kProducts: s, the unit of G
+  float* unit;          // s, the unit of G: kGrad finds and writes it
+  int T;
   uint32_t* status;
   int stages;               // of the ring
   uint32_t a_stage, b_stage;  // bytes of a stage's operands in one CTA
@@ -226,6 +228,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_unit = reinterpret_cast<float*>(tmem_slot + 2);  // one per epilogue warp (kGrad)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -391,6 +394,28 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     const uint32_t tempty_leader = pair::mapa(smem_u32(tempty), 0);
     int seg = 0, n_stores = 0;
     bool go = true;
+    float inv_unit = 1.f;
+    if (kMode == CeMode::kGrad) {
+      // s: the largest finite |d_loss| of a token that is not masked (1 if it is
+      // 0, or so small that its reciprocal is not a number); every CTA for
+      // itself, while the first tile is on its way
+      float x = 0.f;
+#pragma unroll 4
+      for (int t = static_cast<int>(threadIdx.x) - 64; t < p.T; t += 32 * epi_warps<kMode>()) {
+        const float d = fabsf(__ldg(p.d_loss + t));
+        const int id = __ldg(p.labels + t);
+        if (d <= 3e38f && id >= 0 && id < p.V) x = fmaxf(x, d);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      if (lane == 0) s_unit[warp - 2] = x;
+      bar_sync_named(1, 32 * epi_warps<kMode>());
+#pragma unroll
+      for (int w = 0; w < epi_warps<kMode>(); ++w) x = fmaxf(x, s_unit[w]);
+      if (!(x >= 0x1p-100f)) x = 1.f;
+      if (blockIdx.x == 0 && threadIdx.x == 64) *p.unit = x;
+      inv_unit = 1.f / x;
+    }
     // the next accumulation is complete
     auto wait_full = [&]() {
       go = __all_sync(0xffffffffu, mbar_wait(&tfull[seg & 1], (seg >> 1) & 1, p.status));
@@ -421,10 +446,9 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const bool valid = id >= 0 && id < p.V;
         if (valid) label = id - p.v0 - col0;  // column of this tile, if it is one
         if (kMode == CeMode::kGrad) {
-          const float inv = 1.f / __ldg(p.unit);
           const float dl = valid ? __ldg(p.d_loss + row) : 0.f;
-          ga = inv * (dl + (p.d_lse ? __ldg(p.d_lse + row) : 0.f));
-          gb = inv * dl;
+          ga = inv_unit * (dl + (p.d_lse ? __ldg(p.d_lse + row) : 0.f));
+          gb = inv_unit * dl;
           lse2 = __ldg(p.lse + row) * kLog2e;
         }
       }
@@ -573,31 +597,6 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     tc_fence_after();
     pair::tmem_dealloc2<512>(tmem_base);
   }
-}
-
-// s: the largest finite |d_loss| of a token that is not masked (1 if it is 0
-// or so small that its reciprocal is not a number).
-__global__ void __launch_bounds__(1024)
-ce_unit_kernel(const float* __restrict__ d_loss, const int32_t* __restrict__ labels, int T, int V,
-               float* __restrict__ unit) {
-  pdl_enter();
-  __shared__ float s[32];
-  float m = 0.f;
-#pragma unroll 4
-  for (int t = threadIdx.x; t < T; t += 1024) {
-    const float x = fabsf(d_loss[t]);
-    const int id = labels[t];
-    if (x <= 3e38f && id >= 0 && id < V) m = fmaxf(m, x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  m = s[threadIdx.x];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (threadIdx.x == 0) *unit = m >= 0x1p-100f ? m : 1.f;
 }
 
 // lse and loss of every token from its tiles' (max, sum), in tile order: 32
@@ -1021,10 +1020,7 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
   k.status = static_cast<uint32_t*>(ws);
   float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kUnitOffset);
   k.unit = unit;
-  if (launch_kernel(ce_unit_kernel, dim3(1), dim3(1024), 0, s, 1, d_loss, labels, p->T, p->V,
-                    unit) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  ++launches;
+  k.T = p->T;
   Matrix xm, wm;
   if (operand(&xm, p, x, p->T, base + L.pad_x, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
   for (int i = 0; i < pieces; ++i) {
