@@ -6,7 +6,8 @@
 // CTA pairs (tcgen05.mma.cta_group::2, fp32 accumulators in TMEM) whose
 // epilogue keeps, per token and tile, the running maximum and the sum of
 // exponentials (log2 units) and picks out the label's logit; a small kernel
-// joins a token's tiles in order.  Per token and vocabulary tile 8 bytes leave
+// joins a token's tiles in order.  Up to 128 tokens: tiles of (128 x 128) of
+// single CTAs (one_cta).  Per token and vocabulary tile 8 bytes leave
 // the kernel instead of 2 N of logits.
 //
 // Backward, in pieces of the vocabulary whose logit gradients (bf16) fit in
@@ -49,8 +50,8 @@
 // Measured (one GB300): T=4096 H=4096 V=32000 forward 0.57 ms (1890 TFLOP/s),
 // backward 1.80 ms (1790, its three products), the rate a plain library GEMM
 // reaches there under the power cap; with few tokens the forward streams W:
-// T=4 H=2048 V=32000 31 us with the join (131 MB, of which 20 us at HBM rate;
-// launches, set-up and the join are the rest), T=4 H=4096 V=128000 176 us (6.0
+// T=4 H=2048 V=32000 29 us with the join (131 MB, of which 20 us at HBM rate;
+// launches, set-up and the join are the rest), T=4 H=4096 V=128000 167 us (6.3
 // TB/s).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -210,7 +211,51 @@ struct Deal {
   }
 };
 
-template <CeMode kMode>
+// The tensor core's operations of a CTA pair (cta_group::2) or of one CTA.
+template <bool kPair>
+struct Core {
+  static __device__ __forceinline__ uint32_t rank() { return kPair ? cluster_ctarank() : 0; }
+  static __device__ __forceinline__ void sync() {
+    if (kPair) cluster_sync();
+  }
+  static __device__ __forceinline__ void load(void* dst, const CUtensorMap* map, bool planes,
+                                              int c, int r, uint32_t plane, uint64_t* bar,
+                                              uint64_t pol) {
+    uint8_t* second = static_cast<uint8_t*>(dst) + plane;
+    if (kPair) {  // a pair's loads complete on the leader's barrier
+      const uint32_t b = pair::mapa(smem_u32(bar), 0);
+      if (planes) {
+        pair::tma_load_3d(dst, map, 0, r, c / 64, b, pol);
+      } else {
+        pair::tma_load(dst, map, c, r, b, pol);
+        pair::tma_load(second, map, c + 64, r, b, pol);
+      }
+    } else if (planes) {
+      tma_load_3d(dst, map, 0, r, c / 64, bar, pol);
+    } else {
+      tma_load_2d(dst, map, c, r, bar, pol);
+      tma_load_2d(second, map, c + 64, r, bar, pol);
+    }
+  }
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             bool accumulate) {
+    if (kPair) pair::mma(d, a, b, idesc, accumulate);
+    else mma_bf16_ss(d, a, b, idesc, accumulate);
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar) {  // in both CTAs
+    if (kPair) pair::commit_both(bar);
+    else mma_commit(bar);
+  }
+  static __device__ __forceinline__ void commit_here(uint64_t* bar) {
+    if (kPair) pair::commit_local(bar);
+    else mma_commit(bar);
+  }
+};
+
+// kPair: 256-row tiles of CTA pairs.  Otherwise (forward and logit gradients of at
+// most 128 tokens: one_cta) every CTA takes 128-row tiles of its own: in a pair
+// the second CTA would have no rows, and half of the epilogues nothing to do.
+template <CeMode kMode, bool kPair>
 __global__ void __launch_bounds__(threads_ce<kMode>(), 1)
 linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMaps m1,
                  const __grid_constant__ CeParams p) {
@@ -231,7 +276,9 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   float* s_unit = reinterpret_cast<float*>(tmem_slot + 2);  // one per epilogue warp (kGrad)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  using C = Core<kPair>;
+  constexpr int kCtas = kPair ? 2 : 1;
+  const uint32_t rank = C::rank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
@@ -240,7 +287,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * epi_warps<kMode>());  // one arrival per epilogue warp
+      mbar_init(&tempty[b], kCtas * epi_warps<kMode>());  // one arrival per epilogue warp
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -250,16 +297,19 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     prefetch_tensormap(&m0.a);
     prefetch_tensormap(&m0.b);
   }
-  if (warp == 1) pair::tmem_alloc2<512>(tmem_slot);
+  if (warp == 1) {
+    if (kPair) pair::tmem_alloc2<512>(tmem_slot);
+    else tmem_alloc<512>(tmem_slot);
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before anything signals them
+  C::sync();  // both CTAs' barriers exist before anything signals them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   // nothing above touches global memory
   pdl_enter();
-  const Deal deal(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1),
+  const Deal deal(p, static_cast<int>(blockIdx.x) / kCtas, static_cast<int>(gridDim.x) / kCtas,
                   kMode == CeMode::kProducts);
   int tile, m, n, split;
   bool two;
@@ -276,8 +326,8 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const Gemm& g = p.g[two];
         const CeMaps& maps = two ? m1 : m0;
         tile_of(g, tile, m, n, split);
-        const int row0 = m * kTileM + static_cast<int>(rank) * 128;
-        const int half = g.n_step / 2;
+        const int row0 = m * (128 * kCtas) + static_cast<int>(rank) * 128;
+        const int half = g.n_step / kCtas;  // this CTA's columns of B
         const int col0 = n * g.n_step + static_cast<int>(rank) * half;
         const bool a_mn = g.a_mn, b_mn = g.b_mn, a_planes = g.a_planes, b_planes = g.b_planes;
         const uint32_t a_plane = static_cast<uint32_t>(a_mn ? g.k_step : g.a_rows) * 128;
@@ -286,7 +336,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         // whatever the shared memory behind them holds: rows of the
         // accumulator that nobody reads)
         const bool a_load = rank == 0 || g.M > 128;
-        const uint32_t bytes = (g.M > 128 ? 4 : 2) * a_plane + 4 * b_plane;
+        const uint32_t bytes = (g.M > 128 ? 4 : 2) * a_plane + 2 * kCtas * b_plane;
         const int k_first = g.k_begin(split), k_last = g.k_begin(split + 1);
         // with one m-tile every pair reads the same A: each starts elsewhere in
         // K, so that they do not all ask for the same lines at once
@@ -296,26 +346,12 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         for (int j = k_first; j < k_last; ++j) {
           if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = pair::mapa(smem_u32(&full[stage]), 0);
-          uint8_t* a = sA + stage * a_stage;
-          uint8_t* b = sB + stage * b_stage;
           const int k0 = kb * g.k_step;
-          if (a_load) {
-            const int c = a_mn ? row0 : k0, r = a_mn ? k0 : row0;
-            if (a_planes) {
-              pair::tma_load_3d(a, &maps.a, 0, r, c / 64, bar, pol);
-            } else {
-              pair::tma_load(a, &maps.a, c, r, bar, pol);
-              pair::tma_load(a + a_plane, &maps.a, c + 64, r, bar, pol);
-            }
-          }
-          const int c = b_mn ? col0 : k0, r = b_mn ? k0 : col0;
-          if (b_planes) {
-            pair::tma_load_3d(b, &maps.b, 0, r, c / 64, bar, pol);
-          } else {
-            pair::tma_load(b, &maps.b, c, r, bar, pol);
-            pair::tma_load(b + b_plane, &maps.b, c + 64, r, bar, pol);
-          }
+          if (a_load)
+            C::load(sA + stage * a_stage, &maps.a, a_planes, a_mn ? row0 : k0, a_mn ? k0 : row0,
+                    a_plane, &full[stage], pol);
+          C::load(sB + stage * b_stage, &maps.b, b_planes, b_mn ? col0 : k0, b_mn ? k0 : col0,
+                  b_plane, &full[stage], pol);
           ++issued;
           if (++kb == k_last) kb = k_first;
           if (++stage == n_stages) { stage = 0; phase ^= 1; }
@@ -345,7 +381,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         const bool a_mn = g.a_mn, b_mn = g.b_mn;
         split = g.splits > 1 ? tile / (g.m_tiles * g.n_tiles) : 0;
         const int ksteps = g.k_begin(split + 1) - g.k_begin(split), k_step = g.k_step;
-        const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(g.n_step)) |
+        const uint32_t idesc = idesc_bf16_f32(128 * kCtas, static_cast<uint32_t>(g.n_step)) |
                                (static_cast<uint32_t>(a_mn) << 15) |
                                (static_cast<uint32_t>(b_mn) << 16);
         // a K=16 step is 32 bytes along a K-major plane, which holds four (the
@@ -353,7 +389,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         // which hold eight; in units of 16 bytes
         const uint32_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;
         const uint32_t a4 = a_mn ? 512 : static_cast<uint32_t>(g.a_rows) * 8;
-        const uint32_t b4 = b_mn ? 512 : static_cast<uint32_t>(g.n_step) * 4;
+        const uint32_t b4 = b_mn ? 512 : static_cast<uint32_t>(g.n_step / kCtas) * 8;
         const int per_seg = kMode == CeMode::kLse ? kPromote : ksteps;
         for (int k0 = 0; ok && k0 < ksteps; k0 += per_seg, ++seg) {
           const int buf = seg & 1;
@@ -371,17 +407,17 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
 #pragma unroll
             for (int kk = 0; kk < kTileK / 16; ++kk) {
               if (kk * 16 >= k_step) break;
-              pair::mma(d_tmem, ad + (kk & 3) * as + (kk >> 2) * a4,
+              C::mma(d_tmem, ad + (kk & 3) * as + (kk >> 2) * a4,
                         bd + (kk & 3) * bs + (kk >> 2) * b4, idesc, kb > k0 || kk != 0);
             }
-            pair::commit_both(&empty[stage]);
+            C::commit(&empty[stage]);
             if (++stage == n_stages) { stage = 0; phase ^= 1; }
           }
-          if (ok) pair::commit_both(&tfull[buf]);
+          if (ok) C::commit(&tfull[buf]);
         }
         if (!ok) *abort_flag = 1;
       }
-      pair::commit_local(drain);  // every MMA done before TMEM is released
+      C::commit_here(drain);  // every MMA done before TMEM is released
       mbar_wait(drain, 0, p.status);
     }
     __syncwarp();
@@ -391,7 +427,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     uint8_t* staging = s_out + (warp - 2) * kStagingBuffers * kStagingBox;
     const int rsw = lane & 7;
     const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t tempty_leader = pair::mapa(smem_u32(tempty), 0);
+    const uint32_t tempty_leader = kPair ? pair::mapa(smem_u32(tempty), 0) : 0;
     int seg = 0, n_stores = 0;
     bool go = true;
     float inv_unit = 1.f;
@@ -427,14 +463,17 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) pair::arrive_remote(tempty_leader + (seg & 1) * 8);
+      if (lane == 0) {
+        if (kPair) pair::arrive_remote(tempty_leader + (seg & 1) * 8);
+        else mbar_arrive(&tempty[seg & 1]);
+      }
       ++seg;
     };
     for (int i = 0; go && deal.at(i, tile, two); ++i) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
       const Gemm& g = p.g[two];
       tile_of(g, tile, m, n, split);
-      const int wrow0 = m * kTileM + static_cast<int>(rank) * 128 + quad * 32;
+      const int wrow0 = m * (128 * kCtas) + static_cast<int>(rank) * 128 + quad * 32;
       const int row = wrow0 + lane;
       const bool row_ok = row < g.M, warp_ok = wrow0 < g.M;
       const int col0 = n * g.n_step;
@@ -455,9 +494,11 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
       const float c2 = p.scale * kLog2e;
 
       if (kMode == CeMode::kLse) {
-        // this warp's half of the columns, up to 128 of a row per thread
-        const int half = (warp - 2) >> 2, c0 = half * 128;
-        uint32_t z[4][32];  // fp32
+        // this warp's half of the columns: up to 128 of a row per thread, of one
+        // CTA's tiles up to 64
+        constexpr int kChunks = kPair ? 4 : 2;
+        const int half = (warp - 2) >> 2, c0 = half * 32 * kChunks;
+        uint32_t z[kChunks][32];  // fp32
         for (int k0 = 0; k0 < g.ksteps; k0 += kPromote) {
           if (!wait_full()) break;
           const uint32_t t_lane = t_quad + (seg & 1) * kTileN + c0;
@@ -465,11 +506,11 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             __syncwarp();
             if (k0 == 0) {  // all at once (columns past the tile's are not used)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_lane + 32 * q, z[q]);
+              for (int q = 0; q < kChunks; ++q) tmem_ld_32x32b_x32(t_lane + 32 * q, z[q]);
               tmem_ld_wait();
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < kChunks; ++q) {
                 uint32_t a[32];
                 tmem_ld_32x32b_x32(t_lane + 32 * q, a);
                 tmem_ld_wait();
@@ -484,7 +525,7 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
         if (!go) break;
         float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kChunks; ++q) {
           const int c = c0 + 32 * q, left = ncols - c;
           if (!warp_ok || left <= 0) continue;
           if (label >= c && label < c + 32) {
@@ -592,10 +633,11 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
   __syncthreads();
   // neither CTA frees TMEM or exits while the other may still signal its
   // barriers or the leader's MMAs may still write its TMEM
-  cluster_sync();
+  C::sync();
   if (warp == 1) {
     tc_fence_after();
-    pair::tmem_dealloc2<512>(tmem_base);
+    if (kPair) pair::tmem_dealloc2<512>(tmem_base);
+    else tmem_dealloc<512>(tmem_base);
   }
 }
 
@@ -720,16 +762,29 @@ bool make_map(CUtensorMap* map, const void* base, long rows, long cols, long ld,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns per tile: with the waves that 256-column tiles would take over the
-// CTA pairs, the narrowest tile (a multiple of `unit`) that needs no more
-// waves, so that the last wave is as full as the others.  The unit is what
+// Tiles of one CTA each (at most 128 columns: a stage is then as large as a
+// pair's) instead of a pair's.  Forward / logit gradients and products, one CTA
+// against pairs, us: T=1 H=64 V=32000 10.8 against 13.8 / 24.2 against 27.4; T=8
+// H=128 V=50021 12.9, 17.8 / 37.7, 42.0; T=32 H=256 V=32000 11.3, 15.9 / 30.1,
+// 33.4; T=128 H=1024 V=32000 22.6, 25.3 / 75.6, 77.6; T=4 H=4096 V=128000 172,
+// 176 / 780, 775.  Rows that are not whole planes copy slowly, and tiles half
+// as wide copy those of x twice as often: T=96 H=1000 V=50021 44.7, 39.2 / 115,
+// 113; T=128 H=8 V=200000 141, 93 / 251, 209: pairs there.
+bool one_cta(const moe_ce_problem* p) { return p->T <= 128 && p->H % 64 == 0; }
+
+// Columns per tile: with the waves that the widest tiles would take over the
+// CTA pairs (or the CTAs), the narrowest tile (a multiple of `unit`) that needs
+// no more waves, so that the last wave is as full as the others.  The unit is what
 // the epilogue takes at a time: 32 columns, or 64 where it stores them.
 constexpr int kUnitLse = 32, kUnitGrad = 64;
-int tile_columns(int m_tiles, int N, int unit) {
-  const int pairs = std::max(1, num_sms() / 2);
-  const long waves = ceil_div(static_cast<long>(m_tiles) * ceil_div(N, kTileN), pairs);
-  int n = kTileN;
-  while (n > unit && static_cast<long>(m_tiles) * ceil_div(N, n - unit) <= waves * pairs) n -= unit;
+int tile_columns(const moe_ce_problem* p, int N, int unit) {
+  const int m_tiles = ceil_div(p->T, kTileM);
+  const int workers = one_cta(p) ? num_sms() : std::max(1, num_sms() / 2);
+  const int most = one_cta(p) ? 128 : kTileN;
+  const long waves = ceil_div(static_cast<long>(m_tiles) * ceil_div(N, most), workers);
+  int n = most;
+  while (n > unit && static_cast<long>(m_tiles) * ceil_div(N, n - unit) <= waves * workers)
+    n -= unit;
   return n;
 }
 
@@ -743,7 +798,7 @@ struct Matrix {
 // [K, M] and [K, N] read MN-major) and their maps; false if a map could not be
 // made.
 bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const Matrix& a,
-               bool a_mn, const Matrix& b, bool b_mn) {
+               bool a_mn, const Matrix& b, bool b_mn, bool pair = true) {
   *g = Gemm{};
   g->M = static_cast<int>(M);
   g->N = static_cast<int>(N);
@@ -766,17 +821,17 @@ bool make_gemm(Gemm* g, CeMaps* maps, long M, long N, long K, int n_step, const 
                   : make_map(m, x.p, x.rows, x.cols, x.ld, rows);
   };
   return make(&maps->a, a, g->a_planes, a_mn ? g->k_step : g->a_rows) &&
-         make(&maps->b, b, g->b_planes, b_mn ? g->k_step : n_step / 2);
+         make(&maps->b, b, g->b_planes, b_mn ? g->k_step : pair ? n_step / 2 : n_step);
 }
 
-template <CeMode kMode>
+template <CeMode kMode, bool kPair>
 cudaError_t launch_ce(const CeMaps& m0, const CeMaps& m1, CeParams& p, cudaStream_t s) {
-  auto kern = linear_ce_kernel<kMode>;
+  auto kern = linear_ce_kernel<kMode, kPair>;
   p.a_stage = p.b_stage = 0;
   for (const Gemm& g : p.g) {
     if (g.tiles() == 0) continue;
     p.a_stage = std::max(p.a_stage, static_cast<uint32_t>(g.a_rows) * 256);
-    p.b_stage = std::max(p.b_stage, static_cast<uint32_t>(g.n_step) * 128);
+    p.b_stage = std::max(p.b_stage, static_cast<uint32_t>(g.n_step) * (kPair ? 128 : 256));
   }
   // the forward has no staging for output tiles: its ring takes that room too
   const uint32_t ring = kRingCe + (kMode == CeMode::kLse ? kStagingCe : 0);
@@ -785,8 +840,15 @@ cudaError_t launch_ce(const CeMaps& m0, const CeMaps& m1, CeParams& p, cudaStrea
                                                static_cast<int>(kSmemCe));
   if (err != cudaSuccess) return err;
   const long tiles = static_cast<long>(p.g[0].tiles()) + p.g[1].tiles();
-  const int pairs = static_cast<int>(std::max(1L, std::min<long>(num_sms() / 2, tiles)));
-  return launch_kernel(kern, dim3(2 * pairs), dim3(threads_ce<kMode>()), kSmemCe, s, 2, m0, m1, p);
+  constexpr int kCtas = kPair ? 2 : 1;
+  const int groups = static_cast<int>(std::max(1L, std::min<long>(num_sms() / kCtas, tiles)));
+  return launch_kernel(kern, dim3(kCtas * groups), dim3(threads_ce<kMode>()), kSmemCe, s, kCtas, m0,
+                       m1, p);
+}
+template <CeMode kMode>
+cudaError_t launch_ce_logits(const CeMaps& m, bool one, CeParams& p, cudaStream_t s) {
+  return one ? launch_ce<kMode, false>(m, m, p, s)
+             : launch_ce<kMode, true>(m, m, p, s);
 }
 
 constexpr size_t kCeHeader = 256;
@@ -832,7 +894,7 @@ size_t ce_pad_bytes(const moe_ce_problem* p, long w_rows) {
 }
 
 size_t ce_forward_bytes(const moe_ce_problem* p) {
-  const int n = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
+  const int n = tile_columns(p, p->V, kUnitLse);
   const size_t T = static_cast<size_t>(p->T);
   return kCeHeader + up(sizeof(float2) * T * 2 * ceil_div(p->V, n)) + up(sizeof(float) * T) +
          ce_pad_bytes(p, p->V);
@@ -950,7 +1012,7 @@ extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, con
   rc = check_ce_tensors(x, w, labels, lse, loss, ws);
   if (rc != MOE_OK) return rc;
   if (ws_bytes < ce_forward_bytes(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  const int n_step = tile_columns(ceil_div(p->T, kTileM), p->V, kUnitLse);
+  const int n_step = tile_columns(p, p->V, kUnitLse);
   uint8_t* base = static_cast<uint8_t*>(ws) + kCeHeader;
   CeParams k{};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -963,7 +1025,7 @@ extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, con
               &launches) != cudaSuccess)
     return MOE_ERR_CUDA;
   CeMaps m{};
-  if (!make_gemm(&k.g[0], &m, p->T, p->V, xm.cols, n_step, xm, false, wm, false))
+  if (!make_gemm(&k.g[0], &m, p->T, p->V, xm.cols, n_step, xm, false, wm, false, !one_cta(p)))
     return MOE_ERR_CUDA;
   k.labels = labels;
   k.V = p->V;
@@ -971,7 +1033,7 @@ extern "C" int moe_linear_ce_forward(const moe_ce_problem* p, const void* x, con
   k.part = reinterpret_cast<float2*>(base);
   k.label_logit = reinterpret_cast<float*>(base + n_part);
   k.status = static_cast<uint32_t*>(ws);
-  if (launch_ce<CeMode::kLse>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_ce_logits<CeMode::kLse>(m, one_cta(p), k, s) != cudaSuccess) return MOE_ERR_CUDA;
   if (launch_kernel(ce_join_kernel, dim3(ceil_div(p->T, 32)), dim3(1024), 0, s, 1,
                     static_cast<const float2*>(k.part), static_cast<const float*>(k.label_logit),
                     labels, p->T, p->V, 2 * k.g[0].n_tiles, loss, lse, k.status) != cudaSuccess)
@@ -1028,16 +1090,17 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
     const uint8_t* wp = static_cast<const uint8_t*>(w) + 2 * static_cast<size_t>(v0) * p->H;
     uint8_t* dwp = static_cast<uint8_t*>(dw) + 2 * static_cast<size_t>(v0) * p->H;
     k.v0 = v0;
-    const int n_step = tile_columns(ceil_div(p->T, kTileM), nv, kUnitGrad);
+    const int n_step = tile_columns(p, nv, kUnitGrad);
     if (operand(&wm, p, wp, nv, base + L.pad_w, s, &launches) != cudaSuccess) return MOE_ERR_CUDA;
     // padded to whole planes: the epilogue writes zeros there
     const Matrix gm{grad, p->T, ceil_div(nv, 64) * 64L, rows};
     CeMaps m{}, m1{};
     k.g[1] = Gemm{};
-    if (!make_gemm(&k.g[0], &m, p->T, nv, xm.cols, n_step, xm, false, wm, false) ||
+    if (!make_gemm(&k.g[0], &m, p->T, nv, xm.cols, n_step, xm, false, wm, false,
+                   !one_cta(p)) ||
         !make_map(&m.out, grad, p->T, gm.cols, rows, 32))
       return MOE_ERR_CUDA;
-    if (launch_ce<CeMode::kGrad>(m, m, k, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_ce_logits<CeMode::kGrad>(m, one_cta(p), k, s) != cudaSuccess) return MOE_ERR_CUDA;
     if (!make_gemm(&k.g[0], &m, p->T, p->H, nv, kTileN, gm, false, wm, true) ||
         !make_map(&m.out, dx, p->T, p->H, p->H, 32) ||
         !make_gemm(&k.g[1], &m1, nv, p->H, p->T, kTileN, gm, true, xm, true) ||
@@ -1052,7 +1115,7 @@ extern "C" int moe_linear_ce_backward(const moe_ce_problem* p, const void* x, co
     k.g[1].splits = sp.dw;
     k.g[1].acc = acc_dw;
     k.g[1].keep = sp.dw > 1;
-    if (launch_ce<CeMode::kProducts>(m, m1, k, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_ce<CeMode::kProducts, true>(m, m1, k, s) != cudaSuccess) return MOE_ERR_CUDA;
     launches += 2;
     if (sp.dw > 1 && join_splits(acc_dw, sp.dw, static_cast<long>(nv) * p->H, p->logit_scale, unit,
                                  dwp, s, &launches) != cudaSuccess)

@@ -106,6 +106,15 @@ def test_widths(H):
     check(70, H, 300)
 
 
+@pytest.mark.parametrize("T", [1, 33, 96, 127, 128, 129])
+@pytest.mark.parametrize("H,V", [(64, 1), (64, 129), (128, 127), (64, 20011), (128, 60000),
+                                 (1088, 5000), (2112, 20011)])
+def test_tiles_of_one_cta(T, H, V):
+    """Few tokens of whole 64-column planes take tiles of single CTAs; 129 take a pair's.  Several
+    tiles per CTA, ragged last ones, and rows longer than one run of the accumulator."""
+    check(T, H, V, use_d_lse=T % 2 == 0)
+
+
 @pytest.mark.parametrize("T,V", [(300, 40000), (3, 60000), (2100, 20011)])
 def test_several_waves_and_tile_widths(T, V):
     check(T, 256, V)
