@@ -140,6 +140,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A running softmax (maximum m, sum of 2^(v - m)): what the exponents are taken
+// against.  It is finite also where m is not, so that the sum stays what the
+// formula has: 0 while every logit is -inf, infinite once one is +inf, and NaN
+// once one is NaN, which a maximum (fmaxf) does not show.
+__device__ __forceinline__ float sum_unit(float m) { return fabsf(m) < INFINITY ? m : 0.f; }
+
 // Descriptor of an MN-major operand: planes of 64 columns x k_step K rows with
 // the 128-byte swizzle; leading offset = the next 64 columns (one plane),
 // stride offset = 8 K rows.
@@ -541,13 +547,12 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
             cm[j & 3] = fmaxf(cm[j & 3], v[j]);
           }
           const float m4 = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
-          // ordinary rows: one rescaling a chunk; all -inf so far: the sum stays 0
-          if (m4 != -INFINITY) {
+          // one rescaling a chunk
+          const float unit = sum_unit(m4);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(v[j] - m4);
-            sum = fmaf(sum, ex2(mx - m4), (s4[0] + s4[1]) + (s4[2] + s4[3]));
-            mx = m4;
-          }
+          for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(v[j] - unit);
+          sum = fmaf(sum, ex2(mx - unit), (s4[0] + s4[1]) + (s4[2] + s4[3]));
+          mx = m4;
         }
         if (row_ok) p.part[static_cast<long>(2 * n + half) * g.M + row] = make_float2(mx, sum);
       } else {
@@ -653,9 +658,8 @@ ce_join_kernel(const float2* __restrict__ part, const float* __restrict__ label_
   const int t = blockIdx.x * 32 + lane;
   float m = -INFINITY, sum = 0.f;
   auto add = [&](float2 x) {
-    const float cm = fmaxf(m, x.x);
-    if (cm == -INFINITY) return;
-    sum = sum * ex2(m - cm) + x.y * ex2(x.x - cm);
+    const float cm = fmaxf(m, x.x), unit = sum_unit(cm);
+    sum = sum * ex2(m - unit) + x.y * ex2(x.x - unit);
     m = cm;
   };
   if (t < T) {

@@ -260,3 +260,50 @@ def test_binding_refuses_wrong_tensors():
             moe.linear_ce_forward(p, *a, ws)
     with pytest.raises(moe.MoEError):
         moe.linear_ce_forward(p, x, w, labels, f, f, ws[:256])
+
+
+def logits_of(x, w):
+    return x.double() @ w.double().t()
+
+
+@pytest.mark.parametrize("T,H", [(4, 64), (4, 72), (200, 64), (300, 1088)])
+@pytest.mark.parametrize("V", [1, 2, 33, 65, 129, 257, 700, 40001])
+def test_lse_of_logits_that_are_not_finite(T, H, V):
+    """NaN in a token (masked or not), NaN in the vocabulary's last row alone, infinite logits of
+    either sign, and nothing but -inf: lse as the formula has it in 64 bits, and no other token
+    touched.  V - 1 is the first column of a tile, of a warp's half or of a chunk of 32."""
+    x, w, labels, _ = inputs(T, H, V, masked=0.0)
+    labels[1], labels[2] = -1, 0
+    p = moe.CEProblem.make(T, H, V)
+    ws = moe.alloc_linear_ce_workspace(p)
+    clean_loss, clean = forward(p, x, w, labels, ws)
+
+    bad = x.clone()
+    bad[1, 3], bad[2, 5] = float("nan"), float("nan")
+    loss, lse = forward(p, bad, w, labels, ws)
+    assert torch.isnan(lse).nonzero()[:, 0].tolist() == [1, 2]
+    assert loss[1] == 0 and torch.isnan(loss[2])
+    keep = ~torch.isnan(lse)
+    assert torch.equal(lse[keep], clean[keep]) and torch.equal(loss[keep], clean_loss[keep])
+
+    bad = w.clone()
+    bad[V - 1, 7] = float("nan")
+    loss, lse = forward(p, x, bad, labels, ws)
+    assert torch.isnan(lse).all() and torch.isnan(loss[labels >= 0]).all() and loss[1] == 0
+
+    for value in (float("inf"), float("-inf")):
+        bad = w.clone()
+        bad[V // 2, 0] = value  # +inf or -inf by the sign of x's first column
+        _, lse = forward(p, x, bad, labels, ws)
+        want = torch.logsumexp(logits_of(x, bad), 1)
+        assert (x[:, 0] != 0).all() and torch.equal(torch.isinf(want), torch.isinf(lse))
+        inf = torch.isinf(want)
+        assert torch.equal(want[inf], lse[inf].double()) and not torch.isnan(lse).any()
+        assert ((lse.double() - want)[~inf].abs() <= 1e-4 * (1 + want[~inf].abs())).all()
+
+    bad = w.clone()
+    bad[:, 0] = float("-inf")
+    positive = x.clone()
+    positive[:, 0] = 1.0
+    _, lse = forward(p, positive, bad, labels, ws)
+    assert torch.equal(lse, torch.full_like(lse, float("-inf")))
