@@ -442,12 +442,15 @@ linear_ce_kernel(const __grid_constant__ CeMaps m0, const __grid_constant__ CeMa
       // 0, or so small that its reciprocal is not a number); every CTA for
       // itself, while the first tile is on its way
       float x = 0.f;
+      bool bad = false;
 #pragma unroll 4
       for (int t = static_cast<int>(threadIdx.x) - 64; t < p.T; t += 32 * epi_warps<kMode>()) {
         const float d = fabsf(__ldg(p.d_loss + t));
         const int id = __ldg(p.labels + t);
+        bad |= id >= p.V;
         if (d <= 3e38f && id >= 0 && id < p.V) x = fmaxf(x, d);
       }
+      if (blockIdx.x == 0 && bad) record_status(p.status, kStatusIndex);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
       if (lane == 0) s_unit[warp - 2] = x;

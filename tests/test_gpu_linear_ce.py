@@ -307,3 +307,16 @@ def test_lse_of_logits_that_are_not_finite(T, H, V):
     positive[:, 0] = 1.0
     _, lse = forward(p, positive, bad, labels, ws)
     assert torch.equal(lse, torch.full_like(lse, float("-inf")))
+
+
+def test_backward_records_labels_beyond_the_vocabulary():
+    T, H, V = 300, 64, 100
+    x, w, labels, d_loss = inputs(T, H, V, masked=0.3)
+    p = moe.CEProblem.make(T, H, V)
+    ws = moe.alloc_linear_ce_workspace(p, backward=True)
+    _, lse = forward(p, x, w, labels, ws)
+    backward(p, x, w, labels, lse, d_loss, ws)
+    assert moe.get_device_status(ws) == moe.MOE_OK
+    labels[T - 1] = V
+    backward(p, x, w, labels, lse, d_loss, ws)
+    assert moe.get_device_status(ws) == 7
