@@ -106,6 +106,12 @@ __device__ __forceinline__ float square16(uint4 v) {
   return s;
 }
 
+// 0 exactly if every element is a zero of either sign.
+template <bool kF32>
+__device__ __forceinline__ uint32_t magnitude16(uint4 v) {
+  return (v.x | v.y | v.z | v.w) & (kF32 ? 0x7fffffffu : 0x7fff7fffu);
+}
+
 template <bool kF32>
 __device__ __forceinline__ double square16_f64(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -150,7 +156,16 @@ __device__ __forceinline__ double part_squares(const Chunk& c, const Part& p) {
     if (u * kClipThreads + static_cast<int>(threadIdx.x) < p.vecs) s += square16<kF32>(p.x[u]);
   const float e = p.single >= 0 ? to_float(reinterpret_cast<const T*>(c.grad)[p.single]) : 0.f;
   s = fmaf(e, e, s);
-  if (s == 0.f || (s >= 0x1p-80f && s < __int_as_float(0x7f800000))) return s;
+  if (s == 0.f) {  // zeros, or squares that are all below fp32's smallest number
+    uint32_t bits = __float_as_uint(e) << 1;
+#pragma unroll
+    for (int u = 0; u < kClipVecs; ++u)
+      if (u * kClipThreads + static_cast<int>(threadIdx.x) < p.vecs)
+        bits |= magnitude16<kF32>(p.x[u]);
+    if (bits == 0) return 0.;
+  } else if (s >= 0x1p-80f && s < __int_as_float(0x7f800000)) {
+    return s;
+  }
   double d = static_cast<double>(e) * e;  // out of fp32's comfortable range: again in fp64
 #pragma unroll 1
   for (int i = threadIdx.x; i < p.vecs; i += kClipThreads)

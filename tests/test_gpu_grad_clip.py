@@ -173,3 +173,15 @@ def test_binding_refuses_wrong_tensors():
         moe.clip_grad_norm(lst, -1.0, torch.empty(2, device=DEV), moe.alloc_clip_workspace(lst))
     with pytest.raises(ValueError):
         moe.clip_grad_norm(lst, 1.0, torch.empty(1, device=DEV), moe.alloc_clip_workspace(lst))
+
+
+@pytest.mark.parametrize("value,dtype", [(1e-25, F32), (1e-30, BF), (1e-39, F32)])
+def test_squares_that_vanish_in_fp32(value, dtype):
+    """Every square is below fp32's smallest number, the norm is not: it is neither lost in a
+    tensor of such elements nor in one that has a few of them among zeros."""
+    g = torch.full((40000,), value, dtype=dtype, device=DEV)
+    total, _, _ = reference([g], 1.0, 1.0, 0.0)
+    check([g], total / 8, eps=0.0)
+    g = torch.zeros(100003, dtype=dtype, device=DEV)
+    g[[0, 77777, 100002]] = value
+    check([g], value, eps=0.0)
