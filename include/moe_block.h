@@ -119,11 +119,12 @@ typedef struct moe_grad_tensor {
 MOE_API size_t moe_clip_workspace_size(int32_t n);
 
 /*   tensors   [n] in HOST memory, read before the call returns
- *   max_norm  >= 0; +infinity: only grad_scale is applied
+ *   max_norm  >= 0; +infinity: only grad_scale is applied (coef 1, whatever the
+ *             norm: an element that is not finite stays the only one)
  *   norm_out  [2] fp32 device out: norm and coef
- * A norm that is not finite gives the coef its formula has (0 for infinity,
- * NaN for NaN); the caller can read it from norm_out.  In place, a factor of
- * exactly 1 writes nothing. */
+ * Under a finite max_norm, a norm that is not finite gives the coef its formula
+ * has (0 for infinity, NaN for NaN); the caller can read it from norm_out.  In
+ * place, a factor of exactly 1 writes nothing. */
 MOE_API int moe_clip_grad_norm(int32_t n, const moe_grad_tensor* tensors, float grad_scale,
                                float max_norm, float eps, float* norm_out, void* ws,
                                size_t ws_bytes, void* stream);

@@ -261,7 +261,8 @@ grad_scale_kernel(const __grid_constant__ GradTable<kCap> t, const double* __res
   if (threadIdx.x == 0) {
     const float norm = static_cast<float>(fabs(static_cast<double>(grad_scale)) * sqrt(sum));
     float coef = max_norm / (norm + eps);
-    if (coef >= 1.f) coef = 1.f;  // a NaN stays
+    // a NaN stays, unless there is no limit
+    if (coef >= 1.f || max_norm == __int_as_float(0x7f800000)) coef = 1.f;
     if (norm_out && blockIdx.x == 0) {
       norm_out[0] = norm;
       norm_out[1] = coef;

@@ -185,3 +185,19 @@ def test_squares_that_vanish_in_fp32(value, dtype):
     g = torch.zeros(100003, dtype=dtype, device=DEV)
     g[[0, 77777, 100002]] = value
     check([g], value, eps=0.0)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 3e38])
+def test_no_limit_and_a_norm_that_is_not_finite(value):
+    """max_norm = +inf applies grad_scale and nothing else: an element that is not finite, or a
+    norm beyond fp32, leaves the other gradients as they are."""
+    a = torch.arange(20000, device=DEV, dtype=torch.float32)
+    a[7:90] = value
+    out = torch.empty_like(a)
+    norm = run([a], [out], math.inf, scale=0.5).cpu()
+    assert norm[1] == 1.0 and not math.isfinite(norm[0])
+    assert torch.equal(out.nan_to_num(nan=-1.0), (0.5 * a).nan_to_num(nan=-1.0))
+    keep = a.clone()
+    norm = run([a], None, math.inf).cpu()
+    assert norm[1] == 1.0 and not math.isfinite(norm[0])
+    assert torch.equal(a.nan_to_num(nan=-1.0), keep.nan_to_num(nan=-1.0))
