@@ -158,6 +158,13 @@ def _rows(t: Optional[torch.Tensor], dtype, shape, strides):
     return t.data_ptr()
 
 
+def _gate(t: Optional[torch.Tensor], p):
+    """The address of a gate of the problem's kind, or of its gradient (None for None)."""
+    if t is not None and p._gate is None:
+        raise ValueError('a gate or its gradient, for a problem of gate "none"')
+    return _dense(t, p._w, p._gate)
+
+
 # the current stream's handle without a Stream object around it (3 us of a call of 11)
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -189,7 +196,7 @@ def block_norm_forward(p: NormProblem, residual, branch=None, w_post=None, gate=
     b, r, ro, n = p._ld
     rc = load().moe_block_norm_forward(
         ctypes.byref(p), _rows(branch, p._b, p._rows, b), _dense(w_post, p._w, p._cols),
-        _dense(gate, p._w, p._gate), _rows(residual, p._r, p._rows, r),
+        _gate(gate, p), _rows(residual, p._r, p._rows, r),
         _dense(w_pre, p._w, p._cols), _rows(residual_out, p._r, p._rows, ro),
         _rows(normed, p._b, p._rows, n), _raw_stream(stream))
     if rc != MOE_OK:
@@ -212,11 +219,11 @@ def block_norm_backward(p: NormProblem, residual_out, d_residual, ws, branch=Non
     b, r, ro, n = p._ld
     rc = load().moe_block_norm_backward(
         ctypes.byref(p), _rows(branch, p._b, p._rows, b), _dense(w_post, p._w, p._cols),
-        _dense(gate, p._w, p._gate), _rows(residual_out, p._r, p._rows, ro),
+        _gate(gate, p), _rows(residual_out, p._r, p._rows, ro),
         _dense(w_pre, p._w, p._cols), _rows(d_residual_out, p._r, p._rows, ro),
         _rows(d_normed, p._b, p._rows, n), _rows(d_residual, p._r, p._rows, r),
         _rows(d_branch, p._b, p._rows, b), _dense(d_w_post, p._w, p._cols),
-        _dense(d_gate, p._w, p._gate), _dense(d_w_pre, p._w, p._cols), ws.data_ptr(), ws.numel(),
+        _gate(d_gate, p), _dense(d_w_pre, p._w, p._cols), ws.data_ptr(), ws.numel(),
         _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_block_norm_backward", rc)

@@ -220,3 +220,13 @@ def test_ce_workspace_does_not_hold_the_logits(lib):
     p = moe.CEProblem.make(65536, 4096, 131072)
     logits = 2 * 65536 * 131072
     assert lib.moe_linear_ce_backward_workspace_size(ctypes.byref(p)) < logits / 8
+
+
+def test_binding_refuses_a_gate_where_the_problem_has_none(monkeypatch):
+    monkeypatch.setattr(moe.block, "_rows", lambda t, *a: None if t is None else A)
+    p, r, g = norm(), torch.zeros(8, 64), torch.ones(64)
+    with pytest.raises(ValueError, match="gate"):
+        moe.block_norm_forward(p, r, branch=r, gate=g, residual_out=r)
+    with pytest.raises(ValueError, match="gate"):
+        moe.block_norm_backward(p, r, r, torch.zeros(512, dtype=torch.uint8), branch=r, d_gate=g,
+                                d_branch=r)
