@@ -165,6 +165,14 @@ def _gate(t: Optional[torch.Tensor], p):
     return _dense(t, p._w, p._gate)
 
 
+def _workspace(ws: torch.Tensor):
+    """The address and the bytes of a workspace."""
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"expected a contiguous workspace on the GPU, got one with strides "
+                         f"{ws.stride()} on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.itemsize
+
+
 # the current stream's handle without a Stream object around it (3 us of a call of 11)
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -223,8 +231,7 @@ def block_norm_backward(p: NormProblem, residual_out, d_residual, ws, branch=Non
         _dense(w_pre, p._w, p._cols), _rows(d_residual_out, p._r, p._rows, ro),
         _rows(d_normed, p._b, p._rows, n), _rows(d_residual, p._r, p._rows, r),
         _rows(d_branch, p._b, p._rows, b), _dense(d_w_post, p._w, p._cols),
-        _gate(d_gate, p), _dense(d_w_pre, p._w, p._cols), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream))
+        _gate(d_gate, p), _dense(d_w_pre, p._w, p._cols), *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_block_norm_backward", rc)
 
@@ -241,7 +248,7 @@ def clip_grad_norm(grads: GradList, max_norm: float, norm, ws, grad_scale: float
     coefficient.  Nothing is read back to the host."""
     rc = load().moe_clip_grad_norm(len(grads.grads), ctypes.addressof(grads.table), grad_scale,
                                    max_norm, eps, _dense(norm, torch.float32, (2,)),
-                                   ws.data_ptr(), ws.numel(), _raw_stream(stream))
+                                   *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_clip_grad_norm", rc)
 
@@ -251,7 +258,8 @@ def embedding_forward(p: EmbedProblem, ids, table, out, ws=None, stream=None) ->
     workspace) an id outside the vocabulary is recorded in its status word."""
     rc = load().moe_embedding_forward(
         ctypes.byref(p), _dense(ids, torch.int32, p._ids), _dense(table, p._t, p._table),
-        _dense(out, p._o, p._out), ws.data_ptr() if ws is not None else None, _raw_stream(stream))
+        _dense(out, p._o, p._out), _workspace(ws)[0] if ws is not None else None,
+        _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_embedding_forward", rc)
 
@@ -266,7 +274,7 @@ def embedding_backward(p: EmbedProblem, ids, d_out, d_table, ws, stream=None) ->
     """d_table[v] = scale * sum of d_out over the tokens of id v, every row written."""
     rc = load().moe_embedding_backward(
         ctypes.byref(p), _dense(ids, torch.int32, p._ids), _dense(d_out, p._o, p._out),
-        _dense(d_table, p._t, p._table), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+        _dense(d_table, p._t, p._table), *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_embedding_backward", rc)
 
@@ -283,7 +291,7 @@ def linear_ce_forward(p: CEProblem, x, w, labels, loss, lse, ws, stream=None) ->
     rc = load().moe_linear_ce_forward(
         ctypes.byref(p), _dense(x, torch.bfloat16, p._x), _dense(w, torch.bfloat16, p._w),
         _dense(labels, torch.int32, p._rows), _dense(loss, torch.float32, p._rows),
-        _dense(lse, torch.float32, p._rows), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+        _dense(lse, torch.float32, p._rows), *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_linear_ce_forward", rc)
 
@@ -295,8 +303,8 @@ def linear_ce_backward(p: CEProblem, x, w, labels, lse, d_loss, dx, dw, ws, d_ls
         ctypes.byref(p), _dense(x, torch.bfloat16, p._x), _dense(w, torch.bfloat16, p._w),
         _dense(labels, torch.int32, p._rows), _dense(lse, torch.float32, p._rows),
         _dense(d_loss, torch.float32, p._rows), _dense(d_lse, torch.float32, p._rows),
-        _dense(dx, torch.bfloat16, p._x), _dense(dw, torch.bfloat16, p._w), ws.data_ptr(),
-        ws.numel(), _raw_stream(stream))
+        _dense(dx, torch.bfloat16, p._x), _dense(dw, torch.bfloat16, p._w),
+        *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_linear_ce_backward", rc)
 

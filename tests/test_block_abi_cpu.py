@@ -230,3 +230,29 @@ def test_binding_refuses_a_gate_where_the_problem_has_none(monkeypatch):
     with pytest.raises(ValueError, match="gate"):
         moe.block_norm_backward(p, r, r, torch.zeros(512, dtype=torch.uint8), branch=r, d_gate=g,
                                 d_branch=r)
+
+
+def test_binding_refuses_workspaces_that_are_not_on_the_gpu(monkeypatch):
+    """Before the library is called: the kernels would write to the host's address."""
+    called = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: called.append(name) or 0
+
+    monkeypatch.setattr(moe.block, "load", Library)
+    monkeypatch.setattr(moe.block, "_raw_stream", lambda s: 0)
+    for name in ("_rows", "_dense", "_gate"):
+        monkeypatch.setattr(moe.block, name, lambda t, *a: None if t is None else A)
+    n, e, c, t = norm(), embed(), ce(), torch.zeros(8, 64)
+    grads = moe.GradList([])
+    for ws in (torch.zeros(1 << 16, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8).expand(4096)):
+        for f, a, kw in ((moe.block_norm_backward, (n, t, t, ws), dict(w_pre=t, d_normed=t, d_w_pre=t)),
+                         (moe.clip_grad_norm, (grads, 1.0, t, ws), {}),
+                         (moe.embedding_forward, (e, t, t, t, ws), {}),
+                         (moe.embedding_backward, (e, t, t, t, ws), {}),
+                         (moe.linear_ce_forward, (c, t, t, t, t, t, ws), {}),
+                         (moe.linear_ce_backward, (c, t, t, t, t, t, t, t, ws), {})):
+            with pytest.raises(ValueError, match="workspace"):
+                f(*a, **kw)
+    assert not called
