@@ -30,6 +30,14 @@ def _dtype(d) -> int:
     return _DTYPES[d]
 
 
+def _sizes(*n, bits=32):
+    """The sizes as integers that fit a field of so many bits (ctypes would cut them)."""
+    n = tuple(int(i) for i in n)
+    if any(i.bit_length() >= bits for i in n):
+        raise ValueError(f"sizes {n}: beyond {bits} bits")
+    return n
+
+
 class NormProblem(ctypes.Structure):
     """Mirror of ``moe_norm_problem``; made with ``NormProblem.make``."""
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32),
@@ -49,15 +57,14 @@ class NormProblem(ctypes.Structure):
         The row strides (elements) are 0 for dense rows."""
         if gate not in GATES:
             raise ValueError(f"gate must be one of {sorted(GATES)}")
-        T, H = int(T), int(H)
+        T, H = _sizes(T, H)
+        lds = _sizes(ld_branch, ld_residual, ld_residual_out, ld_normed, bits=64)
         p = cls(T, H, _dtype(branch_dtype), _dtype(residual_dtype), _dtype(weight_dtype),
                 GATES[gate], float(eps), float(weight_offset), float(residual_scale),
-                float(branch_scale), int(ld_branch), int(ld_residual), int(ld_residual_out),
-                int(ld_normed))
+                float(branch_scale), *lds)
         p._rows, p._cols = (T, H), (H,)
         p._b, p._r, p._w = branch_dtype, residual_dtype, weight_dtype
-        p._ld = tuple((int(ld) or H, 1) for ld in (ld_branch, ld_residual, ld_residual_out,
-                                                   ld_normed))
+        p._ld = tuple((ld or H, 1) for ld in lds)
         p._gate = {"none": None, "channel": (H,), "token": (T,), "element": (T, H)}[gate]
         return p
 
@@ -70,7 +77,7 @@ class EmbedProblem(ctypes.Structure):
 
     @classmethod
     def make(cls, T, V, H, table_dtype=torch.bfloat16, out_dtype=torch.bfloat16, scale=1.0):
-        p = cls(int(T), int(V), int(H), _dtype(table_dtype), _dtype(out_dtype), float(scale))
+        p = cls(*_sizes(T, V, H), _dtype(table_dtype), _dtype(out_dtype), float(scale))
         p._ids, p._out, p._table = (p.T,), (p.T, p.H), (p.V, p.H)
         p._t, p._o = table_dtype, out_dtype
         return p
@@ -83,7 +90,7 @@ class CEProblem(ctypes.Structure):
 
     @classmethod
     def make(cls, T, H, V, logit_scale=1.0):
-        p = cls(int(T), int(H), int(V), float(logit_scale))
+        p = cls(*_sizes(T, H, V), float(logit_scale))
         p._rows, p._x, p._w = (p.T,), (p.T, p.H), (p.V, p.H)
         return p
 

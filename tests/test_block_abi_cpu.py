@@ -256,3 +256,19 @@ def test_binding_refuses_workspaces_that_are_not_on_the_gpu(monkeypatch):
             with pytest.raises(ValueError, match="workspace"):
                 f(*a, **kw)
     assert not called
+
+
+@pytest.mark.parametrize("make", [
+    lambda n: moe.NormProblem.make(n, 64), lambda n: moe.NormProblem.make(8, n),
+    lambda n: moe.NormProblem.make(8, 64, ld_branch=n << 32),
+    lambda n: moe.NormProblem.make(8, 64, ld_residual=n << 32),
+    lambda n: moe.NormProblem.make(8, 64, ld_residual_out=n << 32),
+    lambda n: moe.NormProblem.make(8, 64, ld_normed=n << 32),
+    lambda n: moe.EmbedProblem.make(n, 100, 64), lambda n: moe.EmbedProblem.make(8, n, 64),
+    lambda n: moe.EmbedProblem.make(8, 100, n), lambda n: moe.CEProblem.make(n, 64, 100),
+    lambda n: moe.CEProblem.make(8, n, 100), lambda n: moe.CEProblem.make(8, 64, n)])
+def test_problems_refuse_sizes_beyond_their_fields(make):
+    """A size is not taken modulo 2^32: 2^32 + 8 rows would be 8."""
+    for n in ((1 << 32) + 8, 1 << 31):
+        with pytest.raises(ValueError):
+            make(n)
