@@ -233,3 +233,47 @@ def test_binding_refuses_wrong_tensors():
               (ids, t, o.cpu()), (ids, t, torch.zeros(16, 4, dtype=BF, device=DEV).t())):
         with pytest.raises(ValueError):
             moe.embedding_forward(p, *a)
+
+
+def pieces_of(p):
+    """The pieces of the sorted list, from what the workspace holds past the lists."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    lists = 256 + 2 * up(4 * p.T) + up(4 * (p.V + 1))
+    part = moe.alloc_embedding_workspace(p).numel() - lists
+    return next(n for n in (8, 16, 32) if up(8 * -(-p.T // n) * p.H) == part)
+
+
+# pieces of 16 and of 32 tokens, which sizes of training take: rows of wide accesses and of single
+# elements, and every number of tokens in flight
+@pytest.mark.parametrize("T,piece", [(4500, 16), (10000, 32), (10015, 32)])
+@pytest.mark.parametrize("H", [4104, 4101])
+@pytest.mark.parametrize("tt,to", [(BF, BF), (F32, F32), (F32, BF)])
+def test_longer_pieces(T, piece, H, tt, to):
+    V = 701
+    p = moe.EmbedProblem.make(T, V, H, tt, to, 0.7)
+    assert pieces_of(p) == piece
+    g = torch.Generator(device=DEV).manual_seed(T + H)
+    d_out = torch.randn(T, H, generator=g, device=DEV).to(to)
+    # runs that end at, one before and one behind the pieces' ends; single tokens; one long run
+    edges = [n for q in range(1, 12) for n in (q * piece - 1, q * piece, q * piece + 1)]
+    runs, at = [], 0
+    for e in edges:
+        runs.append(e - at)
+        at = e
+    runs += [1] * 200 + [3000] + [5, 11] * 20
+    bounded = torch.repeat_interleave(torch.arange(len(runs)), torch.tensor(runs))
+    bounded = torch.cat([bounded, torch.full((T - bounded.numel(),), 400)])
+    bounded = bounded[torch.randperm(T, generator=torch.Generator().manual_seed(T))]
+    for ids in (bounded.to(torch.int32), ids_of(T, V, "mixed"), ids_of(T, V, "one"),
+                ids_of(T, V, "few"), ids_of(T, V, "uniform")):
+        d_table = torch.full((V, H), float("nan"), dtype=tt, device=DEV)
+        moe.embedding_backward(p, ids.to(DEV), d_out, d_table, moe.alloc_embedding_workspace(p))
+        at = ids.to(DEV).long()
+        ok = at >= 0
+        d = d_out.double()[ok] * 0.7
+        want, mag = (torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, at[ok], t)
+                     for t in (d, d.abs()))
+        n = torch.bincount(at[ok], minlength=V).double()[:, None]
+        tol = rounding(tt) * want.abs() + (n + 2) * 2.0 ** -24 * mag
+        err = (d_table.double() - want).abs()
+        assert (err <= tol).all(), float((err / tol.clamp(min=1e-30)).max())
