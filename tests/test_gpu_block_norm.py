@@ -422,3 +422,43 @@ def test_binding_refuses_wrong_tensors():
             moe.block_norm_forward(p, r, **{**dict(w_pre=w, normed=n), **bad})
     with pytest.raises(moe.MoEError):
         moe.block_norm_forward(p, r)  # nothing to compute
+
+
+@pytest.mark.parametrize("kind", ["channel", "token", "element"])
+@pytest.mark.parametrize("H,ld", [(200, 0), (203, 0), (1000, 0), (1003, 0), (2304, 0), (2301, 0),
+                                  (2301, 2307)])
+@pytest.mark.parametrize("T", [9, 700])
+def test_infinite_gates(T, H, ld, kind):
+    """An infinite gate value, and a NaN in another row: the forward has infinities and NaN where
+    the formula in 64 bits has them, and the backward is finite where it is (sums of infinities of
+    both signs are NaN in one order of the factors and infinite in another)."""
+    s = inputs(T, H, BF, F32, F32, kind, seed=5, ld=ld)
+    at = {"channel": H - 2, "token": 6, "element": (6, H - 2)}[kind]
+    s["gate"][at] = float("inf")
+    s["branch"][4, 5] = float("nan")
+    p = problem(T, H, BF, F32, F32, kind, 0.0, 0.9, 0.5, ld)
+    d = {k: dev(v, ld) if k not in ("w_post", "w_pre", "gate") else dev(v) for k, v in s.items()}
+    kw = dict(branch=d["branch"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"])
+    out, n = like(s["residual"], ld)[0], like(s["branch"], ld)[0]
+    moe.block_norm_forward(p, d["residual"], residual_out=out, normed=n, **kw)
+    want, mag, nw, n_mag = ref_forward(s, kind, 0.0, 0.9, 0.5)
+    for got, ref, m, dtype in ((out, want, mag, F32), (n, nw, n_mag, BF)):
+        g = got.double().cpu()
+        assert torch.equal(torch.isnan(g), torch.isnan(ref))
+        inf = torch.isinf(ref)
+        assert torch.equal(torch.isinf(g), inf) and torch.equal(g[inf], ref[inf])
+        fine = torch.isfinite(ref)
+        m = torch.where(torch.isfinite(m), m, ref.abs())  # a finite value's terms may be infinite
+        close(got.cpu()[fine], ref[fine], m[fine], dtype)
+    o = {k: like(s[k], ld if k in ("branch", "residual") else 0)[0]
+         for k in ("branch", "residual", "w_post", "w_pre", "gate")}
+    moe.block_norm_backward(p, d["residual"], o["residual"], moe.alloc_block_norm_workspace(p),
+                            d_normed=d["d_normed"], d_residual_out=d["d_residual_out"],
+                            d_branch=o["branch"], **kw,
+                            **{"d_" + k: o[k] for k in ("w_post", "gate", "w_pre")})
+    for k, (ref, m) in ref_backward(s, kind, 0.0, 0.9, 0.5).items():
+        fine = torch.isfinite(ref)
+        assert torch.equal(torch.isfinite(o[k]).cpu(), fine), k
+        dtype = BF if k == "branch" else F32
+        close(o[k].cpu()[fine], ref[fine], m[fine], dtype,
+              sums=T if ref.shape == (H,) else H if ref.dim() == 1 else 1)
