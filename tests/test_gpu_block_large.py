@@ -153,3 +153,33 @@ def test_captured_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(want, (loss, lse, dy, norm, *outs)):
             assert torch.equal(a, b)
+
+
+def test_nothing_is_allocated():
+    """The second run of every operator takes no device memory, from torch or from the driver."""
+    T, H, V = 777, 1000, 5003
+    x, w = (torch.randn(n, H, device=DEV).to(BF) for n in (T, V))
+    ids = torch.randint(-1, V, (T,), device=DEV, dtype=torch.int32)
+    pe, pc = moe.EmbedProblem.make(T, V, H), moe.CEProblem.make(T, H, V)
+    pn = moe.NormProblem.make(T, H, weight_dtype=F32)
+    scale = torch.ones(H, device=DEV)
+    loss, lse, d_loss, norm = *(torch.ones(T, device=DEV) for _ in range(3)), torch.ones(2, device=DEV)
+    a, b, c, d = (torch.empty_like(x) for _ in range(4))
+    dw, g = torch.empty_like(w), [torch.empty_like(scale) for _ in range(2)]
+    lst = moe.GradList([dw, *g])
+    ws = [moe.alloc_embedding_workspace(pe), moe.alloc_block_norm_workspace(pn),
+          moe.alloc_linear_ce_workspace(pc, backward=True), moe.alloc_clip_workspace(lst)]
+
+    def once():
+        moe.embedding_forward(pe, ids, w, a, ws=ws[0])
+        moe.block_norm_forward(pn, a, branch=x, w_post=scale, w_pre=scale, residual_out=b, normed=c)
+        moe.linear_ce_forward(pc, c, w, ids, loss, lse, ws[2])
+        moe.linear_ce_backward(pc, c, w, ids, lse, d_loss, d, dw, ws[2])
+        moe.block_norm_backward(pn, b, a, ws[1], branch=x, w_post=scale, w_pre=scale, d_normed=d,
+                                d_branch=c, d_w_post=g[0], d_w_pre=g[1])
+        moe.embedding_backward(pe, ids, a, dw, ws[0])
+        moe.clip_grad_norm(lst, 1.0, norm, ws[3])
+        torch.cuda.synchronize()
+        return torch.cuda.mem_get_info()[0], torch.cuda.memory_stats()["allocation.all.allocated"]
+
+    assert once() == once()
