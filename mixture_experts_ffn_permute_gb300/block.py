@@ -174,10 +174,10 @@ def _gate(t: Optional[torch.Tensor], p):
 
 def _workspace(ws: torch.Tensor):
     """The address and the bytes of a workspace."""
-    if not ws.is_cuda or not ws.is_contiguous():
+    if not (ws.is_cuda and ws.is_contiguous()):
         raise ValueError(f"expected a contiguous workspace on the GPU, got one with strides "
                          f"{ws.stride()} on {ws.device}")
-    return ws.data_ptr(), ws.numel() * ws.itemsize
+    return ws.data_ptr(), ws.nbytes
 
 
 # the current stream's handle without a Stream object around it (3 us of a call of 11)
