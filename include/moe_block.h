@@ -98,13 +98,14 @@ MOE_API int moe_block_norm_backward(const moe_norm_problem* p, const void* branc
                                     void* stream);
 
 /* ---- Gradient clipping by the global norm ---------------------------------
- *   norm = grad_scale * sqrt(sum over all tensors and elements of grad^2)
+ *   norm = |grad_scale| * sqrt(sum over all tensors and elements of grad^2)
  *   coef = min(1, max_norm / (norm + eps))
  *   out  = grad * (grad_scale * coef)
  * grad_scale undoes a loss scale in the same pass.  Squares are summed in
- * fp32 over at most 128 elements of one thread, those sums in fp64; a
- * thread's sum that overflows fp32 or falls below 2^-80 is taken again in
- * fp64, so the norm overflows only where it is above the fp32 range itself. */
+ * fp32 over at most 65 elements of one thread, those sums in fp64; a thread's
+ * sum that overflows fp32 or falls below 2^-80 (or to 0, of elements that are
+ * not) is taken again in fp64, so the norm leaves the fp32 range only where it
+ * is outside it itself. */
 typedef struct moe_grad_tensor {
   const void* grad; /* device, numel elements, dense; any element alignment */
   void* out;        /* device, same type; may be grad; NULL: counted, not written */
@@ -165,6 +166,9 @@ MOE_API int moe_embedding_backward(const moe_embed_problem* p, const int32_t* id
  *   d z_tv = (d_loss[t] + d_lse[t]) exp(z_tv - lse[t]) - d_loss[t] [v = labels[t]]
  *   dx[t]  = logit_scale * sum_v d z_tv w_v
  *   dw[v]  = logit_scale * sum_t d z_tv x_t
+ * A masked token has a loss of 0 and an lse, and its weight in dw is
+ * d_lse[t] exp(z - lse) or 0; as the formula has it, 0 times NaN is NaN, so the x
+ * of a masked token has to be finite where dw is wanted.
  * x [T, H] and w [V, H] bf16, dense, 16-byte aligned; H a multiple of 8;
  * loss, lse, d_loss, d_lse fp32.  The backward recomputes the logits in pieces
  * of the vocabulary and rounds d z / max |d_loss| to bf16 for its two products,

@@ -86,10 +86,6 @@ __device__ __forceinline__ Chunk chunk_at(const GradTable<kCap>& t, int c) {
   return k;
 }
 
-__device__ __forceinline__ uint4 load16(const void* p) {
-  return *static_cast<const uint4*>(p);
-}
-
 template <bool kF32>
 __device__ __forceinline__ float square16(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -284,7 +280,7 @@ grad_scale_kernel(const __grid_constant__ GradTable<kCap> t, const double* __res
   }
 }
 
-// Fills the table with tensors[0 .. n); false if a tensor is too large.
+// Fills the table with tensors[0 .. n).
 template <int kCap>
 void fill_table(GradTable<kCap>& t, const moe_grad_tensor* g, int n) {
   t.n = n;

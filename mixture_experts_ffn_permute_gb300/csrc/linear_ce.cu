@@ -10,8 +10,9 @@
 // single CTAs (one_cta).  Per token and vocabulary tile 8 bytes leave
 // the kernel instead of 2 N of logits.
 //
-// Backward, in pieces of the vocabulary whose logit gradients (bf16) fit in
-// L2:
+// Backward, in pieces of the vocabulary whose logit gradients (bf16) take 128 MB
+// (about what L2 holds; W and x pass through it too, and W and G are read about
+// twice from HBM):
 //   G  = a exp(z - lse) - b [v = label]  the forward's GEMM with another
 //                                        epilogue, [T, piece] to the workspace
 //   dx += S G W_piece    A = G K-major, B = W_piece read MN-major (as stored)
@@ -36,7 +37,9 @@
 // was 1e-6 of its value too small.  The forward therefore takes the
 // accumulator out every 1024 of K and adds the parts in registers (128
 // columns a thread, eight epilogue warps), while the tensor core fills the
-// other accumulator.
+// other accumulator.  The backward's logits keep all of K there: their exponents
+// are off by that much from the forward's, a thousandth of the rounding of G to
+// bf16 for logits of order one.
 //
 // Warp roles (one CTA per SM, tiles dealt to the pairs in a fixed order):
 //   warp 0     TMA producer: 3 stages of 32 KB of A and 32 KB of B per CTA, up to 8
@@ -47,12 +50,14 @@
 //              through swizzled staging and bulk-tensor stores
 // Every wait is bounded (ptx.cuh).
 //
-// Measured (one GB300): T=4096 H=4096 V=32000 forward 0.57 ms (1890 TFLOP/s),
-// backward 1.80 ms (1790, its three products), the rate a plain library GEMM
-// reaches there under the power cap; with few tokens the forward streams W:
-// T=4 H=2048 V=32000 29 us with the join (131 MB, of which 20 us at HBM rate;
-// launches, set-up and the join are the rest), T=4 H=4096 V=128000 167 us (6.3
-// TB/s).
+// Measured (one GB300): T=4096 H=4096 V=32000, runs of 20 of one direction:
+// forward 0.56 ms (1920 TFLOP/s), backward 1.79 ms (1800, its three products);
+// both in turn, where the board's power cap counts, 2.5 to 2.6 ms (1640 to 1720
+// for the four products; a plain library GEMM sustains 1695).  With few tokens
+// the forward streams W: T=4 H=2048 V=32000 29 us with the join (131 MB, 19 us at
+// HBM rate; 250 tiles on 152 CTAs, so that some take 256 rows of W where an even
+// share is 210; launches, set-up and the join are the rest), T=4 H=4096 V=128000
+// 165 us (6.4 TB/s).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -774,7 +779,8 @@ bool make_map(CUtensorMap* map, const void* base, long rows, long cols, long ld,
 // against pairs, us: T=1 H=64 V=32000 10.8 against 13.8 / 24.2 against 27.4; T=8
 // H=128 V=50021 12.9, 17.8 / 37.7, 42.0; T=32 H=256 V=32000 11.3, 15.9 / 30.1,
 // 33.4; T=128 H=1024 V=32000 22.6, 25.3 / 75.6, 77.6; T=4 H=4096 V=128000 172,
-// 176 / 780, 775.  Rows that are not whole planes copy slowly, and tiles half
+// 176 / 780, 775 (the only row where one of the two, the backward, is slower, by
+// less than 1%).  Rows that are not whole planes copy slowly, and tiles half
 // as wide copy those of x twice as often: T=96 H=1000 V=50021 44.7, 39.2 / 115,
 // 113; T=128 H=8 V=200000 141, 93 / 251, 209: pairs there.
 bool one_cta(const moe_ce_problem* p) { return p->T <= 128 && p->H % 64 == 0; }
@@ -862,9 +868,10 @@ constexpr size_t kCeHeader = 256;
 constexpr size_t kUnitOffset = 64;  // of s in the header
 // A piece's logit gradients: 128 MB, and 4096 vocabulary rows at least.  Larger
 // pieces mean fewer passes over dx's fp32 sums and fuller last waves, smaller
-// ones less workspace and more of the piece in L2.  The backward with 32, 64,
-// 128, 256 MB and one piece: T=4096 H=4096 V=32000 2.16, 1.87, 1.79, 1.73,
-// 1.74 ms; T=2048 H=1024 V=131072 1.64, 1.22, 1.11, 1.03, 1.00 ms.
+// ones less workspace.  The backward with 32, 64, 128, 256 MB and one piece:
+// T=4096 H=4096 V=32000 2.16, 1.87, 1.79, 1.73, 1.74 ms; T=2048 H=1024 V=131072
+// 1.64, 1.22, 1.11, 1.03, 1.00 ms.  128 MB is not the fastest, it is what 3% and 10%
+// more time buy: a workspace that does not double.
 constexpr size_t kPieceBytes = 128u << 20;
 constexpr int kPieceRows = 4096;
 
