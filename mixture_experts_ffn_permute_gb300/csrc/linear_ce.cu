@@ -52,7 +52,7 @@
 //
 // Measured (one GB300): T=4096 H=4096 V=32000, runs of 20 of one direction:
 // forward 0.56 ms (1920 TFLOP/s), backward 1.79 ms (1800, its three products);
-// both in turn, where the board's power cap counts, 2.5 to 2.6 ms (1640 to 1720
+// both in turn, where the board's power cap counts, 2.5 to 2.65 ms (1620 to 1720
 // for the four products; a plain library GEMM sustains 1695).  With few tokens
 // the forward streams W: T=4 H=2048 V=32000 29 us with the join (131 MB, 19 us at
 // HBM rate; 250 tiles on 152 CTAs, so that some take 256 rows of W where an even
