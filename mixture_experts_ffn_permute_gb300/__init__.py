@@ -13,8 +13,9 @@ function names mirror the C entry points of ``include/moe_ffn.h``:
     forward_routed        -> moe_forward_routed
 
 The operators around the layer (``include/moe_block.h``: embedding, block
-norms, linear cross entropy, gradient clipping) are in ``block.py`` and are
-reached from here by the same names.
+norms, linear cross entropy, gradient clipping) are in ``block.py``, the expert
+router and the experts' products in 8 bits (``include/moe_experts.h``) in
+``experts.py``; both are reached from here by the same names.
 
 There is no CPU fallback: if the library is missing or a call returns an
 error status, a ``MoEError`` is raised.
@@ -112,8 +113,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_forward_fp8_nvfp4": ([pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                                    vp], ci),
     }
-    from .block import SIGS
-    for name, (args, res) in {**sigs, **SIGS}.items():
+    from . import block, experts
+    for name, (args, res) in {**sigs, **block.SIGS, **experts.SIGS}.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
@@ -402,5 +403,7 @@ __all__ = ["Problem", "MoEError", "MoEFFN", "load", "workspace_size", "alloc_wor
 
 from . import block as _block  # noqa: E402  (uses the names above)
 from .block import *  # noqa: E402,F401,F403
+from . import experts as _experts  # noqa: E402
+from .experts import *  # noqa: E402,F401,F403
 
-__all__ += _block.__all__
+__all__ += _block.__all__ + _experts.__all__

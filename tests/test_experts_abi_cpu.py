@@ -1,0 +1,166 @@
+"""CPU checks of the entry points of include/moe_experts.h: bad arguments are refused on the host,
+before any CUDA call (no kernel is launched here)."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_ffn_permute_gb300 as moe
+from mixture_experts_ffn_permute_gb300 import _build
+
+A = 1 << 20  # a 256-byte aligned address that is never dereferenced
+BIG = 1 << 50
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return moe.load()
+
+
+def changed(p, fields):
+    for k, v in fields.items():
+        setattr(p, k, v)
+    return ctypes.byref(p)
+
+
+# ------------------------------------------------------------------ router
+def router(lib, forward=True, tensors=(), **fields):
+    p = changed(moe.RouterProblem.make(8, 64, 4, groups=8), fields)
+    a = dict(logits=A, bias=A, idx=A, w=A) if forward else dict(logits=A, idx=A, dw=A, dl=A)
+    a.update(dict(tensors))
+    return (lib.moe_router_forward if forward else lib.moe_router_backward)(p, *a.values(), None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(T=-1), 1), (dict(E=0), 1), (dict(k=0), 1), (dict(k=65), 1), (dict(logits_dtype=2), 1),
+    (dict(score=2), 1), (dict(score=-1), 1), (dict(groups=0), 1), (dict(groups=7), 1),
+    (dict(topk_groups=0), 1), (dict(topk_groups=9), 1), (dict(group_top=0), 1),
+    (dict(group_top=3), 1), (dict(groups=64, topk_groups=64), 2), (dict(E=1032), 2),
+    (dict(E=128, k=33), 2), (dict(topk_groups=1, k=9), 1), (dict(scale=float("inf")), 1),
+    (dict(scale=float("nan")), 1), (dict(ld_logits=63), 1), (dict(ld_logits=-64), 1),
+    (dict(ld_logits=1 << 41), 2), (dict(E=8, k=1, group_top=2), 1)])
+def test_router_rejects_bad_problems(lib, fields, code):
+    assert router(lib, **fields) == code
+    assert router(lib, forward=False, **fields) == code
+
+
+@pytest.mark.parametrize("forward", [True, False])
+def test_router_rejects_bad_tensors(lib, forward):
+    names = ("logits", "idx", "w") if forward else ("logits", "idx", "dw", "dl")
+    for name in names:
+        assert router(lib, forward, {name: None}) == 1
+        assert router(lib, forward, {name: A + 2}) == 3
+    assert router(lib, forward, {"logits": A + 1}, logits_dtype=0) == 3
+    if forward:
+        assert router(lib, forward, {"bias": A + 1}) == 3
+    assert router(lib, forward, {n: None for n in names}, T=0) == 0
+    assert moe.last_launch_count() == 0
+    fn = lib.moe_router_forward if forward else lib.moe_router_backward
+    assert fn(None, A, A, A, A, None) == 1
+
+
+def test_router_problem_rejects_unknown_options():
+    with pytest.raises(ValueError):
+        moe.RouterProblem.make(4, 8, 2, score="tanh")
+    with pytest.raises(ValueError):
+        moe.RouterProblem.make(4, 8, 2, logits_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        moe.RouterProblem.make(1 << 32, 8, 2)
+
+
+# ------------------------------------------------------------------ quantisation
+def rows(lib, tensors=(), **fields):
+    p = changed(moe.QuantProblem.make(8, 256), fields)
+    a = dict(src=A, codes=A, scales=A)
+    a.update(dict(tensors))
+    return lib.moe_fp8_quantize_rows(p, *a.values(), None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(T=-1), 1), (dict(H=0), 1), (dict(H=264), 2), (dict(H=1 << 29), 2), (dict(src_dtype=2), 1),
+    (dict(glu_interleave=-16), 1), (dict(swiglu=1, glu_interleave=8), 2),
+    (dict(swiglu=1, glu_interleave=48), 2), (dict(ld_src=255), 1), (dict(ld_src=-256), 1),
+    (dict(swiglu=1, ld_src=256), 1), (dict(ld_src=260), 2), (dict(ld_src=1 << 41), 2),
+    (dict(T=(1 << 30) + 5), 2)])
+def test_quantize_rows_rejects_bad_problems(lib, fields, code):
+    assert rows(lib, **fields) == code
+
+
+def test_quantize_rows_rejects_bad_tensors(lib):
+    for name in ("src", "codes", "scales"):
+        assert rows(lib, {name: None}) == 1
+        assert rows(lib, {name: A + 2}) == 3
+    assert rows(lib, {"src": A + 8}) == rows(lib, {"codes": A + 8}) == 3
+    assert rows(lib, {n: None for n in ("src", "codes", "scales")}, T=0) == 0
+    assert lib.moe_fp8_quantize_rows(None, A, A, A, None) == 1
+
+
+def weights(lib, tensors=(), **fields):
+    p = changed(moe.QuantWeightsProblem.make(2, 256, 384), fields)
+    a = dict(src=A, codes=A, scales=A, codes_t=A, scales_t=A)
+    a.update(dict(tensors))
+    return lib.moe_fp8_quantize_weights(p, *a.values(), None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(E=-1), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(src_dtype=2), 1), (dict(K=388), 2),
+    (dict(N=250), 2), (dict(E=1 << 30), 2), (dict(N=1 << 30, K=1 << 30), 2)])
+def test_quantize_weights_rejects_bad_problems(lib, fields, code):
+    assert weights(lib, **fields) == code
+
+
+def test_quantize_weights_rejects_bad_tensors(lib):
+    for name in ("src", "codes", "scales", "codes_t", "scales_t"):
+        assert weights(lib, {name: None}) == 1  # (one of the transposed alone as well)
+        assert weights(lib, {name: A + 2}) == 3
+    assert weights(lib, {n: None for n in ("src", "codes", "scales")}, E=0) == 0
+    assert lib.moe_fp8_quantize_weights(None, *[A] * 5, None) == 1
+
+
+# ------------------------------------------------------------------ product
+def matmul(lib, tensors=(), n=BIG, **fields):
+    p = changed(moe.FP8Problem.make(64, 256, 384, 4), fields)
+    a = dict(x=A, xs=A, w=A, ws=A, offsets=A, out=A, work=A)
+    a.update(dict(tensors))
+    return lib.moe_fp8_matmul(p, *a.values(), n, None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(M=-1), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(E=0), 1), (dict(out_dtype=2), 1),
+    (dict(E=1025), 2), (dict(K=392), 2), (dict(M=(1 << 30) + 1), 2), (dict(N=(1 << 30) + 1), 2),
+    (dict(K=(1 << 30) + 16), 2), (dict(M=1 << 30, N=1 << 20), 2), (dict(N=1 << 20, K=1 << 21), 2)])
+def test_matmul_rejects_bad_problems(lib, fields, code):
+    assert matmul(lib, **fields) == code
+    p = moe.FP8Problem.make(64, 256, 384, 4)
+    assert lib.moe_fp8_matmul_workspace_size(changed(p, fields)) == 0
+
+
+def test_matmul_rejects_bad_tensors(lib):
+    for name in ("x", "xs", "w", "ws", "out", "work"):
+        assert matmul(lib, {name: None}) == 1
+        assert matmul(lib, {name: A + 2}) == 3
+    assert matmul(lib, {"offsets": None}) == 1  # four experts
+    assert matmul(lib, {"offsets": A + 2}) == 3
+    for name in ("x", "w", "out"):
+        assert matmul(lib, {name: A + 8}) == 3
+    assert matmul(lib, {"work": A + 128}) == 3
+    assert matmul(lib, n=16) == 4
+    assert matmul(lib, {n: None for n in ("x", "xs", "w", "ws", "out", "work")}, M=0) == 0
+    assert lib.moe_fp8_matmul(None, *[A] * 7, BIG, None) == 1
+    assert lib.moe_fp8_matmul_workspace_size(None) == 0
+
+
+# ------------------------------------------------------------------ binding
+def test_binding_rejects_tensors_that_are_not_the_problems():
+    p = moe.RouterProblem.make(4, 8, 2)
+    cpu = torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        moe.router_forward(p, cpu, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+    q = moe.QuantProblem.make(4, 16)
+    with pytest.raises(ValueError):
+        moe.fp8_quantize_rows(q, torch.zeros(4, 16), None, None)
+    with pytest.raises(moe.MoEError):
+        moe.alloc_fp8_matmul_workspace(moe.FP8Problem.make(4, 8, 24))
+    with pytest.raises(ValueError):
+        moe.FP8Experts(torch.zeros(2, 64, 256), torch.zeros(2, 256, 48), 1)
