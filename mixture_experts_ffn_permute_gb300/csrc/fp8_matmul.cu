@@ -208,6 +208,26 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// Arrival on a barrier of the pair that hands over no memory.
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
+
+// Until the loads from TMEM have come; the values take part, so that their uses
+// stay behind it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 struct Maps {
   CUtensorMap x, w;
 };
@@ -357,13 +377,35 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
       Pair acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-      constexpr int kAhead = 4;  // factors on their way
+      // The next block's sums are complete: the accumulator's columns.
+      auto wait_full = [&]() {
+        go = __all_sync(0xffffffffu, mbar_wait(&tfull[seg & 1], (seg >> 1) & 1, p.status));
+        tc_fence_after();
+        return t_lane + (seg & 1) * 256;
+      };
+      // They have been read (the leader's barrier; nothing else is handed over).
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair) arrive_remote_relaxed(tempty_leader + (seg & 1) * 8);
+          else mbar_arrive(&tempty[seg & 1]);
+        }
+        ++seg;
+      };
+      // A step is 32 columns of a block: the next step's sums are on their way
+      // from TMEM while this one's are scaled and added, and the accumulator is
+      // free as soon as its last ones have come.
+      constexpr int kSteps = kCols / 32;
+      constexpr int kAhead = 2;  // factors on their way
       float fx[kAhead], fw[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         fx[j] = j < p.kblocks ? __ldg(xs + j) : 0.f;
         fw[j] = j < p.kblocks ? __ldg(ws + j) : 0.f;
       }
+      uint32_t a[2][32], t = wait_full();
+      if (go && live) tmem_ld_32x32b_x32(t, a[0]);
       for (int kb0 = 0; go && kb0 < p.kblocks; kb0 += kAhead) {
         float f[kAhead];
 #pragma unroll
@@ -375,37 +417,32 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          if (kb0 + j >= p.kblocks) break;
-          go = __all_sync(0xffffffffu, mbar_wait(&tfull[seg & 1], (seg >> 1) & 1, p.status));
-          if (!go) {
-            if (lane == 0) *abort_flag = 1;
-            break;
-          }
-          tc_fence_after();
-          if (live) {
-            const Pair f2 = pair_of(f[j], f[j]);
-            const uint32_t t = t_lane + (seg & 1) * 256;
+          if (!go || kb0 + j >= p.kblocks) break;
+          const Pair f2 = pair_of(f[j], f[j]);
 #pragma unroll
-            for (int q = 0; q < kCols / 32; ++q) {
-              uint32_t a[32];
-              tmem_ld_32x32b_x32(t + 32 * q, a);
-              tmem_ld_wait();
+          for (int q = 0; q < kSteps; ++q) {
+            const int here = (j * kSteps + q) & 1;
+            if (live) tmem_ld_wait_for(a[here]);
+            if (q + 1 < kSteps) {
+              if (live) tmem_ld_32x32b_x32(t + 32 * (q + 1), a[here ^ 1]);
+            } else {
+              release();
+              if (kb0 + j + 1 < p.kblocks) {
+                t = wait_full();
+                if (go && live) tmem_ld_32x32b_x32(t, a[here ^ 1]);
+              }
+            }
+            if (live) {
 #pragma unroll
               for (int n = 0; n < 16; ++n)
                 acc[q * 16 + n] = pair_fma(
-                    pair_of(__uint_as_float(a[2 * n]), __uint_as_float(a[2 * n + 1])), f2,
+                    pair_of(__uint_as_float(a[here][2 * n]), __uint_as_float(a[here][2 * n + 1])), f2,
                     acc[q * 16 + n]);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (kPair) pair::arrive_remote(tempty_leader + (seg & 1) * 8);
-            else mbar_arrive(&tempty[seg & 1]);
-          }
-          ++seg;
         }
       }
+      if (!go && lane == 0) *abort_flag = 1;
       if (!go) break;
       if (!live || !row_ok) continue;
       const int ncols = min(kCols, p.N - col);
