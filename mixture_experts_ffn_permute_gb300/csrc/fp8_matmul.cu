@@ -38,17 +38,24 @@ namespace {
 
 constexpr int kBlk = 128;                       // a scale's extent along K and N
 constexpr uint32_t kPlane = 128 * kBlk;         // 128 rows x 128 codes, 16 KB
-constexpr uint32_t kStageBytes = 4 * kPlane;    // two blocks of both operands
-constexpr int kStages = 3;
+constexpr int kMaxStages = 6;
+constexpr uint32_t kRing = 3 * 4 * kPlane;      // stages of two blocks of both operands
 constexpr int kMaxE = MOE_MAX_EXPERTS;
 constexpr int kGroupM = 8;  // row tiles whose sweep over the columns shares weight tiles in L2
+constexpr int kNarrow = 128;                    // rows of a narrow tile at most
+constexpr int kBoxes = 4;                       // heights of its copies: 16, 32, 64, 128 rows
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;  // warps 0-3: copies, MMA, two idle
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // warps 0-3: copies, MMA (two), factors
 constexpr uint32_t kBarBytes = 256;
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + kBarBytes + 2 * (kMaxE + 1) * sizeof(int32_t);
+constexpr int kChunk = 8;                        // blocks whose factors come together
+constexpr uint32_t kFactors = kChunk * 2 * 128;  // [block][weight block][row]
+constexpr size_t kSmem = 1024 + kRing + kBarBytes + 2 * kFactors * sizeof(float) +
+                         2 * (kMaxE + 1) * sizeof(int32_t);
 static_assert(kSmem <= 232448, "shared memory budget");
+static_assert((2 * kMaxStages + 10) * 8 + 8 <= kBarBytes, "barrier area");
 // registers: a launch's 168 x 384, moved as 40 x 128 + 232 x 256
-static_assert(40 * 128 + 232 * 256 <= 168 * kThreads, "register split");
+constexpr int kRegsOther = 56, kRegsEpilogue = 224;
+static_assert(kRegsOther * 128 + kRegsEpilogue * 32 * kEpiWarps <= 168 * kThreads, "register split");
 
 struct MmParams {
   const int32_t* offsets;  // NULL: one expert, all rows
@@ -56,6 +63,9 @@ struct MmParams {
   const float* ws;
   void* out;
   int M, N, E, kblocks, nblocks, n_tiles;
+  int tile_rows;    // rows of a tile at most: 256 (pairs), or of a narrow one
+  int stages;       // of the ring
+  uint32_t x_stage; // bytes of a stage's rows in one CTA
   int planes;  // operands come as planes
   int f32;     // out
   int vec;     // 32-byte stores
@@ -138,7 +148,7 @@ __device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, bool p
 }
 
 // Expert offsets into s_off[E + 1] and the experts' first tiles into
-// s_tile[E + 1], tile heights of `rows`; the number of tiles (0, and the status,
+// s_tile[E + 1], tiles of `rows` rows; the number of tiles (0, and the status,
 // where the offsets decrease or leave [0, M]).  Every thread of the block.
 template <int kBlockThreads>
 __device__ __forceinline__ int build_tiles(const int32_t* offsets, int E, int M, int n_tiles,
@@ -184,22 +194,41 @@ __device__ __forceinline__ int build_tiles(const int32_t* offsets, int E, int M,
   return total;
 }
 
-// Where tile `i` lies: `e` only ever grows along a CTA's tiles.
-struct Cursor {
+// The tiles of a CTA (pair), in order: which expert's, and where.
+//
+// A wide tile (pairs alone) has 256 rows on the tensor core's M side and 256
+// columns on its N side.  A narrow one, an expert's last rows where they are at
+// most 128, has the weights on the M side and only as many rows as there are on
+// the N side: its tensor core and epilogue time goes with them, and the weights'
+// bytes are what is left.
+struct Tile {
   int e = 0, m = 0, n = 0;
-  __device__ __forceinline__ void at(int i, const int32_t* s_tile, int n_tiles) {
+  int row, left;  // first row, rows (at most the tile's)
+  bool narrow;
+  int half;       // narrow: rows per CTA, a multiple of 16
+  int box;        // rows per copy: 16 << index
+  // `e` only ever grows along a CTA's tiles
+  template <bool kPair>
+  __device__ __forceinline__ void at(int i, const MmParams& p, const int32_t* s_off,
+                                     const int32_t* s_tile) {
     while (s_tile[e + 1] <= i) ++e;
-    const int local = i - s_tile[e], m_tiles = (s_tile[e + 1] - s_tile[e]) / n_tiles;
+    const int local = i - s_tile[e], m_tiles = (s_tile[e + 1] - s_tile[e]) / p.n_tiles;
     if (m_tiles == 1) {
       m = 0;
       n = local;
-      return;
+    } else {
+      const int per = kGroupM * p.n_tiles, grp = local / per, within = local - grp * per;
+      const int size = min(kGroupM, m_tiles - grp * kGroupM);
+      n = within / size;
+      m = grp * kGroupM + (within - n * size);
     }
-    const int per = kGroupM * n_tiles, grp = local / per, within = local - grp * per;
-    const int size = min(kGroupM, m_tiles - grp * kGroupM);
-    n = within / size;
-    m = grp * kGroupM + (within - n * size);
+    row = s_off[e] + m * p.tile_rows;
+    left = min(s_off[e + 1] - row, p.tile_rows);
+    narrow = !kPair || left <= kNarrow;
+    half = kPair ? ((left + 1) / 2 + 15) & ~15 : (left + 15) & ~15;
+    box = !narrow ? 3 : half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
   }
+  __device__ __forceinline__ uint32_t x_plane() const { return 16u * kBlk << box; }
 };
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
@@ -229,7 +258,240 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
 }
 
 struct Maps {
-  CUtensorMap x, w;
+  CUtensorMap x[kBoxes], w;  // x in boxes of 16, 32, 64 and 128 rows
+};
+
+// Shared memory behind the ring, by constant offsets from its aligned base.
+struct Smem {
+  uint8_t* base;
+  __device__ __forceinline__ uint64_t* bar(int i) const {
+    return reinterpret_cast<uint64_t*>(base + kRing) + i;
+  }
+  __device__ __forceinline__ uint64_t* full(int s) const { return bar(s); }
+  __device__ __forceinline__ uint64_t* empty(int s) const { return bar(kMaxStages + s); }
+  __device__ __forceinline__ uint64_t* tfull(int b) const { return bar(2 * kMaxStages + b); }
+  __device__ __forceinline__ uint64_t* tempty(int b) const { return bar(2 * kMaxStages + 2 + b); }
+  __device__ __forceinline__ uint64_t* ffull(int b) const { return bar(2 * kMaxStages + 4 + b); }
+  __device__ __forceinline__ uint64_t* fempty(int b) const { return bar(2 * kMaxStages + 6 + b); }
+  // of either issuer
+  __device__ __forceinline__ uint64_t* drain(int b) const { return bar(2 * kMaxStages + 8 + b); }
+  __device__ __forceinline__ uint32_t* tmem_slot() const {
+    return reinterpret_cast<uint32_t*>(bar(2 * kMaxStages + 10));
+  }
+  __device__ __forceinline__ volatile int* abort_flag() const {
+    return reinterpret_cast<volatile int*>(tmem_slot() + 1);
+  }
+  __device__ __forceinline__ float* factors(int b) const {
+    return reinterpret_cast<float*>(base + kRing + kBarBytes) + b * kFactors;
+  }
+  __device__ __forceinline__ int32_t* off() const { return reinterpret_cast<int32_t*>(factors(2)); }
+  __device__ __forceinline__ int32_t* tile() const { return off() + kMaxE + 1; }
+};
+
+// What an epilogue warp carries from tile to tile.
+struct Turn {
+  int chunk = 0;             // chunks of factors so far
+  uint32_t buf = 0, par = 0; // the accumulator that comes next, and its phase
+  bool go = true;            // no wait has run out
+};
+
+// The epilogue warps' part of a tile.
+template <bool kPair>
+struct Epilogue {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kN = 128 * kCtas;
+  // Its way through a tile's blocks.
+  struct Walk : Turn {
+    const MmParams& p;
+    const Smem sm;
+    // Of this lane's waits: it skips them once one has run out, and the warp
+    // leaves together before the next factors.
+    bool ok = true;
+    int left = 0;  // blocks whose factors are there
+    const float* factors = nullptr;
+    __device__ __forceinline__ Walk(const MmParams& p_, Smem s, Turn t) : Turn(t), p(p_), sm(s) {}
+    // The next block's sums are in accumulator `buf`, their factors at `factors`.
+    __device__ __forceinline__ bool next(int kb) {
+      if (left == 0) {
+        ok = ok && mbar_wait(sm.ffull(chunk & 1), (chunk >> 1) & 1, p.status);
+        go = __all_sync(0xffffffffu, ok);
+        if (!go) return false;
+        factors = sm.factors(chunk & 1);
+        left = min(kChunk, p.kblocks - kb);
+      }
+      ok = ok && mbar_wait(sm.tfull(buf), par, p.status);
+      __syncwarp();
+      tc_fence_after();
+      return true;
+    }
+    // The accumulator has been read (nothing else is handed over).
+    __device__ __forceinline__ void release() {
+      tc_fence_before();
+      if ((threadIdx.x & 31) == 0) {
+        if (kPair) arrive_remote_relaxed(pair::mapa(smem_u32(sm.tempty(buf)), 0));
+        else mbar_arrive(sm.tempty(buf));
+      }
+      par ^= buf;
+      buf ^= 1;
+    }
+    // So have the factors, once a chunk is through.
+    __device__ __forceinline__ void release_factors() {
+      factors += 256;
+      if (--left == 0) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(sm.fempty(chunk & 1));
+        ++chunk;
+      }
+    }
+    __device__ __forceinline__ Turn done() {
+      go = __all_sync(0xffffffffu, ok);
+      return *this;
+    }
+  };
+
+  // A tile that this warp has no part of.
+  static __device__ __forceinline__ Turn idle(const MmParams& p, Smem sm, Turn turn) {
+    Walk walk(p, sm, turn);
+    for (int kb = 0; kb < p.kblocks; ++kb) {
+      if (!walk.next(kb)) break;
+      walk.release();
+      walk.release_factors();
+    }
+    return walk.done();
+  }
+
+  // A wide tile: a thread has a row and the columns of one weight block.
+  static __device__ __forceinline__ Turn wide(const MmParams& p, Smem sm, uint32_t tmem_base, int rank,
+                                              int i, int e, Turn turn) {
+    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
+    const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + group * 128;
+    float sum[128];
+#pragma unroll
+    for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+    Walk walk(p, sm, turn);
+    for (int kb = 0; kb < p.kblocks; ++kb) {
+      if (!walk.next(kb)) break;
+      const float f = walk.factors[group * 128 + quad * 32 + lane];
+      const uint32_t tm = tm0 + walk.buf * 256;
+#pragma unroll
+      for (int q = 0; q < 128; q += 64) {
+        uint32_t a[2][32];
+        tmem_ld_32x32b_x32(tm + q, a[0]);
+        tmem_ld_32x32b_x32(tm + q + 32, a[1]);
+        tmem_ld_wait_for(a[0]);
+        tmem_ld_wait_for(a[1]);
+        if (q == 64) walk.release();
+#pragma unroll
+        for (int n = 0; n < 64; ++n)
+          sum[q + n] = fmaf(__uint_as_float(a[n / 32][n % 32]), f, sum[q + n]);
+      }
+      walk.release_factors();
+    }
+    turn = walk.done();
+    // where the tile lies, found again: kept through the loop it would cost
+    // registers that the sums need
+    int again = i;
+    asm volatile("" : "+r"(again));
+    Tile t;
+    t.e = e;
+    t.at<kPair>(again, p, sm.off(), sm.tile());
+    const int r = rank * 128 + quad * 32 + lane;
+    if (turn.go && r < t.left) {
+      const int col = t.n * kN + group * 128, ncols = min(128, p.N - col);
+      const long at = static_cast<long>(t.row + r) * p.N + col;
+      if (p.vec) {  // (columns in multiples of 16)
+#pragma unroll
+        for (int j = 0; j < 128; j += 16) {
+          if (j >= ncols) continue;
+          uint32_t w[8];
+          if (p.f32) {
+#pragma unroll
+            for (int h = 0; h < 16; h += 8) {
+#pragma unroll
+              for (int n = 0; n < 8; ++n) w[n] = __float_as_uint(sum[j + h + n]);
+              store32(static_cast<float*>(p.out) + at + j + h, w);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
+            store32(static_cast<uint16_t*>(p.out) + at + j, w);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) {
+          if (j < ncols) {
+            if (p.f32) static_cast<float*>(p.out)[at + j] = sum[j];
+            else from_float(static_cast<Bf16*>(p.out)[at + j], sum[j]);
+          }
+        }
+      }
+    }
+    return turn;
+  }
+
+  // A narrow tile: a thread has a column and kParts of every other 32 rows.
+  template <int kParts>
+  static __device__ __forceinline__ Turn narrow(const MmParams& p, Smem sm, uint32_t tmem_base,
+                                                int rank, const Tile& t, Turn turn) {
+    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
+    const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + group * 32;
+    float sum[32 * kParts];
+#pragma unroll
+    for (int j = 0; j < 32 * kParts; ++j) sum[j] = 0.f;
+    Walk walk(p, sm, turn);
+    for (int kb = 0; kb < p.kblocks; ++kb) {
+      if (!walk.next(kb)) break;
+      const uint32_t tm = tm0 + walk.buf * 256;
+      uint32_t a[kParts][32];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x32(tm + 64 * q, a[q]);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) tmem_ld_wait_for(a[q]);
+      walk.release();
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        const float4* f = reinterpret_cast<const float4*>(walk.factors + 64 * q + 32 * group);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float4 f4 = f[n];
+          float* s = sum + 32 * q + 4 * n;
+          s[0] = fmaf(__uint_as_float(a[q][4 * n]), f4.x, s[0]);
+          s[1] = fmaf(__uint_as_float(a[q][4 * n + 1]), f4.y, s[1]);
+          s[2] = fmaf(__uint_as_float(a[q][4 * n + 2]), f4.z, s[2]);
+          s[3] = fmaf(__uint_as_float(a[q][4 * n + 3]), f4.w, s[3]);
+        }
+      }
+      walk.release_factors();
+    }
+    turn = walk.done();
+    const int col = t.n * kN + rank * 128 + quad * 32 + lane;
+    if (turn.go && col < p.N) {
+      long at = static_cast<long>(t.row + group * 32) * p.N + col;
+#pragma unroll
+      for (int j = 0; j < 32 * kParts; ++j) {
+        if (group * 32 + (j / 32) * 64 + j % 32 < t.left) {
+          if (p.f32) static_cast<float*>(p.out)[at] = sum[j];
+          else from_float(static_cast<Bf16*>(p.out)[at], sum[j]);
+        }
+        at += j == 31 ? 33L * p.N : p.N;
+      }
+    }
+    return turn;
+  }
+
+  static __device__ __forceinline__ Turn tile(const MmParams& p, Smem sm, uint32_t tmem_base, int rank,
+                                              int i, const Tile& t, Turn turn) {
+    const int quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
+    if (kPair && !t.narrow) {
+      if (rank * 128 + quad * 32 >= t.left || t.n * kN + group * 128 >= p.N) return idle(p, sm, turn);
+      return wide(p, sm, tmem_base, rank, i, t.e, turn);
+    }
+    const int parts = ((t.left + 31) / 32 - group + 1) / 2;  // 32s of rows
+    if (parts <= 0 || t.n * kN + rank * 128 + quad * 32 >= p.N) return idle(p, sm, turn);
+    return parts == 1 ? narrow<1>(p, sm, tmem_base, rank, t, turn)
+                      : narrow<2>(p, sm, tmem_base, rank, t, turn);
+  }
 };
 
 template <bool kPair>
@@ -237,261 +499,184 @@ __global__ void __launch_bounds__(kThreads, 1)
 fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmParams p) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kN = 128 * kCtas;           // columns of a tile
-  constexpr int kCols = kN / 2;             // of an epilogue thread
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sX = smem;                        // [stage][2 planes]
-  uint8_t* sW = smem + kStages * 2 * kPlane;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* s_off = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + kBarBytes);
-  int32_t* s_tile = s_off + kMaxE + 1;
+  uint8_t* sW = smem;  // [stage][2 planes]
+  uint8_t* sX = smem + p.stages * 2 * kPlane;
+  const Smem sm{smem};
+  volatile int* abort_flag = sm.abort_flag();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(sm.full(s), 1);
+      mbar_init(sm.empty(s), 2);  // both issuers
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kCtas * kEpiWarps);  // one arrival per epilogue warp
+      mbar_init(sm.tfull(b), 1);
+      mbar_init(sm.tempty(b), kCtas * kEpiWarps);  // one arrival per epilogue warp
+      mbar_init(sm.ffull(b), 1);
+      mbar_init(sm.fempty(b), kEpiWarps);
+      mbar_init(sm.drain(b), 1);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&maps.x);
-    prefetch_tensormap(&maps.w);
-  }
+  if (warp == 0 && lane < kBoxes + 1)
+    prefetch_tensormap(lane < kBoxes ? &maps.x[lane] : &maps.w);
   if (warp == 1) {
-    if (kPair) pair::tmem_alloc2<512>(tmem_slot);
-    else tmem_alloc<512>(tmem_slot);
+    if (kPair) pair::tmem_alloc2<512>(sm.tmem_slot());
+    else tmem_alloc<512>(sm.tmem_slot());
   }
   // nothing above touches global memory
   pdl_enter();
-  const int total = build_tiles<kThreads>(p.offsets, p.E, p.M, p.n_tiles, 128 * kCtas, s_off,
-                                          s_tile, p.status);
+  const int total = build_tiles<kThreads>(p.offsets, p.E, p.M, p.n_tiles, p.tile_rows, sm.off(),
+                                          sm.tile(), p.status);
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();  // both CTAs' barriers exist before anything signals them
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = *sm.tmem_slot();
   const int first = static_cast<int>(blockIdx.x) / kCtas, step = static_cast<int>(gridDim.x) / kCtas;
 
   if (warp < 4) {
-    regs_down<40>();
+    regs_down<kRegsOther>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- producer
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
-      Cursor c;
+      Tile t;
       bool ok = true;
       for (int i = first; ok && i < total && !*abort_flag; i += step) {
-        c.at(i, s_tile, p.n_tiles);
-        const int row = s_off[c.e] + (c.m * kCtas + static_cast<int>(rank)) * 128;
-        const int col = (c.n * kCtas + static_cast<int>(rank)) * 128;
+        t.at<kPair>(i, p, sm.off(), sm.tile());
+        const int row = t.row + rank * (t.narrow ? t.half : 128);
+        const int col = (t.n * kCtas + rank) * 128;
+        const uint32_t plane = t.x_plane(), bytes = kCtas * 2 * (kPlane + plane);
+        const CUtensorMap* map = &maps.x[t.box];
         for (int kb = 0; kb < p.kblocks; kb += 2) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, p.status)) { ok = false; break; }
-          if (leader) mbar_arrive_expect_tx(&full[stage], kCtas * kStageBytes);
-          load_x<kPair>(sX + stage * 2 * kPlane, &maps.x, p.planes, kb, row, kPlane, &full[stage], pol);
-          load_w<kPair>(sW + stage * 2 * kPlane, &maps.w, p.planes, kb, col, c.e, kPlane, &full[stage],
+          if (!mbar_wait(sm.empty(stage), phase ^ 1, p.status)) { ok = false; break; }
+          if (leader) mbar_arrive_expect_tx(sm.full(stage), bytes);
+          load_w<kPair>(sW + stage * 2 * kPlane, &maps.w, p.planes, kb, col, t.e, kPlane, sm.full(stage),
                         pol);
+          load_x<kPair>(sX + stage * p.x_stage, map, p.planes, kb, row, plane, sm.full(stage), pol);
           ++issued;
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+          if (++stage == p.stages) { stage = 0; phase ^= 1; }
         }
       }
       if (!ok) *abort_flag = 1;
       // no bulk copy left in flight (a pair's complete on the leader's barriers)
-      for (int i = 1; leader && i <= kStages && i <= issued; ++i) {
+      for (int i = 1; leader && i <= p.stages && i <= issued; ++i) {
         int s = stage - i;
         uint32_t ph = phase;
-        if (s < 0) { s += kStages; ph ^= 1; }
-        mbar_wait(&full[s], ph, p.status);
+        if (s < 0) { s += p.stages; ph ^= 1; }
+        mbar_wait(sm.full(s), ph, p.status);
       }
-    } else if (warp == 1 && leader && lane == 0) {
-      // -------------------------------------------------------------- MMA issuer
-      const uint32_t idesc = idesc_e4m3(128 * kCtas, kN);
+    } else if ((warp == 1 || warp == 2) && leader && lane == 0) {
+      // -------------------------------------------------------------- MMA issuers
+      // Blocks alternate between the accumulators, and either issuer has one of
+      // them: what one thread needs to wait, issue and commit for a block (some
+      // 800 cycles) is more than the block takes the tensor core.
+      const int mine = warp - 1;
+      const uint32_t d = tmem_base + mine * 256;
       int stage = 0;
       uint32_t phase = 0;
-      int seg = 0;  // blocks so far: they alternate between the two accumulators
+      int seg = 0;  // blocks so far
+      Tile t;
       bool ok = true;
       for (int i = first; ok && i < total && !*abort_flag; i += step) {
-        for (int kb = 0; ok && kb < p.kblocks; kb += 2) {
-          if (!mbar_wait(&full[stage], phase, p.status)) { ok = false; break; }
-          tc_fence_after();
-          for (int h = 0; h < 2 && kb + h < p.kblocks; ++h, ++seg) {
-            const int buf = seg & 1;
-            if (!mbar_wait(&tempty[buf], ((seg >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
+        t.at<kPair>(i, p, sm.off(), sm.tile());
+        const uint32_t plane = t.x_plane();
+        const uint32_t idesc = idesc_e4m3(128 * kCtas, t.narrow ? kCtas * t.half : kN);
+        for (int kb = 0; kb < p.kblocks; kb += 2) {
+          if (!mbar_wait(sm.full(stage), phase, p.status)) { ok = false; break; }
+          // this stage's block for this accumulator, if it has one
+          const int h = (seg ^ mine) & 1, blocks = min(2, p.kblocks - kb);
+          if (h < blocks) {
+            if (!mbar_wait(sm.tempty(mine), (((seg + h) >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t a = sw128_kmajor_desc(smem_u32(sX + (stage * 2 + h) * kPlane));
-            const uint64_t b = sw128_kmajor_desc(smem_u32(sW + (stage * 2 + h) * kPlane));
+            const uint64_t w = sw128_kmajor_desc(smem_u32(sW + (stage * 2 + h) * kPlane));
+            const uint64_t x = sw128_kmajor_desc(smem_u32(sX + stage * p.x_stage + h * plane));
+            const uint64_t a = t.narrow ? w : x, b = t.narrow ? x : w;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_e4m3<kPair>(tmem_base + buf * 256, a + 2 * kk, b + 2 * kk, idesc, kk != 0);
-            if (kPair) pair::commit_both(&tfull[buf]);
-            else mma_commit(&tfull[buf]);
+              mma_e4m3<kPair>(d, a + 2 * kk, b + 2 * kk, idesc, kk != 0);
+            if (kPair) pair::commit_both(sm.tfull(mine));
+            else mma_commit(sm.tfull(mine));
           }
-          if (!ok) break;
-          if (kPair) pair::commit_both(&empty[stage]);
-          else mma_commit(&empty[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+          if (kPair) pair::commit_both(sm.empty(stage));
+          else mma_commit(sm.empty(stage));
+          seg += blocks;
+          if (++stage == p.stages) { stage = 0; phase ^= 1; }
         }
       }
       if (!ok) *abort_flag = 1;
-      if (kPair) pair::commit_local(drain);  // every MMA done before TMEM is released
-      else mma_commit(drain);
-      mbar_wait(drain, 0, p.status);
+      if (kPair) pair::commit_local(sm.drain(mine));  // every MMA done before TMEM is released
+      else mma_commit(sm.drain(mine));
+      mbar_wait(sm.drain(mine), 0, p.status);
+    } else if (warp == 3) {
+      // -------------------------------------------------------------- factors
+      // x_scale * w_scale of every block and row, ahead of the epilogue (whose own
+      // loads, a row to a lane, would each touch 32 sectors): of a wide tile for both
+      // of its weight blocks, of a narrow one for this CTA's.
+      int chunk = 0;
+      Tile t;
+      bool ok = true;
+      for (int i = first; ok && i < total; i += step) {
+        if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+        t.at<kPair>(i, p, sm.off(), sm.tile());
+        const int row0 = t.row + (t.narrow ? 0 : rank * 128);
+        const int rows = t.narrow ? t.left : t.left - rank * 128;
+        const int nb = min(t.n * kCtas + (t.narrow ? rank : 0), p.nblocks - 1);
+        const float* ws = p.ws + (static_cast<long>(t.e) * p.nblocks + nb) * p.kblocks;
+        const long second = nb + 1 < p.nblocks ? p.kblocks : 0;  // the next weight block's
+        for (int kb = 0; ok && kb < p.kblocks; kb += kChunk, ++chunk) {
+          const int buf = chunk & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(sm.fempty(buf), ((chunk >> 1) & 1) ^ 1, p.status));
+          if (!ok) break;
+          float* out = sm.factors(buf);
+          const int n = min(kChunk, p.kblocks - kb);
+          // lane j of eight has block j's weight scales
+          const int j8 = lane & 7;
+          const float w0 = j8 < n ? __ldg(ws + kb + j8) : 0.f;
+          const float w1 = !t.narrow && j8 < n ? __ldg(ws + second + kb + j8) : 0.f;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            if (32 * q >= rows && q > 0) break;  // rows that nothing uses
+            const int r = 32 * q + lane;
+            const float* xs = p.xs + (static_cast<long>(row0) + r) * p.kblocks + kb;
+            float x[kChunk];
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) x[j] = r < rows && j < n ? __ldg(xs + j) : 0.f;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) {
+              out[(2 * j) * 128 + r] = x[j] * __shfl_sync(0xffffffffu, w0, j);
+              if (kPair) out[(2 * j + 1) * 128 + r] = x[j] * __shfl_sync(0xffffffffu, w1, j);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm.ffull(buf));
+        }
+      }
+      if (!ok && lane == 0) *abort_flag = 1;
     }
     __syncwarp();
   } else {
-    regs_up<232>();
+    regs_up<kRegsEpilogue>();
     // ---------------------------------------------------------------- epilogue
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * kCols;
-    const uint32_t tempty_leader = kPair ? pair::mapa(smem_u32(tempty), 0) : 0;
-    int seg = 0;
-    bool go = true;
-    Cursor c;
-    for (int i = first; go && i < total; i += step) {
+    Turn turn;
+    int e = 0;
+    for (int i = first; turn.go && i < total; i += step) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      c.at(i, s_tile, p.n_tiles);
-      const int row0 = s_off[c.e] + (c.m * kCtas + static_cast<int>(rank)) * 128 + quad * 32;
-      const int rows = s_off[c.e + 1];
-      const long row = row0 + lane;
-      const int col = c.n * kN + half * kCols;
-      const bool live = row0 < rows && col < p.N, row_ok = row < rows;
-      const float* xs = p.xs + (row_ok ? row : 0) * p.kblocks;
-      const float* ws = p.ws + (static_cast<long>(c.e) * p.nblocks + min(col / kBlk, p.nblocks - 1)) *
-                                   p.kblocks;
-      Pair acc[kCols / 2];
-#pragma unroll
-      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-      // The next block's sums are complete: the accumulator's columns.
-      auto wait_full = [&]() {
-        go = __all_sync(0xffffffffu, mbar_wait(&tfull[seg & 1], (seg >> 1) & 1, p.status));
-        tc_fence_after();
-        return t_lane + (seg & 1) * 256;
-      };
-      // They have been read (the leader's barrier; nothing else is handed over).
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (kPair) arrive_remote_relaxed(tempty_leader + (seg & 1) * 8);
-          else mbar_arrive(&tempty[seg & 1]);
-        }
-        ++seg;
-      };
-      // A step is 32 columns of a block: the next step's sums are on their way
-      // from TMEM while this one's are scaled and added, and the accumulator is
-      // free as soon as its last ones have come.
-      constexpr int kSteps = kCols / 32;
-      constexpr int kAhead = 2;  // factors on their way
-      float fx[kAhead], fw[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        fx[j] = j < p.kblocks ? __ldg(xs + j) : 0.f;
-        fw[j] = j < p.kblocks ? __ldg(ws + j) : 0.f;
-      }
-      uint32_t a[2][32], t = wait_full();
-      if (go && live) tmem_ld_32x32b_x32(t, a[0]);
-      for (int kb0 = 0; go && kb0 < p.kblocks; kb0 += kAhead) {
-        float f[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          f[j] = fx[j] * fw[j];
-          const int kb = kb0 + kAhead + j;
-          fx[j] = kb < p.kblocks ? __ldg(xs + kb) : 0.f;
-          fw[j] = kb < p.kblocks ? __ldg(ws + kb) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (!go || kb0 + j >= p.kblocks) break;
-          const Pair f2 = pair_of(f[j], f[j]);
-#pragma unroll
-          for (int q = 0; q < kSteps; ++q) {
-            const int here = (j * kSteps + q) & 1;
-            if (live) tmem_ld_wait_for(a[here]);
-            if (q + 1 < kSteps) {
-              if (live) tmem_ld_32x32b_x32(t + 32 * (q + 1), a[here ^ 1]);
-            } else {
-              release();
-              if (kb0 + j + 1 < p.kblocks) {
-                t = wait_full();
-                if (go && live) tmem_ld_32x32b_x32(t, a[here ^ 1]);
-              }
-            }
-            if (live) {
-#pragma unroll
-              for (int n = 0; n < 16; ++n)
-                acc[q * 16 + n] = pair_fma(
-                    pair_of(__uint_as_float(a[here][2 * n]), __uint_as_float(a[here][2 * n + 1])), f2,
-                    acc[q * 16 + n]);
-            }
-          }
-        }
-      }
-      if (!go && lane == 0) *abort_flag = 1;
-      if (!go) break;
-      if (!live || !row_ok) continue;
-      const int ncols = min(kCols, p.N - col);
-      const long at = row * p.N + col;
-      if (p.vec && ncols % 16 == 0) {
-        if (p.f32) {
-          float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < kCols; j += 8) {
-            if (j >= ncols) continue;
-            uint32_t w[8];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              float lo, hi;
-              unpair(acc[j / 2 + n], lo, hi);
-              w[2 * n] = __float_as_uint(lo);
-              w[2 * n + 1] = __float_as_uint(hi);
-            }
-            store32(o + j, w);
-          }
-        } else {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < kCols; j += 16) {
-            if (j >= ncols) continue;
-            uint32_t w[8];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              float lo, hi;
-              unpair(acc[j / 2 + n], lo, hi);
-              w[n] = pack_bf16(lo, hi);
-            }
-            store32(o + j, w);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kCols / 2; ++j) {
-          float v[2];
-          unpair(acc[j], v[0], v[1]);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            if (2 * j + n < ncols) {
-              if (p.f32) static_cast<float*>(p.out)[at + 2 * j + n] = v[n];
-              else from_float(static_cast<Bf16*>(p.out)[at + 2 * j + n], v[n]);
-            }
-          }
-        }
-      }
+      Tile t;
+      t.e = e;
+      t.at<kPair>(i, p, sm.off(), sm.tile());
+      e = t.e;
+      turn = Epilogue<kPair>::tile(p, sm, tmem_base, rank, i, t, turn);
+      if (!turn.go && lane == 0) *abort_flag = 1;
     }
     __syncwarp();
   }
@@ -575,20 +760,28 @@ int check_matmul(const moe_fp8_problem* p) {
   return MOE_OK;
 }
 
+// Rows per narrow tile of single CTAs, or 0: pairs.
+int narrow_rows(const moe_fp8_problem* p) {
+  const long mean = ceil_div(p->M, p->E);
+  return mean <= 8 ? 32 : mean <= 64 ? 128 : 0;
+}
+
 template <bool kPair>
 cudaError_t launch_tiles(const moe_fp8_problem* p, const void* x, const void* w, MmParams& k,
                          cudaStream_t s) {
   constexpr int kCtas = kPair ? 2 : 1;
   Maps maps;
-  if (!make_codes_map(&maps.x, x, p->K, p->M, 0, k.planes, 128) ||
-      !make_codes_map(&maps.w, w, p->K, p->N, p->E, k.planes, 128))
-    return cudaErrorInvalidValue;
+  for (int i = 0; i < kBoxes; ++i)
+    if (!make_codes_map(&maps.x[i], x, p->K, p->M, 0, k.planes, 16 << i)) return cudaErrorInvalidValue;
+  if (!make_codes_map(&maps.w, w, p->K, p->N, p->E, k.planes, 128)) return cudaErrorInvalidValue;
   k.n_tiles = ceil_div(p->N, 128 * kCtas);
+  k.x_stage = 2 * kBlk * (kPair ? 128 : k.tile_rows);
+  k.stages = std::min<int>(kMaxStages, kRing / (2 * kPlane + k.x_stage));
   auto kern = fp8_matmul_kernel<kPair>;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
-  const long most = (ceil_div(p->M, 128 * kCtas) + static_cast<long>(std::min(p->E, p->M))) * k.n_tiles;
+  const long most = (ceil_div(p->M, k.tile_rows) + static_cast<long>(std::min(p->E, p->M))) * k.n_tiles;
   const int groups = static_cast<int>(std::max(1L, std::min<long>(num_sms() / kCtas, most)));
   return launch_kernel(kern, dim3(static_cast<unsigned>(kCtas * groups)), dim3(kThreads), kSmem, s,
                        kCtas, maps, k);
@@ -631,7 +824,10 @@ extern "C" int moe_fp8_matmul(const moe_fp8_problem* p, const void* x, const flo
   k.vec = p->N % 16 == 0 && !off(out, 32);
   k.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_tiles<true>(p, x, w, k, s) != cudaSuccess) return MOE_ERR_CUDA;
+  const int narrow = narrow_rows(p);
+  k.tile_rows = narrow ? narrow : 256;
+  if ((narrow ? launch_tiles<false>(p, x, w, k, s) : launch_tiles<true>(p, x, w, k, s)) != cudaSuccess)
+    return MOE_ERR_CUDA;
   set_last_launch_count(1);
   return MOE_OK;
 }
