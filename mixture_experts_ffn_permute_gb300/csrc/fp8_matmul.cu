@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/moe_experts.h"
@@ -53,7 +54,7 @@ constexpr size_t kSmem = 1024 + kRing + kBarBytes + 2 * kFactors * sizeof(float)
                          2 * (kMaxE + 1) * sizeof(int32_t);
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert((2 * kMaxStages + 10) * 8 + 8 <= kBarBytes, "barrier area");
-// registers: a launch's 168 x 384, moved as 40 x 128 + 232 x 256
+// registers: a launch's 168 x 384, moved as 56 x 128 + 224 x 256
 constexpr int kRegsOther = 56, kRegsEpilogue = 224;
 static_assert(kRegsOther * 128 + kRegsEpilogue * 32 * kEpiWarps <= 168 * kThreads, "register split");
 
@@ -68,7 +69,6 @@ struct MmParams {
   uint32_t x_stage; // bytes of a stage's rows in one CTA
   int planes;  // operands come as planes
   int f32;     // out
-  int vec;     // 32-byte stores
   uint32_t* status;
 };
 
@@ -237,6 +237,13 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// The value, of which the compiler knows nothing: what depends on it is not worked
+// out ahead of the tiles' loops, to lie in registers that the sums need.
+__device__ __forceinline__ long opaque(long v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
+
 // Arrival on a barrier of the pair that hands over no memory.
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
@@ -395,35 +402,25 @@ struct Epilogue {
     Tile t;
     t.e = e;
     t.at<kPair>(again, p, sm.off(), sm.tile());
-    const int r = rank * 128 + quad * 32 + lane;
-    if (turn.go && r < t.left) {
-      const int col = t.n * kN + group * 128, ncols = min(128, p.N - col);
-      const long at = static_cast<long>(t.row + r) * p.N + col;
-      if (p.vec) {  // (columns in multiples of 16)
+    const int r0 = rank * 128 + quad * 32, col = t.n * kN + group * 128;
+    const int ncols = min(128, p.N - col);
+    if (turn.go) {  // (columns in multiples of 16, on 32 bytes)
+      const long at = static_cast<long>(t.row + r0 + lane) * p.N + col;
 #pragma unroll
-        for (int j = 0; j < 128; j += 16) {
-          if (j >= ncols) continue;
-          uint32_t w[8];
-          if (p.f32) {
+      for (int j = 0; j < 128; j += 16) {
+        if (j >= ncols || r0 + lane >= t.left) continue;
+        uint32_t w[8];
+        if (p.f32) {
 #pragma unroll
-            for (int h = 0; h < 16; h += 8) {
+          for (int h = 0; h < 16; h += 8) {
 #pragma unroll
-              for (int n = 0; n < 8; ++n) w[n] = __float_as_uint(sum[j + h + n]);
-              store32(static_cast<float*>(p.out) + at + j + h, w);
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
-            store32(static_cast<uint16_t*>(p.out) + at + j, w);
+            for (int n = 0; n < 8; ++n) w[n] = __float_as_uint(sum[j + h + n]);
+            store32(static_cast<float*>(p.out) + at + j + h, w);
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) {
-          if (j < ncols) {
-            if (p.f32) static_cast<float*>(p.out)[at + j] = sum[j];
-            else from_float(static_cast<Bf16*>(p.out)[at + j], sum[j]);
-          }
+          for (int n = 0; n < 8; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
+          store32(static_cast<uint16_t*>(p.out) + at + j, w);
         }
       }
     }
@@ -467,14 +464,15 @@ struct Epilogue {
     turn = walk.done();
     const int col = t.n * kN + rank * 128 + quad * 32 + lane;
     if (turn.go && col < p.N) {
-      long at = static_cast<long>(t.row + group * 32) * p.N + col;
+      const long step = opaque(p.N);
+      long at = static_cast<long>(t.row + group * 32) * step + col;
 #pragma unroll
       for (int j = 0; j < 32 * kParts; ++j) {
         if (group * 32 + (j / 32) * 64 + j % 32 < t.left) {
           if (p.f32) static_cast<float*>(p.out)[at] = sum[j];
           else from_float(static_cast<Bf16*>(p.out)[at], sum[j]);
         }
-        at += j == 31 ? 33L * p.N : p.N;
+        at += j == 31 ? 33 * step : step;
       }
     }
     return turn;
@@ -760,10 +758,32 @@ int check_matmul(const moe_fp8_problem* p) {
   return MOE_OK;
 }
 
-// Rows per narrow tile of single CTAs, or 0: pairs.
-int narrow_rows(const moe_fp8_problem* p) {
-  const long mean = ceil_div(p->M, p->E);
-  return mean <= 8 ? 32 : mean <= 64 ? 128 : 0;
+// Rows of a tile: 64 or 128, narrow ones of single CTAs, or 256, wide ones of
+// pairs (whose rows of out have to lie on 32 bytes).
+//
+// A block takes a CTA about 0.2 us (its weights' 16 KB at the rate of HBM, and less
+// from L2) and 1.9 ns a row of the tile, a pair 0.5 us for a wide tile; the fewest
+// waves of those are the shortest, and of 64 and 128 rows in as many tiles 64 leave
+// room for a stage more.  With 64, 128 and 256 rows, us: M=2048 E=256 N=4096 K=7168
+// 1104, 1146, 1184; M=16384 1600, 1225, 1251; M=32768 2215, 2087, 1551; M=300 E=1
+// N=2048 K=2048 10.8, 12.7, 18.3; M=600 16.5, 13.5, 18.4; M=256 E=1 N=8192 K=8192
+// 43.9, 33.6, 40.7; M=384 63, 60, 43; M=8192 E=8 N=28672 K=4096 1923, 1352, 864.
+int rows_of_tile(const moe_fp8_problem* p, bool wide) {
+  const long groups = std::min(p->E, p->M), mean = ceil_div(p->M, groups);
+  int best = 0;
+  double least = 0;
+  for (int rows = 64; rows <= (wide ? 256 : 128); rows *= 2) {
+    const int ctas = rows == 256 ? 2 : 1;
+    // experts of very different sizes end half a tile behind a whole one
+    const double tall = p->E == 1        ? ceil_div(p->M, rows)
+                        : 2 * mean <= rows ? static_cast<double>(groups)
+                                           : static_cast<double>(p->M) / rows + 0.5 * groups;
+    const double tiles = tall * ceil_div(p->N, 128 * ctas);
+    const double waves = std::max(1.0, std::ceil(tiles / std::max(1, num_sms() / ctas)));
+    const double t = waves * (rows == 256 ? 0.5 : 0.2 + 0.0019 * std::min<long>(rows, mean));
+    if (best == 0 || t < least) best = rows, least = t;
+  }
+  return best;
 }
 
 template <bool kPair>
@@ -821,12 +841,11 @@ extern "C" int moe_fp8_matmul(const moe_fp8_problem* p, const void* x, const flo
   k.nblocks = ceil_div(p->N, kBlk);
   k.planes = p->K % kBlk == 0;
   k.f32 = p->out_dtype == MOE_DTYPE_F32;
-  k.vec = p->N % 16 == 0 && !off(out, 32);
   k.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int narrow = narrow_rows(p);
-  k.tile_rows = narrow ? narrow : 256;
-  if ((narrow ? launch_tiles<false>(p, x, w, k, s) : launch_tiles<true>(p, x, w, k, s)) != cudaSuccess)
+  k.tile_rows = rows_of_tile(p, p->N % 16 == 0 && !off(out, 32));
+  if ((k.tile_rows == 256 ? launch_tiles<true>(p, x, w, k, s) : launch_tiles<false>(p, x, w, k, s)) !=
+      cudaSuccess)
     return MOE_ERR_CUDA;
   set_last_launch_count(1);
   return MOE_OK;
