@@ -299,6 +299,7 @@ struct Smem {
 struct Turn {
   int chunk = 0;             // chunks of factors so far
   uint32_t buf = 0, par = 0; // the accumulator that comes next, and its phase
+  int stage = 0;             // of the ring, of the blocks that come next (single CTAs)
   bool go = true;            // no wait has run out
 };
 
@@ -307,6 +308,7 @@ template <bool kPair>
 struct Epilogue {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kN = 128 * kCtas;
+  static constexpr int kHand = kPair ? 1 : 2;  // blocks handed over at once
   // Its way through a tile's blocks.
   struct Walk : Turn {
     const MmParams& p;
@@ -329,6 +331,10 @@ struct Epilogue {
       ok = ok && mbar_wait(sm.tfull(buf), par, p.status);
       __syncwarp();
       tc_fence_after();
+      if (!kPair) {  // the tensor core is through with the stage's operands
+        if (threadIdx.x == 128) mbar_arrive(sm.empty(stage));
+        if (++stage == p.stages) stage = 0;
+      }
       return true;
     }
     // The accumulator has been read (nothing else is handed over).
@@ -342,9 +348,10 @@ struct Epilogue {
       buf ^= 1;
     }
     // So have the factors, once a chunk is through.
-    __device__ __forceinline__ void release_factors() {
-      factors += 256;
-      if (--left == 0) {
+    __device__ __forceinline__ void release_factors(int blocks) {
+      factors += 256 * blocks;
+      left -= blocks;
+      if (left == 0) {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(sm.fempty(chunk & 1));
         ++chunk;
@@ -359,10 +366,10 @@ struct Epilogue {
   // A tile that this warp has no part of.
   static __device__ __forceinline__ Turn idle(const MmParams& p, Smem sm, Turn turn) {
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < p.kblocks; ++kb) {
+    for (int kb = 0; kb < p.kblocks; kb += kHand) {
       if (!walk.next(kb)) break;
       walk.release();
-      walk.release_factors();
+      walk.release_factors(min(kHand, p.kblocks - kb));
     }
     return walk.done();
   }
@@ -392,7 +399,7 @@ struct Epilogue {
         for (int n = 0; n < 64; ++n)
           sum[q + n] = fmaf(__uint_as_float(a[n / 32][n % 32]), f, sum[q + n]);
       }
-      walk.release_factors();
+      walk.release_factors(1);
     }
     turn = walk.done();
     // where the tile lies, found again: kept through the loop it would cost
@@ -437,29 +444,42 @@ struct Epilogue {
 #pragma unroll
     for (int j = 0; j < 32 * kParts; ++j) sum[j] = 0.f;
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < p.kblocks; ++kb) {
+    for (int kb = 0; kb < p.kblocks; kb += kHand) {
       if (!walk.next(kb)) break;
       const uint32_t tm = tm0 + walk.buf * 256;
-      uint32_t a[kParts][32];
+      const int blocks = min(kHand, p.kblocks - kb);
+      uint32_t a[kHand][kParts][32];
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x32(tm + 64 * q, a[q]);
+      for (int h = 0; h < kHand; ++h) {  // (a second block that is not there is not used)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) tmem_ld_wait_for(a[q]);
+        for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x32(tm + 128 * h + 64 * q, a[h][q]);
+      }
+#pragma unroll
+      for (int h = 0; h < kHand; ++h) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) tmem_ld_wait_for(a[h][q]);
+      }
       walk.release();
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        const float4* f = reinterpret_cast<const float4*>(walk.factors + 64 * q + 32 * group);
+      for (int h = 0; h < kHand; ++h) {
+        if (h < blocks) {
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float4 f4 = f[n];
-          float* s = sum + 32 * q + 4 * n;
-          s[0] = fmaf(__uint_as_float(a[q][4 * n]), f4.x, s[0]);
-          s[1] = fmaf(__uint_as_float(a[q][4 * n + 1]), f4.y, s[1]);
-          s[2] = fmaf(__uint_as_float(a[q][4 * n + 2]), f4.z, s[2]);
-          s[3] = fmaf(__uint_as_float(a[q][4 * n + 3]), f4.w, s[3]);
+          for (int q = 0; q < kParts; ++q) {
+            const float4* f =
+                reinterpret_cast<const float4*>(walk.factors + 256 * h + 64 * q + 32 * group);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float4 f4 = f[n];
+              float* s = sum + 32 * q + 4 * n;
+              s[0] = fmaf(__uint_as_float(a[h][q][4 * n]), f4.x, s[0]);
+              s[1] = fmaf(__uint_as_float(a[h][q][4 * n + 1]), f4.y, s[1]);
+              s[2] = fmaf(__uint_as_float(a[h][q][4 * n + 2]), f4.z, s[2]);
+              s[3] = fmaf(__uint_as_float(a[h][q][4 * n + 3]), f4.w, s[3]);
+            }
+          }
         }
       }
-      walk.release_factors();
+      walk.release_factors(blocks);
     }
     turn = walk.done();
     const int col = t.n * kN + rank * 128 + quad * 32 + lane;
@@ -482,7 +502,8 @@ struct Epilogue {
                                               int i, const Tile& t, Turn turn) {
     const int quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
     if (kPair && !t.narrow) {
-      if (rank * 128 + quad * 32 >= t.left || t.n * kN + group * 128 >= p.N) return idle(p, sm, turn);
+      if (rank * 128 + quad * 32 >= t.left || t.n * kN + group * 128 >= p.N)
+        return idle(p, sm, turn);
       return wide(p, sm, tmem_base, rank, i, t.e, turn);
     }
     const int parts = ((t.left + 31) / 32 - group + 1) / 2;  // 32s of rows
@@ -510,7 +531,7 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(sm.full(s), 1);
-      mbar_init(sm.empty(s), 2);  // both issuers
+      mbar_init(sm.empty(s), 2);  // either issuer, or one and the epilogue
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sm.tfull(b), 1);
@@ -575,14 +596,17 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
       }
     } else if ((warp == 1 || warp == 2) && leader && lane == 0) {
       // -------------------------------------------------------------- MMA issuers
-      // Blocks alternate between the accumulators, and either issuer has one of
-      // them: what one thread needs to wait, issue and commit for a block (some
-      // 800 cycles) is more than the block takes the tensor core.
+      // What is handed to the epilogue at once, a block, or of single CTAs the two of
+      // a stage (each in columns of its own: a commit, some 100 cycles in which the
+      // tensor core stands still, is then one for both), alternates between the
+      // accumulators, and either issuer has one of them: what one thread needs to
+      // wait, issue and commit for a block (some 800 cycles) is more than the block
+      // takes the tensor core.
       const int mine = warp - 1;
       const uint32_t d = tmem_base + mine * 256;
       int stage = 0;
       uint32_t phase = 0;
-      int seg = 0;  // blocks so far
+      int seg = 0;  // hand-overs so far
       Tile t;
       bool ok = true;
       for (int i = first; ok && i < total && !*abort_flag; i += step) {
@@ -590,24 +614,33 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
         const uint32_t plane = t.x_plane();
         const uint32_t idesc = idesc_e4m3(128 * kCtas, t.narrow ? kCtas * t.half : kN);
         for (int kb = 0; kb < p.kblocks; kb += 2) {
+          const int blocks = min(2, p.kblocks - kb), units = kPair ? blocks : 1;
+          const int u = (seg ^ mine) & 1;  // this issuer's of the stage's units, if it has one
           if (!mbar_wait(sm.full(stage), phase, p.status)) { ok = false; break; }
-          // this stage's block for this accumulator, if it has one
-          const int h = (seg ^ mine) & 1, blocks = min(2, p.kblocks - kb);
-          if (h < blocks) {
-            if (!mbar_wait(sm.tempty(mine), (((seg + h) >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
+          // A stage is empty when the tensor core is through with it and both issuers
+          // have seen it full (one that came to it when it was full again would take
+          // it for not filled yet).  Pairs: both commit to it.  Single CTAs: the
+          // epilogue tells, and so does the issuer that has not the stage.
+          if (!kPair && u != 0) mbar_arrive(sm.empty(stage));
+          if (u < units) {
+            if (!mbar_wait(sm.tempty(mine), (((seg + u) >> 1) & 1) ^ 1, p.status)) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            const uint64_t w = sw128_kmajor_desc(smem_u32(sW + (stage * 2 + h) * kPlane));
-            const uint64_t x = sw128_kmajor_desc(smem_u32(sX + stage * p.x_stage + h * plane));
-            const uint64_t a = t.narrow ? w : x, b = t.narrow ? x : w;
+            for (int h = kPair ? u : 0; h < (kPair ? u + 1 : blocks); ++h) {
+              const uint64_t w = sw128_kmajor_desc(smem_u32(sW + (stage * 2 + h) * kPlane));
+              const uint64_t x = sw128_kmajor_desc(smem_u32(sX + stage * p.x_stage + h * plane));
+              const uint64_t a = t.narrow ? w : x, b = t.narrow ? x : w;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_e4m3<kPair>(d, a + 2 * kk, b + 2 * kk, idesc, kk != 0);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_e4m3<kPair>(d + (kPair ? 0 : h * 128), a + 2 * kk, b + 2 * kk, idesc, kk != 0);
+            }
             if (kPair) pair::commit_both(sm.tfull(mine));
             else mma_commit(sm.tfull(mine));
           }
           if (kPair) pair::commit_both(sm.empty(stage));
-          else mma_commit(sm.empty(stage));
-          seg += blocks;
+          seg += units;
           if (++stage == p.stages) { stage = 0; phase ^= 1; }
         }
       }
