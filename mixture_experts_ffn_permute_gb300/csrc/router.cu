@@ -4,19 +4,18 @@
 // One warp per token, the row in registers: lane i holds the experts i N ..
 // i N + N - 1 (N the power of two that fits E), so that among equal keys the lowest
 // lane, and in it the first, is the lowest id.  A key is the value's bits in an
-// order of unsigned integers; a pick is one warp maximum and one ballot.
+// order of unsigned integers.  Up to N = 8 a lane sorts its keys once; a pick is then
+// one warp maximum, one ballot and a shift of the winner's list.
 //
 // The order is that of c in 64 bits.  Without a bias c grows with the logit, and
 // logits compare exactly.  With one, c is computed in fp32 with an error of at
 // most `tol` / 2 (below); only where two neighbours in the order of the picks (or
 // the last group taken and the first one left) are nearer than that, and are not
-// the same logit and bias, the token is chosen again with the experts in question
-// in fp64.  With 256 sigmoid scores and a random bias that is one token in a few
-// hundred; fp64 for all of them would cost 2 M x 60 instructions of a pipe of two
-// lanes an SM.
+// the same logit and bias, the token is chosen again in fp64.  With 256 sigmoid
+// scores and a random bias that is one token in some hundreds; fp64 for all of them
+// would cost 2 M x 30 instructions of a pipe of two lanes an SM.
 //
-// Bound by instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate), a
-// pick is about 50 instructions of a warp.
+// Bound by instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,8 +43,10 @@ struct RouterParams {
   void* d_logits;
   int T, E, k;
   int groups, topk_groups, group_top, per_group;  // experts per group
+  int group_lanes;  // lanes per group, where a group is a power of two of whole ones (else 0)
   int sigmoid, renormalize;
-  int wide;  // rows can be read and written in whole vectors
+  int wide;       // rows can be read and written in whole vectors
+  int bias_wide;  // the bias, too
   float scale;
   long ld;
 };
@@ -185,6 +186,64 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
   }
 }
 
+// The same from lists that every lane has sorted, highest first and the first among
+// equal ones: `at` holds their places, four bits each.
+template <int kN>
+__device__ __forceinline__ void pick_sorted(uint32_t (&key)[kN], uint32_t at, int k, int lane,
+                                            int& id, uint32_t& own) {
+  id = -1;
+  own = 0;
+  for (int j = 0; j <= k && j < 32; ++j) {
+    const uint32_t best = warp_max(key[0]);
+    if (best == 0) break;
+    const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+    const int place = __shfl_sync(kAll, at, from) & 15;
+    if (lane == from) {
+#pragma unroll
+      for (int i = 0; i + 1 < kN; ++i) key[i] = key[i + 1];
+      key[kN - 1] = 0;
+      at >>= 4;
+    }
+    if (lane == j) {
+      id = from * kN + place;
+      own = best;
+    }
+  }
+}
+
+// Sorts by an odd-even merge network (Batcher): kN = 1, 2, 4 or 8.
+template <int kN>
+__device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[kN]) {
+  uint64_t v[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = static_cast<uint64_t>(key[i]) << 32 | (kN - 1 - i);
+#pragma unroll
+  for (int p = 1; p < kN; p *= 2) {
+#pragma unroll
+    for (int q = p; q > 0; q /= 2) {
+#pragma unroll
+      for (int j = q % p; j + q < kN; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int a = i + j, b = i + j + q;
+          if (b < kN && a / (2 * p) == b / (2 * p)) {
+            const uint64_t x = v[a], y = v[b];
+            v[a] = x > y ? x : y;
+            v[b] = x > y ? y : x;
+          }
+        }
+      }
+    }
+  }
+  uint32_t at = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    key[i] = static_cast<uint32_t>(v[i] >> 32);
+    at |= (kN - 1 - static_cast<uint32_t>(v[i])) << (4 * i);
+  }
+  return at;
+}
+
 template <int kN, typename Key>
 __device__ __forceinline__ void top2(const Key (&key)[kN], uint32_t in, Key& a, Key& b) {
   a = b = 0;
@@ -208,12 +267,16 @@ __device__ __forceinline__ void merge2(Key& a, Key& b, int o) {
 // group has none).
 template <int kN, typename Key>
 __device__ __forceinline__ void group_top2(const RouterParams& p, const Key (&key)[kN], int lane,
-                                           Key& a, Key& b) {
-  const int lanes = p.per_group / kN;
-  if (lanes * kN == p.per_group && (lanes & (lanes - 1)) == 0) {
-    // a group is `lanes` whole lanes: all groups at once
+                                           bool sorted, Key& a, Key& b) {
+  const int lanes = p.group_lanes;
+  if (lanes) {  // a group is whole lanes: all groups at once
     Key x, y;
-    top2(key, kAll, x, y);
+    if (sorted) {
+      x = key[0];
+      y = kN > 1 ? key[kN > 1 ? 1 : 0] : 0;
+    } else {
+      top2(key, kAll, x, y);
+    }
     for (int o = 1; o < lanes; o *= 2) merge2(x, y, o);
     const int from = min(31, lane * lanes);
     a = __shfl_sync(kAll, x, from);
@@ -256,6 +319,10 @@ __device__ __forceinline__ uint32_t take_groups(const RouterParams& p, Key score
 // Bit i: expert e0 + i is in one of the groups of the mask.
 template <int kN>
 __device__ __forceinline__ uint32_t in_groups(const RouterParams& p, uint32_t groups, int e0) {
+  if (p.group_lanes) {
+    const int g = (e0 / kN) / p.group_lanes;
+    return g < p.groups && (groups >> g & 1u) ? kAll : 0u;
+  }
   uint32_t in = 0;
   int g = e0 / p.per_group, r = e0 - g * p.per_group;
 #pragma unroll
@@ -275,98 +342,80 @@ __device__ __forceinline__ Key group_key(const RouterParams& p, Key a, Key b) {
   return key_of(value_of(a) + value_of(b));
 }
 
-// The row's softmax in fp64: its maximum and 1 / its sum are the token's.
-struct Score64 {
-  double max, inv;
-  int sigmoid;
-  __device__ __forceinline__ double at(float l) const {
-    return sigmoid ? 1. / (1. + exp(-static_cast<double>(l)))
-                   : exp(static_cast<double>(l) - max) * inv;
-  }
-};
+// exp(x) for x <= 0 in fp64, to about 2^-51 of it: x = n ln 2 + r, the Taylor series
+// of exp(r) to r^13 (|r| < 0.35: the next term is below 2^-57), the exponent by its bits.
+__device__ __forceinline__ double exp64(double x) {
+  if (!(x > -700.)) return x != x ? x : 0.;
+  const float n = rintf(static_cast<float>(x) * 1.4426950408889634f);
+  double r = fma(static_cast<double>(n), -0.69314718055994530942, x);
+  r = fma(static_cast<double>(n), -2.3190468138462996e-17, r);  // ln 2 beyond its 53 bits
+  double y = 1. / 6227020800.;
+  y = fma(y, r, 1. / 479001600.);
+  y = fma(y, r, 1. / 39916800.);
+  y = fma(y, r, 1. / 3628800.);
+  y = fma(y, r, 1. / 362880.);
+  y = fma(y, r, 1. / 40320.);
+  y = fma(y, r, 1. / 5040.);
+  y = fma(y, r, 1. / 720.);
+  y = fma(y, r, 1. / 120.);
+  y = fma(y, r, 1. / 24.);
+  y = fma(y, r, 1. / 6.);
+  y = fma(y, r, 0.5);
+  y = fma(y, r, 1.);
+  y = fma(y, r, 1.);
+  return __longlong_as_double(__double_as_longlong(y) + static_cast<long long>(n) * (1LL << 52));
+}
 
-// The choice again, in fp64 for the experts that can be in question: those
-// within tol of the group_top-th of their group, then those of the groups taken
-// within tol of the k-th.
+// The choice again, in fp64.  Without a bias only the groups were in question, and
+// the experts go by their logits.
 template <int kN>
-__device__ __noinline__ void choose_64(const RouterParams& p, const float (&l)[kN],
-                                       const uint32_t (&key)[kN], float tol, float row_max,
+__device__ __noinline__ void choose_64(const RouterParams& p, const float (&l)[kN], float row_max,
                                        int lane, int& id) {
   const int e0 = lane * kN;
-  Score64 s{static_cast<double>(row_max), 0., p.sigmoid};
+  uint64_t key[kN];
+  double c[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const double x = l[i];
+    if (p.sigmoid) {
+      const double e = exp64(-fabs(x));
+      c[i] = (x < 0. ? e : 1.) / (1. + e);
+    } else {
+      c[i] = l[i] == -kInf ? 0. : exp64(x - row_max);
+    }
+  }
   if (!p.sigmoid) {
     double sum = 0.;
-#pragma unroll 1
-    for (int i = 0; i < kN; ++i)
-      if (l[i] != -kInf) sum += exp(static_cast<double>(l[i]) - s.max);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) sum += c[i];
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    s.inv = 1. / sum;
+    const double inv = 1. / sum;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) c[i] *= inv;
   }
-  uint64_t fine[kN];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) fine[i] = 0;
-  uint32_t done = 0;
-  auto evaluate = [&](uint32_t want) {  // bit i: expert e0 + i
-    want &= ~done;
-    done |= want;
-#pragma unroll 1
-    for (int i = 0; i < kN; ++i) {
-      if (want >> i & 1u) {
-        const double c = s.at(l[i]) + (p.bias ? static_cast<double>(__ldg(p.bias + e0 + i)) : 0.);
-        fine[i] = key_of(c);
-      }
-    }
-  };
-  // NaN keys (1) are known as they are
-#pragma unroll
-  for (int i = 0; i < kN; ++i)
-    if (key[i] == 1u) fine[i] = 1, done |= 1u << i;
+  for (int i = 0; i < kN; ++i) {
+    if (p.bias && e0 + i < p.E) c[i] += __ldg(p.bias + e0 + i);
+    key[i] = l[i] == -kInf ? 0 : key_of(c[i]);
+  }
   uint32_t in = kAll;
   if (p.topk_groups < p.groups) {
-    uint32_t a, b;
-    group_top2(p, key, lane, a, b);
-    const uint32_t edge = p.group_top == 2 && b != 0 ? b : a;
-    const float low = edge > 1u ? value_of(edge) : -kInf;
-    uint32_t want = 0;
-#pragma unroll 1
-    for (int g = 0; g < p.groups; ++g) {
-      const float from = __shfl_sync(kAll, low, g);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const int e = e0 + i - g * p.per_group;
-        if (e >= 0 && e < p.per_group && key[i] > 1u &&
-            !(value_of(key[i]) < from - (tol + fabsf(from) * 0x1p-21f)))
-          want |= 1u << i;
-      }
-    }
-    evaluate(want);
     uint64_t x, y, last, first;
-    group_top2(p, fine, lane, x, y);
-    const uint32_t groups = take_groups(p, group_key(p, x, y), lane, last, first);
-    in = in_groups<kN>(p, groups, e0);
+    group_top2(p, key, lane, false, x, y);
+    in = in_groups<kN>(p, take_groups(p, group_key(p, x, y), lane, last, first), e0);
   }
-  uint32_t rest[kN], own;
+  if (p.bias) {
+    uint64_t own;
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
-    rest[i] = !(in >> i & 1u) ? 0u : p.bias || key[i] <= 1u ? key[i] : key_of(l[i]);
-  if (!p.bias) {  // only the groups were in question
-    pick(rest, p.k, lane, id, own);
-    return;
+    for (int i = 0; i < kN; ++i)
+      if (!(in >> i & 1u)) key[i] = 0;
+    pick(key, p.k - 1, lane, id, own);
+  } else {
+    uint32_t logit[kN], own;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) logit[i] = (in >> i & 1u) && l[i] != -kInf ? key_of(l[i]) : 0u;
+    pick(logit, p.k - 1, lane, id, own);
   }
-  pick(rest, p.k - 1, lane, id, own);  // (its last pick is the k-th)
-  const uint32_t kth = __shfl_sync(kAll, own, p.k - 1);
-  const float from = kth > 1u ? value_of(kth) : -kInf;
-  const float edge = from - (tol + fabsf(from) * 0x1p-21f);
-  uint32_t want = 0;
-#pragma unroll
-  for (int i = 0; i < kN; ++i)
-    if ((in >> i & 1u) && key[i] > 1u && !(value_of(key[i]) < edge)) want |= 1u << i;
-  evaluate(want);
-#pragma unroll
-  for (int i = 0; i < kN; ++i)
-    if (!(in >> i & 1u)) fine[i] = 0;
-  uint64_t none;
-  pick(fine, p.k, lane, id, none);
 }
 
 template <typename T, int kN>
@@ -399,36 +448,54 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
     }
   }
   auto score = [&](float x) { return p.sigmoid ? sigmoid_f32(x) : expf(x - m) * inv; };
+  // for the order alone: the fast exponential and quotient
+  auto rough = [&](float x) {
+    return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : __expf(x - m) * inv;
+  };
 
-  // What fp32 leaves of c: a score is off by 2 units of exp, 1 of the division
-  // and of 1 + exp (sigmoid), or by the exponent's rounding (|l - m| 2^-24, of
-  // a score that falls faster than that) and the sum's (10 of its tree), each of
-  // 2^-24 of at most the largest score: 4 and 16 of them; the sum with the bias
-  // adds 2^-24 of itself, counted where it is compared.
+  // What fp32 leaves of c, in units of 2^-24 of the largest score.  Sigmoid: the
+  // exponential's 2 + 1.2 |l| count s (1 - s) times, half a unit at most; 1 + exp, the
+  // quotient's 2: below 4.  Softmax: the exponent's |l - m| and the fast
+  // exponential's 2 + 1.2 |l - m| of a score that falls faster than that, 3; the
+  // sum's 10 of its tree and 2 of its terms, the quotient's and the product's: below 24.
+  // The sum with the bias adds 2^-24 of itself, counted where it is compared.
   const float tol = (p.sigmoid ? 0x1p-20f : 0x1p-18f) * unit;
   uint32_t key[kN];
   if (by_score) {
+    float b[kN];
+    load_row<float, kN>(p.bias, e0, p.E, p.bias_wide, 0.f, b);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float b = e0 + i < p.E ? __ldg(p.bias + e0 + i) : 0.f;
-      key[i] = l[i] == -kInf ? 0u : broken ? 1u : key_of(score(l[i]) + b);
-    }
+    for (int i = 0; i < kN; ++i)
+      key[i] = l[i] == -kInf ? 0u : broken ? 1u : key_of(rough(l[i]) + b[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < kN; ++i) key[i] = l[i] == -kInf ? 0u : broken ? 1u : key_of(l[i]);
   }
+  constexpr bool kSort = kN <= 8;
+  uint32_t at = 0;
+  if constexpr (kSort) at = sort_lane(key);
 
   auto near = [&](uint32_t hi, uint32_t lo) {
     const float x = value_of(hi), y = value_of(lo);
     return lo > 1u && !(x - y > tol + (fabsf(x) + fabsf(y)) * 0x1p-22f);
   };
   bool redo = false;
-  uint32_t work[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) work[i] = key[i];
   if (groups) {
     uint32_t a, b, last, first;
-    group_top2(p, key, lane, a, b);
+    if (kSort && !p.group_lanes) {  // (by the experts' own places: sorted keys have lost them)
+      uint32_t own[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) own[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const uint32_t place = at >> (4 * j) & 15u;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) own[i] = place == static_cast<uint32_t>(i) ? key[j] : own[i];
+      }
+      group_top2(p, own, lane, false, a, b);
+    } else {
+      group_top2(p, key, lane, kSort, a, b);
+    }
     // keys are logits without a bias: their sums are the scores'
     const bool sums = p.group_top == 2;
     if (!by_score && sums) {
@@ -441,13 +508,36 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
       redo = first > 1u && !(value_of(last) - value_of(first) >
                              2.f * tol + (fabsf(value_of(last)) + fabsf(value_of(first))) * 0x1p-21f);
     const uint32_t in = in_groups<kN>(p, mask, e0);
+    if (kSort && !p.group_lanes) {
+      // (a lane may lie in several groups: its sorted list without those left out)
+      uint32_t kept[kN], places = 0;
+      int n = 0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (!(in >> i & 1u)) work[i] = 0;
+      for (int i = 0; i < kN; ++i) kept[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const uint32_t place = at >> (4 * j) & 15u;
+        if (in >> place & 1u) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (i == n) kept[i] = key[j];
+          places |= place << (4 * n);
+          ++n;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) key[i] = kept[i];
+      at = places;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (!(in >> i & 1u)) key[i] = 0;  // (of a sorted list all or none)
+    }
   }
   int id;
   uint32_t own;
-  pick(work, p.k, lane, id, own);
+  if constexpr (kSort) pick_sorted(key, at, p.k, lane, id, own);
+  else pick(key, p.k, lane, id, own);
   if (by_score) {
     // lane j against pick j + 1 (k of 32 has no lane for the runner-up: always
     // looked at again)
@@ -460,15 +550,10 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
     redo |= __any_sync(kAll, close) || p.k == 32;
   }
   if (redo && !broken) {
-    // (copies: what a call takes by reference does not stay in registers)
-    float l2[kN];
-    uint32_t key2[kN];
+    float l2[kN];  // (a copy: what a call takes by reference does not stay in registers)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      l2[i] = l[i];
-      key2[i] = by_score || key[i] <= 1u ? key[i] : key_of(score(l[i]));
-    }
-    choose_64<kN>(p, l2, key2, tol, m, lane, id);
+    for (int i = 0; i < kN; ++i) l2[i] = l[i];
+    choose_64<kN>(p, l2, m, lane, id);
   }
   if (lane >= p.k) id = -1;
 
@@ -573,6 +658,9 @@ cudaError_t launch_width(RouterParams p, bool backward, cudaStream_t s) {
   const int n = p.E <= 32 ? 1 : p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
   const uintptr_t all = reinterpret_cast<uintptr_t>(p.logits) |
                         (backward ? reinterpret_cast<uintptr_t>(p.d_logits) : 0);
+  p.bias_wide = p.E % n == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
+  const int lanes = p.per_group / n;
+  p.group_lanes = lanes * n == p.per_group && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   p.wide = p.E % n == 0 && all % 16 == 0 && (p.ld * static_cast<long>(sizeof(T))) % 16 == 0;
   return n == 1    ? launch<T, 1>(p, backward, s)
          : n == 2  ? launch<T, 2>(p, backward, s)
