@@ -187,28 +187,34 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
 }
 
 // The same from lists that every lane has sorted, highest first and the first among
-// equal ones: `at` holds their places, four bits each.
+// equal ones: `at` holds their places, four bits each.  Pick `j` alone; false where
+// nothing is left.
 template <int kN>
-__device__ __forceinline__ void pick_sorted(uint32_t (&key)[kN], uint32_t at, int k, int lane,
+__device__ __forceinline__ bool pick_one(uint32_t (&key)[kN], uint32_t& at, int j, int lane, int& id,
+                                         uint32_t& own) {
+  const uint32_t best = warp_max(key[0]);
+  if (best == 0) return false;
+  const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+  const int place = __shfl_sync(kAll, at, from) & 15;
+  if (lane == from) {
+#pragma unroll
+    for (int i = 0; i + 1 < kN; ++i) key[i] = key[i + 1];
+    key[kN - 1] = 0;
+    at >>= 4;
+  }
+  if (lane == j) {
+    id = from * kN + place;
+    own = best;
+  }
+  return true;
+}
+template <int kN>
+__device__ __forceinline__ void pick_sorted(uint32_t (&key)[kN], uint32_t& at, int k, int lane,
                                             int& id, uint32_t& own) {
   id = -1;
   own = 0;
-  for (int j = 0; j <= k && j < 32; ++j) {
-    const uint32_t best = warp_max(key[0]);
-    if (best == 0) break;
-    const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
-    const int place = __shfl_sync(kAll, at, from) & 15;
-    if (lane == from) {
-#pragma unroll
-      for (int i = 0; i + 1 < kN; ++i) key[i] = key[i + 1];
-      key[kN - 1] = 0;
-      at >>= 4;
-    }
-    if (lane == j) {
-      id = from * kN + place;
-      own = best;
-    }
-  }
+  for (int j = 0; j <= k && j < 32; ++j)
+    if (!pick_one(key, at, j, lane, id, own)) break;
 }
 
 // Sorts by an odd-even merge network (Batcher): kN = 1, 2, 4 or 8.
@@ -340,6 +346,111 @@ __device__ __forceinline__ Key group_key(const RouterParams& p, Key a, Key b) {
   if (a == 0) return 0;
   if (p.group_top == 1 || b == 0) return a;
   return key_of(value_of(a) + value_of(b));
+}
+
+// Two fp32 values whose sum is the number (Dekker, Knuth): 44 bits and more.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two fast_two_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  const float e = __fmaf_rn(a.hi, b.hi, -p);
+  return fast_two_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, e)));
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return fast_two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+
+// exp(x) for -80 <= x <= 0 (below: that of -80, 2^-115) to about 2^-43 of it: x = n ln 2
+// + r by three parts of ln 2, the first of 16 bits, the Taylor series to r^13, its
+// terms from r^7 on in fp32 (below 2^-22 of the sum).
+__device__ __forceinline__ Two exp_two(Two x) {
+  if (x.hi < -80.f) x = {-80.f, 0.f};
+  const float n = rintf(x.hi * 1.4426950408889634f);
+  Two r = two_sum(x.hi, -n * 0.693145751953125f);
+  const float p2 = __fmul_rn(n, 1.428606765330187e-06f);
+  r = add(r, {-p2, x.lo - __fmaf_rn(n, 1.428606765330187e-06f, -p2) - n * 5.497923148104107e-14f});
+  float t = 0x1.612462p-33f;
+  t = fmaf(t, r.hi, 0x1.1eed8ep-29f);
+  t = fmaf(t, r.hi, 0x1.ae6456p-26f);
+  t = fmaf(t, r.hi, 0x1.27e4fcp-22f);
+  t = fmaf(t, r.hi, 0x1.71de3ap-19f);
+  t = fmaf(t, r.hi, 0x1.a01a02p-16f);
+  t = fmaf(t, r.hi, 0x1.a01a02p-13f);
+  Two e = add({0x1.6c16c2p-10f, -0x1.27d27ep-35f}, mul(r, {t, 0.f}));
+  e = add({0x1.111112p-7f, -0x1.dddddep-32f}, mul(r, e));
+  e = add({0x1.555556p-5f, -0x1.555556p-30f}, mul(r, e));
+  e = add({0x1.555556p-3f, -0x1.555556p-28f}, mul(r, e));
+  e = add({0.5f, 0.f}, mul(r, e));
+  e = add({1.f, 0.f}, mul(r, e));
+  e = add({1.f, 0.f}, mul(r, e));
+  const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);  // n >= -116
+  return {e.hi * scale, e.lo * scale};
+}
+__device__ __forceinline__ Two inverse(Two d) {
+  const float y = __frcp_rn(d.hi);
+  return fast_two_sum(y, y * __fmaf_rn(-y, d.lo, __fmaf_rn(-y, d.hi, 1.f)));
+}
+
+// The first n picks, lane j's in lane j, in the order of their scores' 41 bits: all
+// of them are there that can be among the first n - 1.  False where they do not tell
+// two apart that are not the same logit and bias.
+template <typename T>
+__device__ __noinline__ bool order_picks(const RouterParams& p, const T* row, float m, int n, int lane,
+                                         int& id) {
+  const bool mine = lane < n && id >= 0;
+  const float l = mine ? to_float(row[id]) : 0.f, b = mine ? __ldg(p.bias + id) : 0.f;
+  Two c;
+  if (p.sigmoid) {
+    const Two e = exp_two({-fabsf(l), 0.f});
+    c = inverse(add({1.f, 0.f}, e));
+    if (l < 0.f) c = mul(e, c);
+  } else {
+    Two sum{0.f, 0.f};
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32) {
+      const float x = to_float(row[i]);
+      if (x != -kInf) sum = add(sum, exp_two(two_sum(x, -m)));
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1)
+      sum = add(sum, {__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
+    c = mul(exp_two(two_sum(l, -m)), inverse(sum));
+  }
+  c = add(c, {b, 0.f});
+  const float eps = 0x1p-40f * (1.f + fabsf(b));  // (twice the error of two)
+  int rank = 0;
+  bool unsure = false;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const float hi = __shfl_sync(kAll, c.hi, j), lo = __shfl_sync(kAll, c.lo, j);
+    const float lj = __shfl_sync(kAll, l, j), bj = __shfl_sync(kAll, b, j);
+    const int ij = __shfl_sync(kAll, id, j);
+    const float d = (hi - c.hi) + (lo - c.lo);
+    const bool same = lj == l && bj == b;
+    if (ij >= 0 && j != lane) {
+      rank += same ? (ij < id ? 1 : 0) : (d > 0.f ? 1 : 0);
+      unsure |= mine && !same && !(fabsf(d) > eps);
+    }
+  }
+  // lane `rank` takes this lane's id
+  int at = -1;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int rj = __shfl_sync(kAll, mine ? rank : -1, j), ij = __shfl_sync(kAll, id, j);
+    if (rj == lane) at = ij;
+  }
+  id = at;
+  return !__any_sync(kAll, unsure);
 }
 
 // exp(x) for x <= 0 in fp64, to about 2^-51 of it: x = n ln 2 + r, the Taylor series
@@ -547,7 +658,27 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
     if (close)  // the same logit and bias are the same score, and in order
       close = !(to_float(row[id]) == to_float(row[next_id]) &&
                 __ldg(p.bias + id) == __ldg(p.bias + next_id));
-    redo |= __any_sync(kAll, close) || p.k == 32;
+    bool tie = __any_sync(kAll, close) || p.k == 32;
+    if constexpr (kSort) {
+      if (tie && !redo && !broken && p.k < 31) {
+        // More picks, until one lies clear of the one before it; then they are put in
+        // order.
+        int n = p.k + 1;
+        bool clear = !near(__shfl_sync(kAll, own, n - 2), __shfl_sync(kAll, own, n - 1));
+        while (!clear && n < 32) {
+          clear = !pick_one(key, at, n, lane, id, own);
+          if (clear) break;  // no others
+          ++n;
+          clear = !near(__shfl_sync(kAll, own, n - 2), __shfl_sync(kAll, own, n - 1));
+        }
+        if (clear) {
+          int ordered = id;
+          tie = !order_picks<T>(p, row, m, n, lane, ordered);
+          if (!tie) id = ordered;
+        }
+      }
+    }
+    redo |= tie;
   }
   if (redo && !broken) {
     float l2[kN];  // (a copy: what a call takes by reference does not stay in registers)
