@@ -76,10 +76,10 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
       __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
-__device__ __forceinline__ float warp_fmax(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+__device__ __forceinline__ float warp_fmax(float v) {  // (a NaN counts as nothing)
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
@@ -730,28 +730,32 @@ __global__ void __launch_bounds__(256) router_backward_kernel(const RouterParams
   const bool have = x != -kInf;
   const float g = have ? p.scale * __ldg(p.dw + t * p.k + lane) : 0.f;
   float out[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) out[i] = 0.f;
-  float mine;  // of slot `lane`
+  float mine;        // of slot `lane`
+  float rest = 0.f;  // what its expert gets besides
   if (!p.sigmoid && !p.renormalize) {
-    float l[kN], ex[kN];
+    float l[kN];
     load_row<T, kN>(row, e0, p.E, p.wide, -kInf, l);
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < kN; ++i) m = fmaxf(m, l[i]);
     m = warp_fmax(m);
-    // (an expert out of the choice has the score 0, in a row of such ones too)
+    if (m == -kInf) m = 0.f;  // every expert is out of the choice: scores of 0
+    // the fast exponential: off by (2 + 1.2 |l - m|) 2^-24 of a score that falls faster
 #pragma unroll
-    for (int i = 0; i < kN; ++i) ex[i] = l[i] == -kInf ? 0.f : expf(l[i] - m);
-    const float sum = warp_add(tree_sum(ex));
+    for (int i = 0; i < kN; ++i) l[i] = __expf(l[i] - m);
+    const float sum = warp_add(tree_sum(l));
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    mine = have ? g * (expf(x - m) * inv) : 0.f;
-    const float dot = warp_add(mine);
+    const float s = have ? __expf(x - m) * inv : 0.f;
+    mine = g * s;
+    const float dot = warp_add(mine), f = -inv * dot;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) out[i] = l[i] == -kInf ? 0.f : -(ex[i] * inv) * dot;
+    for (int i = 0; i < kN; ++i) out[i] = l[i] * f;
+    rest = -(s * dot);
   } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = 0.f;
     const float s = p.sigmoid ? sigmoid_f32(x) : 0.f;
-    const float rest = p.sigmoid ? 1.f / (1.f + expf(x)) : 1.f;  // 1 - s
+    const float off = p.sigmoid ? 1.f / (1.f + expf(x)) : 1.f;  // 1 - s
     if (p.renormalize) {
       const float top = warp_fmax(x);
       float u = p.sigmoid && top > -20.f ? s : x == top ? 1.f : expf(x - top);
@@ -759,20 +763,28 @@ __global__ void __launch_bounds__(256) router_backward_kernel(const RouterParams
       if (have && x != x) u = x;
       const float total = warp_add(u), q = have ? u / total : 0.f;
       const float dot = warp_add(g * q);
-      mine = q * rest * (g - dot);
+      mine = q * off * (g - dot);
     } else {
-      mine = g * s * rest;
+      mine = g * s * off;
     }
-    if (!have) mine = 0.f;
   }
-  for (int j = 0; j < p.k; ++j) {
-    const int at = __shfl_sync(kAll, have ? id : -1, j) - e0;
-    const float v = __shfl_sync(kAll, mine, j);
+  T* d_row = static_cast<T*>(p.d_logits) + t * p.ld;
+  // an expert in several slots gets their sum
+  const uint32_t same = __match_any_sync(kAll, have ? id : -1 - lane);
+  if (__any_sync(kAll, (same & (same - 1)) != 0)) {
+    for (int j = 0; j < p.k; ++j) {
+      const int at = __shfl_sync(kAll, have ? id : -1, j) - e0;
+      const float v = __shfl_sync(kAll, mine, j);
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (at == i) out[i] += v;
+      for (int i = 0; i < kN; ++i)
+        if (at == i) out[i] += v;
+    }
+    store_row<T, kN>(d_row, e0, p.E, p.wide, out);
+  } else {  // the row, then the slots' experts over it
+    store_row<T, kN>(d_row, e0, p.E, p.wide, out);
+    __syncwarp();
+    if (have) from_float(d_row[id], mine + rest);
   }
-  store_row<T, kN>(static_cast<T*>(p.d_logits) + t * p.ld, e0, p.E, p.wide, out);
 }
 
 template <typename T, int kN>

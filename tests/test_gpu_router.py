@@ -323,6 +323,21 @@ def test_backward_of_masked_slots_and_experts():
             assert ((got - want).abs() <= 1e-5 * dw.abs().sum(1, keepdim=True)).all()
 
 
+def test_backward_of_an_expert_in_several_slots():
+    T, E, k = 20, 50, 5
+    logits, _ = draw(T, E)
+    for dtype in (F32, BF):
+        l = logits.to(dtype)
+        for score in ("softmax", "sigmoid"):
+            for renorm in (True, False):
+                p = moe.RouterProblem.make(T, E, k, dtype, score, renormalize=renorm)
+                ids, _ = reference(p, l, None)
+                ids[3, 4] = ids[3, 0]
+                ids[7:9] = 49
+                ids[9, :3] = ids[9, 3]
+                check_backward(p, dtype, ids, l)
+
+
 def test_gradient_against_differences():
     """Central differences of the forward's own weights, in the part of the logits where the choice
     stays: a step of 2^-6 is off by its square times the third derivative (below 1/8 of the largest
