@@ -180,15 +180,17 @@ def _workspace(ws: torch.Tensor):
     return ws.data_ptr(), ws.nbytes
 
 
-# the current stream's handle without a Stream object around it (3 us of a call of 11)
+# the current stream's handle without a Stream object around it (3 us of a call of 11), and
+# the device's number without a look at whether CUDA runs (0.2 us; its tensors say so)
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _raw_stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _current_raw is not None:
-        return _current_raw(torch.cuda.current_device())
+        return _current_raw(_device())
     return torch.cuda.current_stream().cuda_stream
 
 

@@ -148,29 +148,23 @@ __device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, bool p
 }
 
 // Expert offsets into s_off[E + 1] and the experts' first tiles into
-// s_tile[E + 1], tiles of `rows` rows; the number of tiles (0, and the status,
-// where the offsets decrease or leave [0, M]).  Every thread of the block.
-template <int kBlockThreads>
-__device__ __forceinline__ int build_tiles(const int32_t* offsets, int E, int M, int n_tiles,
-                                           int rows, int32_t* s_off, int32_t* s_tile,
-                                           uint32_t* status) {
-  __shared__ int s_part[kBlockThreads / 32];
+// s_tile[E + 1]; the number of tiles (0, and the status, where the offsets decrease
+// or leave [0, M]).  Every thread of the block.
+__device__ __forceinline__ int build_tiles(const MmParams& p, int32_t* s_off, int32_t* s_tile) {
+  __shared__ int s_part[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i <= E; i += kBlockThreads)
-    s_off[i] = offsets ? offsets[i] : i == 0 ? 0 : M;
-  __syncthreads();
-  const int per = (E + kBlockThreads - 1) / kBlockThreads;
-  const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
+  const int per = (p.E + kThreads - 1) / kThreads;
+  const int e0 = min(p.E, static_cast<int>(threadIdx.x) * per), e1 = min(p.E, e0 + per);
   bool bad = false;
-  int run = 0;
+  int run = 0, a = 0;
   for (int e = e0; e < e1; ++e) {
-    const int a = s_off[e], b = s_off[e + 1];
-    if (a < 0 || b < a || b > M) bad = true;
-    else run += (b - a + rows - 1) / rows * n_tiles;
-  }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) record_status(status, kStatusIndex);
-    return 0;
+    if (e == e0) a = p.offsets ? p.offsets[e] : 0;
+    const int b = p.offsets ? p.offsets[e + 1] : p.M;
+    s_off[e] = a;
+    if (e + 1 == p.E) s_off[p.E] = b;
+    if (a < 0 || b < a || b > p.M) bad = true;
+    else run += (b - a + p.tile_rows - 1) / p.tile_rows * p.n_tiles;
+    a = b;
   }
   int incl = run;
 #pragma unroll
@@ -179,19 +173,23 @@ __device__ __forceinline__ int build_tiles(const int32_t* offsets, int E, int M,
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_part[warp] = incl;
-  __syncthreads();
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_status(p.status, kStatusIndex);
+    return 0;
+  }
   int acc = incl - run, total = 0;
-  for (int w = 0; w < kBlockThreads / 32; ++w) {
-    if (w < warp) acc += s_part[w];
-    total += s_part[w];
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int part = s_part[w];
+    if (w < warp) acc += part;
+    total += part;
   }
   for (int e = e0; e < e1; ++e) {
     s_tile[e] = acc;
-    acc += (s_off[e + 1] - s_off[e] + rows - 1) / rows * n_tiles;
+    acc += (s_off[e + 1] - s_off[e] + p.tile_rows - 1) / p.tile_rows * p.n_tiles;
   }
-  if (threadIdx.x == 0) s_tile[E] = total;
-  __syncthreads();
-  return total;
+  if (threadIdx.x == 0) s_tile[p.E] = total;
+  return total;  // (the caller's barrier shows the tiles to every thread)
 }
 
 // The tiles of a CTA (pair), in order: which expert's, and where.
@@ -551,8 +549,7 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
   }
   // nothing above touches global memory
   pdl_enter();
-  const int total = build_tiles<kThreads>(p.offsets, p.E, p.M, p.n_tiles, p.tile_rows, sm.off(),
-                                          sm.tile(), p.status);
+  const int total = build_tiles(p, sm.off(), sm.tile());
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();  // both CTAs' barriers exist before anything signals them
@@ -824,8 +821,12 @@ cudaError_t launch_tiles(const moe_fp8_problem* p, const void* x, const void* w,
                          cudaStream_t s) {
   constexpr int kCtas = kPair ? 2 : 1;
   Maps maps;
-  for (int i = 0; i < kBoxes; ++i)
-    if (!make_codes_map(&maps.x[i], x, p->K, p->M, 0, k.planes, 16 << i)) return cudaErrorInvalidValue;
+  // boxes up to the rows of a tile, or all rows (the others' maps are not used: copies)
+  const int most_rows = std::min(kPair ? 128 : k.tile_rows, p->M);
+  for (int i = 0; i < kBoxes; ++i) {
+    if (i > 0 && (8 << i) >= most_rows) maps.x[i] = maps.x[i - 1];
+    else if (!make_codes_map(&maps.x[i], x, p->K, p->M, 0, k.planes, 16 << i)) return cudaErrorInvalidValue;
+  }
   if (!make_codes_map(&maps.w, w, p->K, p->N, p->E, k.planes, 128)) return cudaErrorInvalidValue;
   k.n_tiles = ceil_div(p->N, 128 * kCtas);
   k.x_stage = 2 * kBlk * (kPair ? 128 : k.tile_rows);
