@@ -54,9 +54,13 @@ constexpr size_t kSmem = 1024 + kRing + kBarBytes + 2 * kFactors * sizeof(float)
                          2 * (kMaxE + 1) * sizeof(int32_t);
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert((2 * kMaxStages + 10) * 8 + 8 <= kBarBytes, "barrier area");
-// registers: a launch's 168 x 384, moved as 56 x 128 + 224 x 256
-constexpr int kRegsOther = 56, kRegsEpilogue = 224;
-static_assert(kRegsOther * 128 + kRegsEpilogue * 32 * kEpiWarps <= 168 * kThreads, "register split");
+// registers: a launch's 168 x 384, moved to the epilogue as far as the others can do
+// without
+template <bool kSplit>
+struct Regs {
+  static constexpr int kOther = kSplit ? 72 : 56, kEpilogue = kSplit ? 216 : 224;
+  static_assert(kOther * 128 + kEpilogue * 32 * kEpiWarps <= 168 * kThreads, "register split");
+};
 
 struct MmParams {
   const int32_t* offsets;  // NULL: one expert, all rows
@@ -66,6 +70,7 @@ struct MmParams {
   int M, N, E, kblocks, nblocks, n_tiles;
   int tile_rows;    // rows of a tile at most: 256 (pairs), or of a narrow one
   int stages;       // of the ring
+  int splits;       // of K: CTAs of a cluster that share a tile (single CTAs, else 1)
   uint32_t x_stage; // bytes of a stage's rows in one CTA
   int planes;  // operands come as planes
   int f32;     // out
@@ -262,13 +267,30 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// v += four values of a CTA's shared memory of the cluster.
+__device__ __forceinline__ void add_cluster(float (&v)[4], uint32_t addr_cluster) {
+  float a[4];
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3])
+               : "r"(addr_cluster)
+               : "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] += a[j];
+}
+
 struct Maps {
   CUtensorMap x[kBoxes], w;  // x in boxes of 16, 32, 64 and 128 rows
 };
 
-// Shared memory behind the ring, by constant offsets from its aligned base.
+// Shared memory behind the ring, by constant offsets from its aligned base; and (where
+// CTAs share a tile) how many blocks along K this CTA has of it.
 struct Smem {
   uint8_t* base;
+  int part;
+  template <bool kSplit>
+  __device__ __forceinline__ int blocks(const MmParams& p) const {
+    return kSplit ? part : p.kblocks;
+  }
   __device__ __forceinline__ uint64_t* bar(int i) const {
     return reinterpret_cast<uint64_t*>(base + kRing) + i;
   }
@@ -302,7 +324,7 @@ struct Turn {
 };
 
 // The epilogue warps' part of a tile.
-template <bool kPair>
+template <bool kPair, bool kSplit>
 struct Epilogue {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kN = 128 * kCtas;
@@ -324,7 +346,7 @@ struct Epilogue {
         go = __all_sync(0xffffffffu, ok);
         if (!go) return false;
         factors = sm.factors(chunk & 1);
-        left = min(kChunk, p.kblocks - kb);
+        left = min(kChunk, sm.blocks<kSplit>(p) - kb);
       }
       ok = ok && mbar_wait(sm.tfull(buf), par, p.status);
       __syncwarp();
@@ -364,10 +386,10 @@ struct Epilogue {
   // A tile that this warp has no part of.
   static __device__ __forceinline__ Turn idle(const MmParams& p, Smem sm, Turn turn) {
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < p.kblocks; kb += kHand) {
+    for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kHand) {
       if (!walk.next(kb)) break;
       walk.release();
-      walk.release_factors(min(kHand, p.kblocks - kb));
+      walk.release_factors(min(kHand, sm.blocks<kSplit>(p) - kb));
     }
     return walk.done();
   }
@@ -381,7 +403,7 @@ struct Epilogue {
 #pragma unroll
     for (int j = 0; j < 128; ++j) sum[j] = 0.f;
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < p.kblocks; ++kb) {
+    for (int kb = 0; kb < sm.blocks<kSplit>(p); ++kb) {
       if (!walk.next(kb)) break;
       const float f = walk.factors[group * 128 + quad * 32 + lane];
       const uint32_t tm = tm0 + walk.buf * 256;
@@ -442,10 +464,10 @@ struct Epilogue {
 #pragma unroll
     for (int j = 0; j < 32 * kParts; ++j) sum[j] = 0.f;
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < p.kblocks; kb += kHand) {
+    for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kHand) {
       if (!walk.next(kb)) break;
       const uint32_t tm = tm0 + walk.buf * 256;
-      const int blocks = min(kHand, p.kblocks - kb);
+      const int blocks = min(kHand, sm.blocks<kSplit>(p) - kb);
       uint32_t a[kHand][kParts][32];
 #pragma unroll
       for (int h = 0; h < kHand; ++h) {  // (a second block that is not there is not used)
@@ -480,6 +502,13 @@ struct Epilogue {
       walk.release_factors(blocks);
     }
     turn = walk.done();
+    if (kSplit) {  // for the join, in the ring (this tile is the CTA's last)
+      float* part = reinterpret_cast<float*>(sm.base) + quad * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < 32 * kParts; ++j)
+        part[(group * 32 + (j / 32) * 64 + j % 32) * 128] = sum[j];
+      return turn;
+    }
     const int col = t.n * kN + rank * 128 + quad * 32 + lane;
     if (turn.go && col < p.N) {
       const long step = opaque(p.N);
@@ -511,7 +540,8 @@ struct Epilogue {
   }
 };
 
-template <bool kPair>
+// kSplit (single CTAs): the CTAs of a cluster share one tile along K.
+template <bool kPair, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmParams p) {
   constexpr int kCtas = kPair ? 2 : 1;
@@ -520,7 +550,12 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sW = smem;  // [stage][2 planes]
   uint8_t* sX = smem + p.stages * 2 * kPlane;
-  const Smem sm{smem};
+  static_assert(!(kPair && kSplit), "pairs have whole tiles");
+  // the blocks of K, whole stages of them, that are this CTA's
+  const int split = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int all = (p.kblocks + 1) / 2;
+  const int kb0 = kSplit ? all * split / p.splits * 2 : 0;
+  const Smem sm{smem, kSplit ? min(p.kblocks, all * (split + 1) / p.splits * 2) - kb0 : 0};
   volatile int* abort_flag = sm.abort_flag();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -555,10 +590,12 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
   if (kPair) cluster_sync();  // both CTAs' barriers exist before anything signals them
   tc_fence_after();
   const uint32_t tmem_base = *sm.tmem_slot();
-  const int first = static_cast<int>(blockIdx.x) / kCtas, step = static_cast<int>(gridDim.x) / kCtas;
+  const int group_ctas = kPair ? 2 : kSplit ? p.splits : 1;
+  const int first = static_cast<int>(blockIdx.x) / group_ctas;
+  const int step = static_cast<int>(gridDim.x) / group_ctas;
 
   if (warp < 4) {
-    regs_down<kRegsOther>();
+    regs_down<Regs<kSplit>::kOther>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- producer
       const uint64_t pol = policy_evict_normal();
@@ -573,12 +610,12 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
         const int col = (t.n * kCtas + rank) * 128;
         const uint32_t plane = t.x_plane(), bytes = kCtas * 2 * (kPlane + plane);
         const CUtensorMap* map = &maps.x[t.box];
-        for (int kb = 0; kb < p.kblocks; kb += 2) {
+        for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += 2) {
           if (!mbar_wait(sm.empty(stage), phase ^ 1, p.status)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(sm.full(stage), bytes);
-          load_w<kPair>(sW + stage * 2 * kPlane, &maps.w, p.planes, kb, col, t.e, kPlane, sm.full(stage),
+          load_w<kPair>(sW + stage * 2 * kPlane, &maps.w, p.planes, kb0 + kb, col, t.e, kPlane, sm.full(stage),
                         pol);
-          load_x<kPair>(sX + stage * p.x_stage, map, p.planes, kb, row, plane, sm.full(stage), pol);
+          load_x<kPair>(sX + stage * p.x_stage, map, p.planes, kb0 + kb, row, plane, sm.full(stage), pol);
           ++issued;
           if (++stage == p.stages) { stage = 0; phase ^= 1; }
         }
@@ -610,8 +647,8 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
         t.at<kPair>(i, p, sm.off(), sm.tile());
         const uint32_t plane = t.x_plane();
         const uint32_t idesc = idesc_e4m3(128 * kCtas, t.narrow ? kCtas * t.half : kN);
-        for (int kb = 0; kb < p.kblocks; kb += 2) {
-          const int blocks = min(2, p.kblocks - kb), units = kPair ? blocks : 1;
+        for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += 2) {
+          const int blocks = min(2, sm.blocks<kSplit>(p) - kb), units = kPair ? blocks : 1;
           const int u = (seg ^ mine) & 1;  // this issuer's of the stage's units, if it has one
           if (!mbar_wait(sm.full(stage), phase, p.status)) { ok = false; break; }
           // A stage is empty when the tensor core is through with it and both issuers
@@ -659,14 +696,14 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
         const int row0 = t.row + (t.narrow ? 0 : rank * 128);
         const int rows = t.narrow ? t.left : t.left - rank * 128;
         const int nb = min(t.n * kCtas + (t.narrow ? rank : 0), p.nblocks - 1);
-        const float* ws = p.ws + (static_cast<long>(t.e) * p.nblocks + nb) * p.kblocks;
+        const float* ws = p.ws + (static_cast<long>(t.e) * p.nblocks + nb) * p.kblocks + kb0;
         const long second = nb + 1 < p.nblocks ? p.kblocks : 0;  // the next weight block's
-        for (int kb = 0; ok && kb < p.kblocks; kb += kChunk, ++chunk) {
+        for (int kb = 0; ok && kb < sm.blocks<kSplit>(p); kb += kChunk, ++chunk) {
           const int buf = chunk & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(sm.fempty(buf), ((chunk >> 1) & 1) ^ 1, p.status));
           if (!ok) break;
           float* out = sm.factors(buf);
-          const int n = min(kChunk, p.kblocks - kb);
+          const int n = min(kChunk, sm.blocks<kSplit>(p) - kb);
           // lane j of eight has block j's weight scales
           const int j8 = lane & 7;
           const float w0 = j8 < n ? __ldg(ws + kb + j8) : 0.f;
@@ -675,7 +712,7 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
           for (int q = 0; q < 4; ++q) {
             if (32 * q >= rows && q > 0) break;  // rows that nothing uses
             const int r = 32 * q + lane;
-            const float* xs = p.xs + (static_cast<long>(row0) + r) * p.kblocks + kb;
+            const float* xs = p.xs + (static_cast<long>(row0) + r) * p.kblocks + kb0 + kb;
             float x[kChunk];
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) x[j] = r < rows && j < n ? __ldg(xs + j) : 0.f;
@@ -692,8 +729,12 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
       if (!ok && lane == 0) *abort_flag = 1;
     }
     __syncwarp();
+    if (kSplit) {  // with the epilogue's below
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
-    regs_up<kRegsEpilogue>();
+    regs_up<Regs<kSplit>::kEpilogue>();
     // ---------------------------------------------------------------- epilogue
     Turn turn;
     int e = 0;
@@ -703,10 +744,48 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
       t.e = e;
       t.at<kPair>(i, p, sm.off(), sm.tile());
       e = t.e;
-      turn = Epilogue<kPair>::tile(p, sm, tmem_base, rank, i, t, turn);
+      turn = Epilogue<kPair, kSplit>::tile(p, sm, tmem_base, rank, i, t, turn);
       if (!turn.go && lane == 0) *abort_flag = 1;
     }
     __syncwarp();
+    if (kSplit) {
+      // Every CTA of the cluster has its part of the tile's sums in its ring; each adds
+      // every so manieth row of them up, in the order of K.
+      cluster_sync();
+      if (first < total) {
+        Tile t;
+        t.at<kPair>(first, p, sm.off(), sm.tile());
+        // a warp has a row at a time, a lane four columns; four rows are on their way
+        constexpr int kRows = 4;
+        const int col = t.n * 128 + 4 * lane;
+        const uint32_t part = smem_u32(sm.base) + 16 * lane;
+        for (int r0 = split + p.splits * (warp - 4); r0 < t.left; r0 += kRows * kEpiWarps * p.splits) {
+          float v[kRows][4] = {};
+#pragma unroll 2
+          for (int s = 0; s < p.splits; ++s) {
+            const uint32_t from = pair::mapa(part, s);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+              const int r = r0 + u * kEpiWarps * p.splits;
+              if (r < t.left) add_cluster(v[u], from + r * 512);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
+            const int r = r0 + u * kEpiWarps * p.splits;
+            const long at = static_cast<long>(t.row + r) * p.N + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (r < t.left && col + j < p.N) {
+                if (p.f32) static_cast<float*>(p.out)[at + j] = v[u][j];
+                else from_float(static_cast<Bf16*>(p.out)[at + j], v[u][j]);
+              }
+            }
+          }
+        }
+      }
+      cluster_sync();  // no CTA's shared memory goes before it has been read
+    }
   }
 
   tc_fence_before();
@@ -816,6 +895,22 @@ int rows_of_tile(const moe_fp8_problem* p, bool wide) {
   return best;
 }
 
+// Tiles at most, whatever the offsets.
+long most_tiles(const moe_fp8_problem* p, int rows, int n_tiles) {
+  return (ceil_div(p->M, rows) + (p->E == 1 ? 0L : std::min(p->E, p->M))) * n_tiles;
+}
+
+// CTAs that share a tile along K: two where the tiles leave at least as many SMs idle
+// as they take, four where they leave three times as many (clusters of four do not
+// fill every GPC: of five sixths of the SMs), each with eight blocks or more.  With
+// 1, 2, 4 and 8, us: M=1 N=4096 K=4096 11.6, 9.9, 9.8, 16.0; M=8 N=8192 K=8192 18.2,
+// 13.9, 19.2, 25.1; M=1 N=1024 K=8192 17.6, 12.7, 9.7, 9.6; M=60 N=2048 K=4096 12.8,
+// 10.8, 9.4, 16.6; M=100 N=1024 K=8192 20.1, 14.9, 11.7, 18.0; M=1 N=2048 K=1024 8.7, 8.5,
+// 8.6, 13.3.
+int splits_of(long tiles, int kblocks) {
+  return 4 * tiles <= num_sms() * 5 / 6 && kblocks >= 32 ? 4 : 2 * tiles <= num_sms() && kblocks >= 16 ? 2 : 1;
+}
+
 template <bool kPair>
 cudaError_t launch_tiles(const moe_fp8_problem* p, const void* x, const void* w, MmParams& k,
                          cudaStream_t s) {
@@ -831,14 +926,16 @@ cudaError_t launch_tiles(const moe_fp8_problem* p, const void* x, const void* w,
   k.n_tiles = ceil_div(p->N, 128 * kCtas);
   k.x_stage = 2 * kBlk * (kPair ? 128 : k.tile_rows);
   k.stages = std::min<int>(kMaxStages, kRing / (2 * kPlane + k.x_stage));
-  auto kern = fp8_matmul_kernel<kPair>;
+  const long most = most_tiles(p, k.tile_rows, k.n_tiles);
+  k.splits = kPair ? 1 : splits_of(most, k.kblocks);
+  const int ctas = kPair ? 2 : k.splits;  // of a tile
+  auto kern = k.splits > 1 ? fp8_matmul_kernel<false, true> : fp8_matmul_kernel<kPair, false>;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
-  const long most = (ceil_div(p->M, k.tile_rows) + static_cast<long>(std::min(p->E, p->M))) * k.n_tiles;
-  const int groups = static_cast<int>(std::max(1L, std::min<long>(num_sms() / kCtas, most)));
-  return launch_kernel(kern, dim3(static_cast<unsigned>(kCtas * groups)), dim3(kThreads), kSmem, s,
-                       kCtas, maps, k);
+  const int groups = static_cast<int>(std::max(1L, std::min<long>(num_sms() / ctas, most)));
+  return launch_kernel(kern, dim3(static_cast<unsigned>(ctas * groups)), dim3(kThreads), kSmem, s, ctas,
+                       maps, k);
 }
 
 }  // namespace

@@ -266,6 +266,18 @@ def test_product_lengths(K):
         check_product(M, 144, K, dtype=BF)
 
 
+@pytest.mark.parametrize("M,N,K,E", [(1, 1000, 4096, 1), (1, 128, 2048, 1), (33, 130, 2064, 1), (64, 512, 4112, 1),
+                                     (100, 300, 8192, 1), (128, 17, 16384, 1), (65, 1024, 2048, 1),
+                                     (5, 512, 4096, 4), (40, 130, 6144, 3), (3, 512, 4096, 60)])
+def test_product_of_few_rows_and_long_sums(M, N, K, E):
+    """Few tiles: several CTAs share one along K."""
+    offsets = None if E == 1 else cut(M, E, tail=min(2, M - 1))
+    for dtype in (F32, BF):
+        first, p = check_product(M, N, K, E, dtype, offsets)
+        again, _ = check_product(M, N, K, E, dtype, offsets)
+        assert torch.equal(first.nan_to_num(0.0), again.nan_to_num(0.0))
+
+
 @pytest.mark.parametrize("M,E", [(1, 3), (8, 128), (40, 7), (256, 128), (300, 4), (777, 5), (1000, 64),
                                  (2000, 3), (600, 1024)])
 def test_product_of_experts(M, E):
