@@ -43,7 +43,8 @@ extern "C" {
  * stay, and of their experts the k of the highest c are chosen, highest first.
  * Equal c (equal scores) go to the lowest id.  Without a bias the experts are
  * ordered by their logits; otherwise c and the groups' scores are compared as 64
- * bits have them: fp32 values that are too near to tell are computed again in fp64.
+ * bits have them: fp32 values that are too near to tell are computed again, in pairs
+ * of fp32 and in fp64 where those do not tell.
  *   w_j   = scale * s_j / (renormalize ? sum over the chosen of s : 1)
  * An expert whose logit is -infinity is out of the token's choice: it counts in
  * no group, and slots for which no expert is left get the id -1, which masks a

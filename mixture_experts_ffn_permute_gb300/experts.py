@@ -187,7 +187,8 @@ class FP8Experts:
     """Convenience holder: the experts' weights in 8 bits (quantised here from ``w1`` [E, 2F, H] and
     ``w2`` [E, H, F], bf16 or fp32) and the reusable workspaces of one token count.  A call runs the
     layer of given routing on bf16 rows: quantise, permute, first product, SwiGLU and quantise,
-    second product, weighted sum."""
+    second product, weighted sum.  H is a multiple of 256 and F one of 128, as the layer's are; the
+    workspaces are its own, so one call runs at a time."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int, glu_interleave=0,
                  swiglu_clamp=0.0):
