@@ -35,7 +35,9 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kForwardThreads = 128;  // (256: 0.7 us more at T=8192 E=256, the last blocks' wait)
 constexpr float kInf = INFINITY;
+constexpr uint32_t kMinusInf = 0x007fffffu;  // its key (below)
 
 struct RouterParams {
   const void* logits;
@@ -191,20 +193,23 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
 }
 
 // The same from lists that every lane has sorted, highest first and the first among
-// equal ones: `at` holds their places, four bits each.  Pick `j` alone; false where
-// nothing is left.
-template <int kN>
+// equal ones.  Packed keys have their places in the lane in their last three bits (7:
+// the first), which do not count; else `at` holds the places, four bits each.  Pick `j`
+// alone; false where nothing is left.
+template <bool kPacked, int kN>
 __device__ __forceinline__ bool pick_one(uint32_t (&key)[kN], uint32_t& at, int j, int lane, int& id,
                                          uint32_t& own) {
-  const uint32_t best = warp_max(key[0]);
+  uint32_t best = warp_max(key[0]);
   if (best == 0) return false;
-  const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
-  const int place = __shfl_sync(kAll, at, from) & 15;
+  if (kPacked) best &= ~7u;
+  const int from = __ffs(__ballot_sync(kAll, key[0] >= best)) - 1;
+  const int place = kPacked ? 7 - static_cast<int>(__shfl_sync(kAll, key[0], from) & 7u)
+                            : static_cast<int>(__shfl_sync(kAll, at, from) & 15u);
   if (lane == from) {
 #pragma unroll
     for (int i = 0; i + 1 < kN; ++i) key[i] = key[i + 1];
     key[kN - 1] = 0;
-    at >>= 4;
+    if (!kPacked) at >>= 4;
   }
   if (lane == j) {
     id = from * kN + place;
@@ -212,46 +217,74 @@ __device__ __forceinline__ bool pick_one(uint32_t (&key)[kN], uint32_t& at, int 
   }
   return true;
 }
-template <int kN>
+template <bool kPacked, int kN>
 __device__ __forceinline__ void pick_sorted(uint32_t (&key)[kN], uint32_t& at, int k, int lane,
                                             int& id, uint32_t& own) {
   id = -1;
   own = 0;
   for (int j = 0; j <= k && j < 32; ++j)
-    if (!pick_one(key, at, j, lane, id, own)) break;
+    if (!pick_one<kPacked>(key, at, j, lane, id, own)) break;
 }
 
 // Sorts by an odd-even merge network (Batcher): kN = 1, 2, 4 or 8.
-template <int kN>
-__device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[kN]) {
-  uint64_t v[kN];
+template <int kN, typename Key>
+__device__ __forceinline__ void sort_network(Key (&v)[kN]) {
+  if constexpr (kN > 1) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = static_cast<uint64_t>(key[i]) << 32 | (kN - 1 - i);
+    for (int p = 1; p < kN; p *= 2) {
 #pragma unroll
-  for (int p = 1; p < kN; p *= 2) {
+      for (int q = p; q > 0; q /= 2) {
 #pragma unroll
-    for (int q = p; q > 0; q /= 2) {
+        for (int j = q % p; j + q < kN; j += 2 * q) {
 #pragma unroll
-      for (int j = q % p; j + q < kN; j += 2 * q) {
-#pragma unroll
-        for (int i = 0; i < q; ++i) {
-          const int a = i + j, b = i + j + q;
-          if (b < kN && a / (2 * p) == b / (2 * p)) {
-            const uint64_t x = v[a], y = v[b];
-            v[a] = x > y ? x : y;
-            v[b] = x > y ? y : x;
+          for (int i = 0; i < q; ++i) {
+            const int a = i + j, b = i + j + q;
+            if (b < kN && a / (2 * p) == b / (2 * p)) {
+              const Key x = v[a], y = v[b];
+              v[a] = x > y ? x : y;
+              v[b] = x > y ? y : x;
+            }
           }
         }
       }
     }
   }
+}
+
+// Packed: two instructions an exchange, where 64 bits take six.  (Below 8 is none, from 8
+// a NaN, from kPackedInf -inf.)
+constexpr uint32_t kPackedInf = 0x00800000u;
+template <bool kPacked, int kN>
+__device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[kN]) {
   uint32_t at = 0;
+  if constexpr (kPacked) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    key[i] = static_cast<uint32_t>(v[i] >> 32);
-    at |= (kN - 1 - static_cast<uint32_t>(v[i])) << (4 * i);
+    for (int i = 0; i < kN; ++i)
+      key[i] = key[i] == 0 ? 0u : (max(key[i], key[i] == kMinusInf ? kPackedInf : 8u) & ~7u) | (7u - i);
+    sort_network(key);
+  } else {
+    uint64_t v[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = static_cast<uint64_t>(key[i]) << 32 | (kN - 1 - i);
+    sort_network(v);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      key[i] = static_cast<uint32_t>(v[i] >> 32);
+      at |= (kN - 1 - static_cast<uint32_t>(v[i])) << (4 * i);
+    }
   }
   return at;
+}
+// The key without its place: the value is at most eight steps above the key's.
+__device__ __forceinline__ uint32_t unpacked(uint32_t key) {
+  return key < 8u ? 0u : key < 16u ? 1u : key < kPackedInf + 8u ? kMinusInf : key & ~7u;
+}
+// The key of a logit in bf16, whose lower half is all zeros (positive) or ones.
+__device__ __forceinline__ uint32_t whole_bf16(uint32_t key) {
+  return key <= 1u ? key : (key >> 31) ? key & ~0xffffu : key | 0xffffu;
+}
+__device__ __forceinline__ uint32_t place_of(bool packed, uint32_t key, uint32_t at, int j) {
+  return packed ? 7u - (key & 7u) : at >> (4 * j) & 15u;
 }
 
 template <int kN, typename Key>
@@ -310,20 +343,19 @@ __device__ __forceinline__ void group_top2(const RouterParams& p, const Key (&ke
   }
 }
 
-// Which groups stay, as a mask, from lane g's key of group g; `margin` out: the
-// lowest key taken and the highest one left (0: none).
+// Which groups stay, as a mask, from lane g's key of group g (0 in the other lanes).
 template <typename Key>
-__device__ __forceinline__ uint32_t take_groups(const RouterParams& p, Key score, int lane,
-                                                Key& last, Key& first) {
+__device__ __forceinline__ uint32_t take_groups(const RouterParams& p, Key score, int lane) {
   int before = 0;  // groups that come before this lane's
-  for (int g = 0; g < p.groups; ++g) {
-    const Key o = __shfl_sync(kAll, score, g);
-    before += o > score || (o == score && g < lane) ? 1 : 0;
+#pragma unroll 1
+  for (int g0 = 0; g0 < p.groups; g0 += 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // (lanes past the groups have 0 and come after)
+      const Key o = __shfl_sync(kAll, score, (g0 + i) & 31);
+      before += o >= score + (g0 + i < lane ? 0 : 1) ? 1 : 0;
+    }
   }
-  const bool real = lane < p.groups, taken = real && before < p.topk_groups;
-  first = warp_max(real && !taken ? score : static_cast<Key>(0));
-  last = ~warp_max(taken ? static_cast<Key>(~score) : static_cast<Key>(0));
-  return __ballot_sync(kAll, taken);
+  return __ballot_sync(kAll, lane < p.groups && before < p.topk_groups);
 }
 
 // Bit i: expert e0 + i is in one of the groups of the mask.
@@ -457,6 +489,96 @@ __device__ __noinline__ bool order_picks(const RouterParams& p, const T* row, fl
   return !__any_sync(kAll, unsure);
 }
 
+// Numbers of two parts as keys: hi is their sum rounded, so that hi and then lo give
+// their order.
+__device__ __forceinline__ uint64_t key_of(Two v) {
+  return static_cast<uint64_t>(key_of(v.hi)) << 32 | key_of(v.lo);
+}
+__device__ __forceinline__ Two two_of(uint64_t key) {
+  return {value_of(static_cast<uint32_t>(key >> 32)), value_of(static_cast<uint32_t>(key))};
+}
+__device__ __forceinline__ float minus(uint64_t x, uint64_t y) {
+  const Two a = two_of(x), b = two_of(y);
+  return (a.hi - b.hi) + (a.lo - b.lo);
+}
+
+// The whole choice again in pairs of fp32; false where they do not tell two groups, or
+// two picks that are not the same logit and bias, apart.
+template <typename T, int kN>
+__device__ __noinline__ bool choose_two(const RouterParams& p, const T* row, float m, int lane, int& id) {
+  const int e0 = lane * kN;
+  Two inv{1.f, 0.f};
+  if (!p.sigmoid) {
+    Two sum{0.f, 0.f};
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32) {
+      const float x = to_float(row[i]);
+      if (x != -kInf) sum = add(sum, exp_two(two_sum(x, -m)));
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1)
+      sum = add(sum, {__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
+    inv = inverse(sum);
+  }
+  uint64_t each[kN], key[kN];
+#pragma unroll(kN < 2 ? 1 : 2)
+  for (int i = 0; i < kN; ++i) {
+    const float x = e0 + i < p.E ? to_float(row[e0 + i]) : -kInf;
+    const float b = p.bias && e0 + i < p.E ? __ldg(p.bias + e0 + i) : 0.f;
+    const Two e = exp_two(p.sigmoid ? Two{-fabsf(x), 0.f} : two_sum(x, -m));
+    Two c = mul(p.sigmoid && x >= 0.f ? Two{1.f, 0.f} : e,
+                p.sigmoid ? inverse(add({1.f, 0.f}, e)) : inv);
+    c = add(c, {b, 0.f});
+    each[i] = x == -kInf ? 0 : key_of(c);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) key[i] = each[i];
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) finite &= key[i] == 0 || fabsf(two_of(key[i]).hi) < kInf;
+  if (!__all_sync(kAll, finite)) return false;
+  uint32_t in = kAll;
+  if (p.topk_groups < p.groups) {
+    uint64_t x, y;
+    group_top2(p, key, lane, false, x, y);
+    float size = x != 0 ? fabsf(two_of(x).hi) : 0.f;
+    if (p.group_top == 2 && y != 0) {
+      size += fabsf(two_of(y).hi);
+      x = key_of(add(two_of(x), two_of(y)));
+    }
+    const uint32_t mask = take_groups(p, x, lane);
+    const bool taken = mask >> lane & 1u;
+    const uint64_t first = warp_max(taken ? uint64_t{0} : x);
+    const uint64_t last = ~warp_max(taken ? ~x : uint64_t{0});
+    size = warp_fmax(size);
+    if (first != 0 && !(minus(last, first) > 0x1p-39f * (1.f + size))) return false;
+    in = in_groups<kN>(p, mask, e0);
+  }
+  if (p.bias) {
+    uint64_t own;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (!(in >> i & 1u)) key[i] = 0;
+    pick(key, p.k, lane, id, own);
+    const uint64_t next = __shfl_down_sync(kAll, own, 1);
+    const int next_id = __shfl_down_sync(kAll, id, 1);
+    bool close = p.k == 32;  // (no lane for the runner-up)
+    if (lane < p.k && lane < 31 && next != 0) {
+      const float b = __ldg(p.bias + id);
+      close |= !(minus(own, next) > 0x1p-40f * (1.f + fabsf(b))) &&
+               !(to_float(row[id]) == to_float(row[next_id]) && b == __ldg(p.bias + next_id));
+    }
+    return !__any_sync(kAll, close);
+  }
+  uint32_t logit[kN], own;
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    logit[i] = (in >> i & 1u) && e0 + i < p.E && to_float(row[e0 + i]) != -kInf
+                   ? key_of(to_float(row[e0 + i])) : 0u;
+  pick(logit, p.k - 1, lane, id, own);
+  return true;
+}
+
 // exp(x) for x <= 0 in fp64, to about 2^-51 of it: x = n ln 2 + r, the Taylor series
 // of exp(r) to r^13 (|r| < 0.35: the next term is below 2^-57), the exponent by its bits.
 __device__ __forceinline__ double exp64(double x) {
@@ -515,9 +637,9 @@ __device__ __noinline__ void choose_64(const RouterParams& p, const float (&l)[k
   }
   uint32_t in = kAll;
   if (p.topk_groups < p.groups) {
-    uint64_t x, y, last, first;
+    uint64_t x, y;
     group_top2(p, key, lane, false, x, y);
-    in = in_groups<kN>(p, take_groups(p, group_key(p, x, y), lane, last, first), e0);
+    in = in_groups<kN>(p, take_groups(p, group_key(p, x, y), lane), e0);
   }
   if (p.bias) {
     uint64_t own;
@@ -534,7 +656,7 @@ __device__ __noinline__ void choose_64(const RouterParams& p, const float (&l)[k
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams p) {
+__global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const RouterParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31, e0 = lane * kN;
   const long t = static_cast<long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -568,13 +690,14 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
     return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : __expf(x - m) * inv;
   };
 
-  // What fp32 leaves of c, in units of 2^-24 of the largest score.  Sigmoid: the
-  // exponential's 2 + 1.2 |l| count s (1 - s) times, half a unit at most; 1 + exp, the
-  // quotient's 2: below 4.  Softmax: the exponent's |l - m| and the fast
-  // exponential's 2 + 1.2 |l - m| of a score that falls faster than that, 3; the
-  // sum's 10 of its tree and 2 of its terms, the quotient's and the product's: below 24.
+  // By how much fp32 may be wrong about the difference of two c, in units of 2^-24 of the
+  // largest score.  Sigmoid: the exponential's 2 + 1.2 |l| steps count s (1 - s) times,
+  // a unit at most; 1 + exp one, the quotient's 2: below 4 each.  Softmax: the
+  // exponent's |l - m| and the fast exponential's 2 + 1.2 |l - m| of a score that
+  // falls faster than that, 3; the sum's 10 of its tree and 2 of its terms, the
+  // quotient's and the product's: below 24.
   // The sum with the bias adds 2^-24 of itself, counted where it is compared.
-  const float tol = (p.sigmoid ? 0x1p-20f : 0x1p-18f) * unit;
+  const float tol = (p.sigmoid ? 0x1p-21f : 0x1p-18f) * unit;
   uint32_t key[kN];
   if (by_score) {
     float b[kN];
@@ -586,24 +709,31 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
 #pragma unroll
     for (int i = 0; i < kN; ++i) key[i] = l[i] == -kInf ? 0u : broken ? 1u : key_of(l[i]);
   }
+  // Keys are packed where their last three bits do not matter: scores are looked at
+  // again where they are near, logits in bf16 have none.
   constexpr bool kSort = kN <= 8;
+  const bool packed = kSort && (sizeof(T) == 2 || by_score);
   uint32_t at = 0;
-  if constexpr (kSort) at = sort_lane(key);
+  if constexpr (kSort) at = packed ? sort_lane<true>(key) : sort_lane<false>(key);
 
+  // (a packed value is up to eight steps below, 2^-20 of it: three quarters of that of two
+  // which are near each other)
+  const float slack = packed ? 0x1.cp-21f : 0x1p-22f;
   auto near = [&](uint32_t hi, uint32_t lo) {
+    if (packed) hi = unpacked(hi), lo = unpacked(lo);
     const float x = value_of(hi), y = value_of(lo);
-    return lo > 1u && !(x - y > tol + (fabsf(x) + fabsf(y)) * 0x1p-22f);
+    return lo > 1u && !(x - y > tol + (fabsf(x) + fabsf(y)) * slack);
   };
   bool redo = false;
   if (groups) {
-    uint32_t a, b, last, first;
+    uint32_t a, b;
     if (kSort && !p.group_lanes) {  // (by the experts' own places: sorted keys have lost them)
       uint32_t own[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) own[i] = 0;
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const uint32_t place = at >> (4 * j) & 15u;
+        const uint32_t place = place_of(packed, key[j], at, j);
 #pragma unroll
         for (int i = 0; i < kN; ++i) own[i] = place == static_cast<uint32_t>(i) ? key[j] : own[i];
       }
@@ -611,17 +741,26 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
     } else {
       group_top2(p, key, lane, kSort, a, b);
     }
+    if (packed) a = unpacked(a), b = unpacked(b);
     // keys are logits without a bias: their sums are the scores'
     const bool sums = p.group_top == 2;
     if (!by_score && sums) {
+      if (packed) a = whole_bf16(a), b = whole_bf16(b);
       if (a > 1u) a = key_of(score(value_of(a)));
       if (b > 1u) b = key_of(score(value_of(b)));
     }
-    const uint32_t mask = take_groups(p, group_key(p, a, b), lane, last, first);
-    // (a group's sum has twice a score's error)
-    if (by_score || sums)
-      redo = first > 1u && !(value_of(last) - value_of(first) >
-                             2.f * tol + (fabsf(value_of(last)) + fabsf(value_of(first))) * 0x1p-21f);
+    const uint32_t total = group_key(p, a, b), mask = take_groups(p, total, lane);
+    if (by_score || sums) {
+      // The lowest that a group taken may be against the highest that one left may be: a
+      // sum has twice a score's error, and what its two parts were rounded by.
+      const float v = value_of(total), size = fabsf(value_of(a)) + (sums && b > 1u ? fabsf(value_of(b)) : 0.f);
+      const float margin = tol + size * 0x1p-22f;
+      const bool taken = mask >> lane & 1u;
+      const float least = taken && total != 0 ? (size < kInf ? margin - v : kInf) : -kInf;
+      const float most = taken || total <= 1u || v == -kInf ? -kInf : size < kInf ? v + margin + (packed ? size * 0x1.2p-20f : 0.f) : kInf;
+      const float highest = warp_fmax(most);
+      redo = __any_sync(kAll, !taken && total != 0) && !(-warp_fmax(least) > highest);
+    }
     const uint32_t in = in_groups<kN>(p, mask, e0);
     if (kSort && !p.group_lanes) {
       // (a lane may lie in several groups: its sorted list without those left out)
@@ -631,7 +770,7 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
       for (int i = 0; i < kN; ++i) kept[i] = 0;
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const uint32_t place = at >> (4 * j) & 15u;
+        const uint32_t place = place_of(packed, key[j], at, j);
         if (in >> place & 1u) {
 #pragma unroll
           for (int i = 0; i < kN; ++i)
@@ -651,8 +790,13 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
   }
   int id;
   uint32_t own;
-  if constexpr (kSort) pick_sorted(key, at, p.k, lane, id, own);
-  else pick(key, p.k, lane, id, own);
+  if constexpr (kSort) {
+    if (packed) pick_sorted<true>(key, at, p.k, lane, id, own);
+    else pick_sorted<false>(key, at, p.k, lane, id, own);
+  } else {
+    pick(key, p.k, lane, id, own);
+  }
+  bool fine = true;  // pairs of fp32 may tell
   if (by_score) {
     // lane j against pick j + 1 (k of 32 has no lane for the runner-up: always
     // looked at again)
@@ -670,21 +814,21 @@ __global__ void __launch_bounds__(256) router_forward_kernel(const RouterParams 
         int n = p.k + 1;
         bool clear = !near(__shfl_sync(kAll, own, n - 2), __shfl_sync(kAll, own, n - 1));
         while (!clear && n < 32) {
-          clear = !pick_one(key, at, n, lane, id, own);
+          clear = !pick_one<true>(key, at, n, lane, id, own);
           if (clear) break;  // no others
           ++n;
           clear = !near(__shfl_sync(kAll, own, n - 2), __shfl_sync(kAll, own, n - 1));
         }
         if (clear) {
           int ordered = id;
-          tie = !order_picks<T>(p, row, m, n, lane, ordered);
-          if (!tie) id = ordered;
+          fine = order_picks<T>(p, row, m, n, lane, ordered);
+          if (fine) id = ordered, tie = false;
         }
       }
     }
     redo |= tie;
   }
-  if (redo && !broken) {
+  if (redo && !broken && !(fine && choose_two<T, kN>(p, row, m, lane, id))) {
     float l2[kN];  // (a copy: what a call takes by reference does not stay in registers)
 #pragma unroll
     for (int i = 0; i < kN; ++i) l2[i] = l[i];
@@ -794,7 +938,7 @@ __global__ void __launch_bounds__(256) router_backward_kernel(const RouterParams
 template <typename T, int kN>
 cudaError_t launch(const RouterParams& p, bool backward, cudaStream_t s) {
   // few tokens: a warp to a block, so that they lie on as many SMs as there are
-  const int warps = p.T <= 8 * num_sms() ? 1 : 8;
+  const int warps = p.T <= 8 * num_sms() ? 1 : backward ? 8 : kForwardThreads / 32;
   const dim3 grid(static_cast<unsigned>(ceil_div(p.T, warps))), block(32 * warps);
   return backward ? launch_kernel(router_backward_kernel<T, kN>, grid, block, 0, s, 1, p)
                   : launch_kernel(router_forward_kernel<T, kN>, grid, block, 0, s, 1, p);

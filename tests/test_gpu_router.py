@@ -172,6 +172,62 @@ def test_scores_that_fp32_cannot_tell():
         check(moe.RouterProblem.make(T, E, 8, score=score, groups=16, topk_groups=4, group_top=2), near, tiny)
 
 
+@pytest.mark.parametrize("E", [64, 256, 512])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_groups_that_fp32_cannot_tell(E, dtype):
+    """Groups that are copies of others but for steps of 2^-24 or of 2^-44, with and without a bias."""
+    T, groups, half = 120, 8, E // 2
+    logits, bias = draw(T, E, dtype, seed=21)
+    g = torch.Generator().manual_seed(E)
+    logits[:, half:] = logits[:, :half]
+    if dtype == F32:
+        up = torch.nextafter(logits[:, half:], torch.full((T, half), 9.0))
+        logits[:, half:] = torch.where(torch.rand(T, half, generator=g) < 0.3, up, logits[:, half:])
+    bias[half:] = bias[:half]
+    tiny = torch.zeros(E)
+    tiny[half:] = torch.randint(0, 3, (half,), generator=g).float() * 2.0 ** -44
+    for score in ("softmax", "sigmoid"):
+        for kept, top in ((1, 2), (3, 2), (5, 1)):
+            for b in (None, bias, torch.zeros(E), tiny):
+                check(moe.RouterProblem.make(T, E, 8, dtype, score, groups=groups, topk_groups=kept,
+                                             group_top=top), logits, b)
+
+
+def test_biases_that_cancel_in_a_group():
+    """Two best experts with biases of opposite sign and far above the scores: a sum as small as a score."""
+    T, E = 300, 64
+    logits, bias = draw(T, E, seed=31)
+    bias = bias - 1000.0
+    bias[0::8], bias[1::8] = 100.0, -100.0
+    logits[:, 8:] = logits[:, :8].repeat(1, 7) + 1e-5 * torch.randn(T, 56, generator=torch.Generator().manual_seed(4))
+    for score in ("softmax", "sigmoid"):
+        for kept in (1, 4, 7):
+            check(moe.RouterProblem.make(T, E, 5, score=score, groups=8, topk_groups=kept, group_top=2),
+                  logits, bias)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("low", [NEG, torch.finfo(F32).min])
+def test_experts_taken_out_by_their_bias(low, dtype):
+    """-inf or the type's lowest value for some experts, for whole groups, for all but a few; +inf."""
+    T, E = 40, 64
+    logits, bias = draw(T, E, dtype, seed=41)
+    some = bias.clone()
+    some[torch.rand(E, generator=torch.Generator().manual_seed(6)) < 0.5] = low
+    whole = some.clone()
+    whole[8:32] = low
+    few = torch.full((E,), low)
+    few[50], few[51], few[9] = 0.0, math.inf, -0.25
+    mixed = whole.clone()
+    mixed[20], mixed[21] = NEG, torch.finfo(F32).min
+    for b in (some, whole, few, mixed):
+        for score in ("softmax", "sigmoid"):
+            for kept, top, k in ((8, 1, 6), (2, 2, 12), (6, 2, 31), (5, 1, 32)):
+                p = moe.RouterProblem.make(T, E, k, dtype, score, groups=8, topk_groups=kept, group_top=top)
+                ids, _ = reference(p, logits, b)
+                assert torch.equal(run(p, logits, b)[0], ids), (kept, top, k)
+
+
 def test_experts_out_of_the_choice():
     T, E = 40, 64
     logits, bias = draw(T, E)
