@@ -90,6 +90,7 @@ struct MmParams {
   void* out;
   int M, N, E, kblocks, nblocks, n_tiles;
   int tile_rows;    // rows of a tile at most: 256 (pairs), or of a narrow one
+  int tile_shift;   // its logarithm
   int stages;       // of the ring
   int splits;       // of K: CTAs of a cluster that share a tile (single CTAs, else 1)
   uint32_t x_stage; // bytes of a stage's rows in one CTA
@@ -236,17 +237,20 @@ struct Tile {
   __device__ __forceinline__ void at(int i, const MmParams& p, const int32_t* s_off,
                                      const int32_t* s_tile) {
     while (s_tile[e + 1] <= i) ++e;
-    const int local = i - s_tile[e], m_tiles = (s_tile[e + 1] - s_tile[e]) / p.n_tiles;
+    const int local = i - s_tile[e];
+    row = s_off[e];
+    const int m_tiles = (s_off[e + 1] - row + p.tile_rows - 1) >> p.tile_shift;
     if (m_tiles == 1) {
       m = 0;
       n = local;
-    } else {
-      const int per = kGroupM * p.n_tiles, grp = local / per, within = local - grp * per;
+    } else {  // (divisions where they are needed: each is some 150 cycles of a tile's start)
+      const int per = kGroupM * p.n_tiles;
+      const int grp = m_tiles <= kGroupM ? 0 : local / per, within = local - grp * per;
       const int size = min(kGroupM, m_tiles - grp * kGroupM);
-      n = within / size;
+      n = size == kGroupM ? within / kGroupM : within / size;
       m = grp * kGroupM + (within - n * size);
     }
-    row = s_off[e] + m * p.tile_rows;
+    row += m * p.tile_rows;
     left = min(s_off[e + 1] - row, p.tile_rows);
     narrow = !kPair || left <= kNarrow;
     half = kPair ? ((left + 1) / 2 + 15) & ~15 : (left + 15) & ~15;
@@ -259,6 +263,27 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// Four lanes' rows of four times eight words each to a row after the other of which
+// every lane has eight: words 8 s .. 8 s + 7 of lane c are then those that lane s of
+// the four had at 8 c.
+__device__ __forceinline__ void rows_across(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int b = 1; b <= 2; b *= 2) {
+    const bool high = (threadIdx.x & b) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & b) continue;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        uint32_t &x = v[8 * k + n], &y = v[8 * (k | b) + n];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x : y, b);
+        x = high ? got : x;
+        y = high ? y : got;
+      }
+    }
+  }
 }
 
 // The value, of which the compiler knows nothing: what depends on it is not worked
@@ -335,6 +360,23 @@ struct Smem {
   __device__ __forceinline__ int32_t* off() const { return reinterpret_cast<int32_t*>(factors(2)); }
   __device__ __forceinline__ int32_t* tile() const { return off() + kMaxE + 1; }
 };
+
+// Rows of 128 bytes, four lanes to each: 32 words of a row of every lane, `out` where the
+// lane's words of the first of its four rows belong, whose first `rows` are there.
+template <typename T>
+__device__ __forceinline__ void store_rows(T* out, int N, uint32_t (&w)[32], int rows, bool in) {
+  rows_across(w);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if (s < rows && in) {
+      uint32_t v[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) v[n] = w[8 * s + n];
+      store32(out, v);
+    }
+    out += N;
+  }
+}
 
 // What an epilogue warp carries from tile to tile.
 struct Turn {
@@ -452,23 +494,31 @@ struct Epilogue {
     t.at<kPair>(again, p, sm.off(), sm.tile());
     const int r0 = rank * 128 + quad * 32, col = t.n * kN + group * 128;
     const int ncols = min(128, p.N - col);
-    if (turn.go) {  // (columns in multiples of 16, on 32 bytes)
-      const long at = static_cast<long>(t.row + r0 + lane) * p.N + col;
+    if (turn.go) {
+      // Four lanes store 128 bytes of a row (a store to 32 rows takes the load and store
+      // unit four times as long as one to eight); columns come in multiples of 16,
+      // on 32 bytes.
+      const int r = r0 + (lane & ~3), part = lane & 3;
+      const long at = static_cast<long>(t.row + r) * p.N + col;
+      if (p.f32) {
 #pragma unroll
-      for (int j = 0; j < 128; j += 16) {
-        if (j >= ncols || r0 + lane >= t.left) continue;
-        uint32_t w[8];
-        if (p.f32) {
+        for (int j = 0; j < 128; j += 32) {
+          if (j >= ncols) continue;
+          uint32_t w[32];
 #pragma unroll
-          for (int h = 0; h < 16; h += 8) {
+          for (int n = 0; n < 32; ++n) w[n] = __float_as_uint(sum[j + n]);
+          store_rows(static_cast<float*>(p.out) + at + j + 8 * part, p.N, w, t.left - r,
+                     j + 8 * part < ncols);
+        }
+      } else {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) w[n] = __float_as_uint(sum[j + h + n]);
-            store32(static_cast<float*>(p.out) + at + j + h, w);
-          }
-        } else {
+        for (int j = 0; j < 128; j += 64) {
+          if (j >= ncols) continue;
+          uint32_t w[32];
 #pragma unroll
-          for (int n = 0; n < 8; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
-          store32(static_cast<uint16_t*>(p.out) + at + j, w);
+          for (int n = 0; n < 32; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
+          store_rows(static_cast<uint16_t*>(p.out) + at + j + 16 * part, p.N, w, t.left - r,
+                     j + 16 * part < ncols);
         }
       }
     }
@@ -996,6 +1046,7 @@ extern "C" int moe_fp8_matmul(const moe_fp8_problem* p, const void* x, const flo
   k.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   k.tile_rows = rows_of_tile(p, p->N % 16 == 0 && !off(out, 32));
+  k.tile_shift = k.tile_rows == 64 ? 6 : k.tile_rows == 128 ? 7 : 8;
   if ((k.tile_rows == 256 ? launch_tiles<true>(p, x, w, k, s) : launch_tiles<false>(p, x, w, k, s)) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
