@@ -313,6 +313,14 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// 64 columns of 32 lanes, when they have come.
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+               : "r"(taddr)
+               : "memory");
+}
+
 // v += four values of a CTA's shared memory of the cluster.
 __device__ __forceinline__ void add_cluster(float (&v)[4], uint32_t addr_cluster) {
   float a[4];
@@ -459,12 +467,15 @@ struct Epilogue {
 
   // A wide tile: a thread has a row and the columns of one weight block.
   static __device__ __forceinline__ Turn wide(const MmParams& p, Smem sm, uint32_t tmem_base, int rank,
-                                              int i, int e, Turn turn) {
+                                              const Tile& t, Turn turn) {
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
     const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + group * 128;
     float sum[128];
 #pragma unroll
     for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+    // where the tile lies, a lane each: a register, where the sums need nearly all of them
+    int place = lane == 0 ? t.row : lane == 1 ? t.left : t.n * kN + group * 128;
+    asm volatile("" : "+r"(place));
     Walk walk(p, sm, turn);
     for (int kb = 0; kb < sm.blocks<kSplit>(p); ++kb) {
       if (!walk.next(kb)) break;
@@ -472,34 +483,25 @@ struct Epilogue {
       const uint32_t tm = tm0 + walk.buf * 256;
 #pragma unroll
       for (int q = 0; q < 128; q += 64) {
-        uint32_t a[2][32];
-        tmem_ld_32x32b_x32(tm + q, a[0]);
-        tmem_ld_32x32b_x32(tm + q + 32, a[1]);
-        tmem_ld_wait_for(a[0]);
-        tmem_ld_wait_for(a[1]);
+        uint32_t a[64];
+        tmem_ld_64(tm + q, a);
         if (q == 64) walk.release();
 #pragma unroll
         for (int n = 0; n < 64; ++n)
-          sum[q + n] = fmaf(__uint_as_float(a[n / 32][n % 32]), f, sum[q + n]);
+          sum[q + n] = fmaf(__uint_as_float(a[n]), f, sum[q + n]);
       }
       walk.release_factors(1);
     }
     turn = walk.done();
-    // where the tile lies, found again: kept through the loop it would cost
-    // registers that the sums need
-    int again = i;
-    asm volatile("" : "+r"(again));
-    Tile t;
-    t.e = e;
-    t.at<kPair>(again, p, sm.off(), sm.tile());
-    const int r0 = rank * 128 + quad * 32, col = t.n * kN + group * 128;
+    const int row = __shfl_sync(0xffffffffu, place, 0), rows = __shfl_sync(0xffffffffu, place, 1);
+    const int r0 = rank * 128 + quad * 32, col = __shfl_sync(0xffffffffu, place, 2);
     const int ncols = min(128, p.N - col);
     if (turn.go) {
       // Four lanes store 128 bytes of a row (a store to 32 rows takes the load and store
       // unit four times as long as one to eight); columns come in multiples of 16,
       // on 32 bytes.
       const int r = r0 + (lane & ~3), part = lane & 3;
-      const long at = static_cast<long>(t.row + r) * p.N + col;
+      const long at = static_cast<long>(row + r) * p.N + col;
       if (p.f32) {
 #pragma unroll
         for (int j = 0; j < 128; j += 32) {
@@ -507,7 +509,7 @@ struct Epilogue {
           uint32_t w[32];
 #pragma unroll
           for (int n = 0; n < 32; ++n) w[n] = __float_as_uint(sum[j + n]);
-          store_rows(static_cast<float*>(p.out) + at + j + 8 * part, p.N, w, t.left - r,
+          store_rows(static_cast<float*>(p.out) + at + j + 8 * part, p.N, w, rows - r,
                      j + 8 * part < ncols);
         }
       } else {
@@ -517,7 +519,7 @@ struct Epilogue {
           uint32_t w[32];
 #pragma unroll
           for (int n = 0; n < 32; ++n) w[n] = pack_bf16(sum[j + 2 * n], sum[j + 2 * n + 1]);
-          store_rows(static_cast<uint16_t*>(p.out) + at + j + 16 * part, p.N, w, t.left - r,
+          store_rows(static_cast<uint16_t*>(p.out) + at + j + 16 * part, p.N, w, rows - r,
                      j + 16 * part < ncols);
         }
       }
@@ -597,12 +599,12 @@ struct Epilogue {
   }
 
   static __device__ __forceinline__ Turn tile(const MmParams& p, Smem sm, uint32_t tmem_base, int rank,
-                                              int i, const Tile& t, Turn turn) {
+                                              const Tile& t, Turn turn) {
     const int quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
     if (kPair && !t.narrow) {
       if (rank * 128 + quad * 32 >= t.left || t.n * kN + group * 128 >= p.N)
         return idle(p, sm, turn);
-      return wide(p, sm, tmem_base, rank, i, t.e, turn);
+      return wide(p, sm, tmem_base, rank, t, turn);
     }
     const int parts = ((t.left + 31) / 32 - group + 1) / 2;  // 32s of rows
     if (parts <= 0 || t.n * kN + rank * 128 + quad * 32 >= p.N) return idle(p, sm, turn);
@@ -815,7 +817,7 @@ fp8_matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmP
       t.e = e;
       t.at<kPair>(i, p, sm.off(), sm.tile());
       e = t.e;
-      turn = Epilogue<kPair, kSplit>::tile(p, sm, tmem_base, rank, i, t, turn);
+      turn = Epilogue<kPair, kSplit>::tile(p, sm, tmem_base, rank, t, turn);
       if (!turn.go && lane == 0) *abort_flag = 1;
     }
     __syncwarp();
