@@ -293,10 +293,24 @@ __device__ __forceinline__ long opaque(long v) {
   return v;
 }
 
-// Arrival on a barrier of the pair that hands over no memory.
-__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
+// One thread's arrival by a predicate: a branch that not all lanes take costs the
+// epilogue some 50 cycles a block (M=8192 E=8 N=28672 K=4096 762 us with branches for the
+// arrivals, 743 without).
+__device__ __forceinline__ void arrive_if(bool mine, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(static_cast<uint32_t>(mine))
+      : "memory");
+}
+// On a barrier of the pair's first CTA; hands over no memory.
+__device__ __forceinline__ void arrive_leader_if(bool mine, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+          pair::mapa(smem_u32(bar), 0)),
+      "r"(static_cast<uint32_t>(mine))
+      : "memory");
 }
 
 // Until the loads from TMEM have come; the values take part, so that their uses
@@ -319,6 +333,13 @@ __device__ __forceinline__ void tmem_ld_64(uint32_t taddr, uint32_t (&r)[64]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
                : "r"(taddr)
                : "memory");
+}
+
+// Two sums at once: half the issue slots of two FMAs.
+__device__ __forceinline__ void fma2(uint64_t& s, uint32_t a0, uint32_t a1, uint64_t f) {
+  uint64_t a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "r"(a0), "r"(a1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(a), "l"(f));
 }
 
 // v += four values of a CTA's shared memory of the cluster.
@@ -407,46 +428,40 @@ struct Epilogue {
     // Of this lane's waits: it skips them once one has run out, and the warp
     // leaves together before the next factors.
     bool ok = true;
-    int left = 0;  // blocks whose factors are there
     const float* factors = nullptr;
     __device__ __forceinline__ Walk(const MmParams& p_, Smem s, Turn t) : Turn(t), p(p_), sm(s) {}
-    // The next block's sums are in accumulator `buf`, their factors at `factors`.
-    __device__ __forceinline__ bool next(int kb) {
-      if (left == 0) {
-        ok = ok && mbar_wait(sm.ffull(chunk & 1), (chunk >> 1) & 1, p.status);
-        go = __all_sync(0xffffffffu, ok);
-        if (!go) return false;
-        factors = sm.factors(chunk & 1);
-        left = min(kChunk, sm.blocks<kSplit>(p) - kb);
-      }
-      ok = ok && mbar_wait(sm.tfull(buf), par, p.status);
-      __syncwarp();
+    __device__ __forceinline__ bool first_lane() const { return (threadIdx.x & 31) == 0; }
+    // The next blocks' factors are at `factors`.
+    __device__ __forceinline__ bool next_factors() {
+      ok = ok && mbar_wait(sm.ffull(chunk & 1), (chunk >> 1) & 1, p.status);
+      go = __all_sync(0xffffffffu, ok);
+      factors = sm.factors(chunk & 1);
+      return go;
+    }
+    // The next block's sums are in accumulator `buf`.
+    __device__ __forceinline__ void next() {
+      // (one answer for the warp: no branch that lanes could take apart)
+      if (!__all_sync(0xffffffffu, mbar_try_wait(sm.tfull(buf), par)))
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(sm.tfull(buf), par, p.status));
       tc_fence_after();
       if (!kPair) {  // the tensor core is through with the stage's operands
-        if (threadIdx.x == 128) mbar_arrive(sm.empty(stage));
+        arrive_if(threadIdx.x == 128, sm.empty(stage));
         if (++stage == p.stages) stage = 0;
       }
-      return true;
     }
     // The accumulator has been read (nothing else is handed over).
     __device__ __forceinline__ void release() {
       tc_fence_before();
-      if ((threadIdx.x & 31) == 0) {
-        if (kPair) arrive_remote_relaxed(pair::mapa(smem_u32(sm.tempty(buf)), 0));
-        else mbar_arrive(sm.tempty(buf));
-      }
+      if (kPair) arrive_leader_if(first_lane(), sm.tempty(buf));
+      else arrive_if(first_lane(), sm.tempty(buf));
       par ^= buf;
       buf ^= 1;
     }
-    // So have the factors, once a chunk is through.
-    __device__ __forceinline__ void release_factors(int blocks) {
-      factors += 256 * blocks;
-      left -= blocks;
-      if (left == 0) {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(sm.fempty(chunk & 1));
-        ++chunk;
-      }
+    // So have the factors.
+    __device__ __forceinline__ void release_factors() {
+      __syncwarp();
+      arrive_if(first_lane(), sm.fempty(chunk & 1));
+      ++chunk;
     }
     __device__ __forceinline__ Turn done() {
       go = __all_sync(0xffffffffu, ok);
@@ -457,10 +472,13 @@ struct Epilogue {
   // A tile that this warp has no part of.
   static __device__ __forceinline__ Turn idle(const MmParams& p, Smem sm, Turn turn) {
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kHand) {
-      if (!walk.next(kb)) break;
-      walk.release();
-      walk.release_factors(min(kHand, sm.blocks<kSplit>(p) - kb));
+    for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kChunk) {
+      if (!walk.next_factors()) break;
+      for (int j = 0; j < min(kChunk, sm.blocks<kSplit>(p) - kb); j += kHand) {
+        walk.next();
+        walk.release();
+      }
+      walk.release_factors();
     }
     return walk.done();
   }
@@ -470,29 +488,42 @@ struct Epilogue {
                                               const Tile& t, Turn turn) {
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, group = (threadIdx.x >> 7) - 1;
     const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + group * 128;
-    float sum[128];
+    uint64_t sum2[64];
 #pragma unroll
-    for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+    for (int j = 0; j < 64; ++j) sum2[j] = 0;
     // where the tile lies, a lane each: a register, where the sums need nearly all of them
     int place = lane == 0 ? t.row : lane == 1 ? t.left : t.n * kN + group * 128;
     asm volatile("" : "+r"(place));
     Walk walk(p, sm, turn);
-    for (int kb = 0; kb < sm.blocks<kSplit>(p); ++kb) {
-      if (!walk.next(kb)) break;
-      const float f = walk.factors[group * 128 + quad * 32 + lane];
-      const uint32_t tm = tm0 + walk.buf * 256;
+    for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kChunk) {
+      if (!walk.next_factors()) break;
+      const float* factor = walk.factors + group * 128 + quad * 32 + lane;
+      const float* const end = factor + 256 * min(kChunk, sm.blocks<kSplit>(p) - kb);
+#pragma unroll 1
+      for (; factor != end; factor += 256) {
+        walk.next();
+        const float f = *factor;
+        const uint32_t tm = tm0 + walk.buf * 256;
+        uint64_t ff;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ff) : "r"(__float_as_uint(f)));
 #pragma unroll
-      for (int q = 0; q < 128; q += 64) {
-        uint32_t a[64];
-        tmem_ld_64(tm + q, a);
-        if (q == 64) walk.release();
+        for (int q = 0; q < 128; q += 64) {
+          uint32_t a[64];
+          tmem_ld_64(tm + q, a);
+          if (q == 64) walk.release();
 #pragma unroll
-        for (int n = 0; n < 64; ++n)
-          sum[q + n] = fmaf(__uint_as_float(a[n]), f, sum[q + n]);
+          for (int n = 0; n < 64; n += 2) fma2(sum2[(q + n) / 2], a[n], a[n + 1], ff);
+        }
       }
-      walk.release_factors(1);
+      walk.release_factors();
     }
     turn = walk.done();
+    float sum[128];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      sum[2 * j] = __uint_as_float(static_cast<uint32_t>(sum2[j]));
+      sum[2 * j + 1] = __uint_as_float(static_cast<uint32_t>(sum2[j] >> 32));
+    }
     const int row = __shfl_sync(0xffffffffu, place, 0), rows = __shfl_sync(0xffffffffu, place, 1);
     const int r0 = rank * 128 + quad * 32, col = __shfl_sync(0xffffffffu, place, 2);
     const int ncols = min(128, p.N - col);
@@ -537,8 +568,13 @@ struct Epilogue {
 #pragma unroll
     for (int j = 0; j < 32 * kParts; ++j) sum[j] = 0.f;
     Walk walk(p, sm, turn);
+    int left = 0;  // blocks whose factors are there
     for (int kb = 0; kb < sm.blocks<kSplit>(p); kb += kHand) {
-      if (!walk.next(kb)) break;
+      if (left == 0) {
+        if (!walk.next_factors()) break;
+        left = min(kChunk, sm.blocks<kSplit>(p) - kb);
+      }
+      walk.next();
       const uint32_t tm = tm0 + walk.buf * 256;
       const int blocks = min(kHand, sm.blocks<kSplit>(p) - kb);
       uint32_t a[kHand][kParts][32];
@@ -572,7 +608,9 @@ struct Epilogue {
           }
         }
       }
-      walk.release_factors(blocks);
+      walk.factors += 256 * blocks;
+      left -= blocks;
+      if (left == 0) walk.release_factors();
     }
     turn = walk.done();
     if (kSplit) {  // for the join, in the ring (this tile is the CTA's last)
