@@ -30,16 +30,20 @@
 // row one 256-byte segment; otherwise two copies of 128-byte rows do, which
 // zero-fill past the row's end.
 //
-// What bounds it.  Wide: the epilogue.  A block takes the tensor core 512 cycles and
-// the two epilogue warps of a scheduler about 500 instructions, half of them FMA,
-// behind one another 950 cycles; copies and MMAs alone reach the tensor core's rate
-// (3560 TFLOP/s).  M=8192 E=8 N=28672 K=4096: 0.87 ms, 2210 TFLOP/s.  Measured and
-// not kept: packed FMA (the pairs cost moves: 3% slower), 16 epilogue warps, loads of
-// the next columns under the FMAs (5-10% slower), four accumulators of 128 columns
-// (the MMA is slower at N = 128), tiles of 192 columns (15% slower), wide and narrow
-// tiles interleaved.  Narrow: HBM where there are many tiles (M=2048 E=256 N=4096 K=7168
-// 1.10 ms, 6.9 TB/s); with one tile a CTA its latency, 0.17 us a block and some 6 us of
-// launch, tiles and first copies (M=8 of 128 experts, N=1536 K=2048: 11 us).
+// What bounds it.  Wide: the epilogue.  A block takes the tensor core 512 cycles, its
+// commits some 100, and the epilogue 770: reading TMEM and FMAs, 250 cycles each and
+// behind one another (the two warps of a scheduler go in step), and 270 for the
+// hand-over.  A tile's end, whose sums go out while nothing else is done, takes 5000
+// of its 31000.  M=8192 E=8 N=28672 K=4096: 0.75 ms, 2580 TFLOP/s; without the FMAs, before
+// they were packed, 0.72 for 0.87, and the copies and hand-overs alone take 0.57.
+// Measured and not kept, us at that size: 16 epilogue warps (870 to 1000), loads of the
+// next columns under the FMAs (745 to 1100: registers move), four accumulators of 128
+// columns (the MMA is slower at N = 128; 985 to 1150), tiles of 192 columns (877 to 1007),
+// one commit for epilogue and producer (745 to 755), looking at the next accumulator's
+// barrier ahead of the FMAs (745 to 782), one lane's wait for the warp (816 to 876).
+// Narrow: HBM where there are many tiles (M=2048 E=256 N=4096 K=7168 886 us, 6.9 TB/s);
+// with one tile a CTA its latency, 0.17 us a block and some 6 us of launch, tiles and
+// first copies (M=8 of 128 experts, N=1536 K=2048: 11 us).
 //
 // Every wait is bounded (ptx.cuh).
 #include <cuda.h>
@@ -984,10 +988,11 @@ int check_matmul(const moe_fp8_problem* p) {
 // A block takes a CTA about 0.2 us (its weights' 16 KB at the rate of HBM, and less
 // from L2) and 1.9 ns a row of the tile, a pair 0.5 us for a wide tile; the fewest
 // waves of those are the shortest, and of 64 and 128 rows in as many tiles 64 leave
-// room for a stage more.  With 64, 128 and 256 rows, us: M=2048 E=256 N=4096 K=7168
-// 1104, 1146, 1184; M=16384 1600, 1225, 1251; M=32768 2215, 2087, 1551; M=300 E=1
-// N=2048 K=2048 10.8, 12.7, 18.3; M=600 16.5, 13.5, 18.4; M=256 E=1 N=8192 K=8192
-// 43.9, 33.6, 40.7; M=384 63, 60, 43; M=8192 E=8 N=28672 K=4096 1923, 1352, 864.
+// room for a stage more.  With 64, 128 and 256 rows, us: N=4096 K=7168 of 256 experts by
+// popularity, M=2048 886, 925, 918; M=16384 1468, 1413, 1299 (all experts alike 1268, 1213,
+// 1248: the rows of each are not known here); M=32768 2026, 1817, 1533.  M=4096 E=8 N=4096
+// K=4096 128, 107, 75; M=300 E=1 N=2048 K=2048 9.3, 11.8, 13.7; M=600 13.8, 12.4, 13.9; M=256
+// E=1 N=8192 K=8192 36.1, 30.9, 31.8; M=384 51, 55, 35.
 int rows_of_tile(const moe_fp8_problem* p, bool wide) {
   const long groups = std::min(p->E, p->M), mean = ceil_div(p->M, groups);
   int best = 0;
