@@ -12,14 +12,14 @@
 // most `tol` / 2 (below); only where two neighbours in the order of the picks (or
 // the last group taken and the first one left) are nearer than that, and are not
 // the same logit and bias, it is looked at again.  Picks: their scores to 41 bits in
-// pairs of fp32, a lane each, put them in order.  Groups, and what those do not tell:
-// the whole token in fp64.  With 256 sigmoid scores and a random bias nine tokens of
-// 8192 are looked at; that code is cold, and its fetches are most of its time (one
-// token in fp64: 9 us of a launch).
+// pairs of fp32, a lane each, put them in order.  Groups: the whole token in such pairs.
+// What those do not tell: the token in fp64.  With 256 sigmoid scores and a random bias
+// nine tokens of 8192 are looked at.
 //
-// Bound by instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate); k = 8 with a
-// bias and 8 groups takes 15.5 us (loads and keys 2, the sort 2, groups 2.5, picks 2, looking
-// again 3.5, weights 1.5), with neither 10.4; the backward 6.6, most of it the call.
+// Bound by latency and instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate);
+// k = 8 with a bias and 8 groups takes 14.4 us (a token 8000 cycles, in 1.7 waves; near
+// picks 4500 cycles more, near groups 9000, fp64 30000), without a bias and groups 10.0;
+// T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 30 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
