@@ -18,7 +18,7 @@
 //
 // Bound by latency and instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate);
 // k = 8 with a bias and 8 groups takes 14.4 us (a token 8000 cycles, in 1.7 waves; near
-// picks 4500 cycles more, near groups 9000, fp64 30000), without a bias and groups 10.0;
+// picks 4500 cycles more, near groups 20000, fp64 30000), without a bias and groups 10.0;
 // T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 30 us).
 #include <cuda_runtime.h>
 
