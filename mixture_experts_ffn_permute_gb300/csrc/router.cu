@@ -4,8 +4,8 @@
 // One warp per token, the row in registers: lane i holds the experts i N ..
 // i N + N - 1 (N the power of two that fits E), so that among equal keys the lowest
 // lane, and in it the first, is the lowest id.  A key is the value's bits in an
-// order of unsigned integers.  Up to N = 8 a lane sorts its keys once; a pick is then
-// one warp maximum, one ballot and a shift of the winner's list.
+// order of unsigned integers.  Up to N = 8, and with a bias N = 16, a lane sorts its keys
+// once; a pick is then one warp maximum, one ballot and a shift of the winner's list.
 //
 // The order is that of c in 64 bits.  Without a bias c grows with the logit, and
 // logits compare exactly.  With one, c is computed in fp32 with an error of at
@@ -19,7 +19,7 @@
 // Bound by latency and instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate);
 // k = 8 with a bias and 8 groups takes 14.4 us (a token 8000 cycles, in 1.7 waves; near
 // picks 4500 cycles more, near groups 20000, fp64 30000), without a bias and groups 10.0;
-// T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 30 us).
+// T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 25 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -193,18 +193,21 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
 }
 
 // The same from lists that every lane has sorted, highest first and the first among
-// equal ones.  Packed keys have their places in the lane in their last three bits (7:
-// the first), which do not count; else `at` holds the places, four bits each.  Pick `j`
-// alone; false where nothing is left.
+// equal ones.  Packed keys have their places in the lane in their last three or four
+// bits (all ones: the first), which do not count; else `at` holds the places, four bits
+// each.  Pick `j` alone; false where nothing is left.
+template <int kN>
+constexpr uint32_t kPlace = kN <= 8 ? 7u : 15u;
 template <bool kPacked, int kN>
 __device__ __forceinline__ bool pick_one(uint32_t (&key)[kN], uint32_t& at, int j, int lane, int& id,
                                          uint32_t& own) {
   uint32_t best = warp_max(key[0]);
   if (best == 0) return false;
-  if (kPacked) best &= ~7u;
+  if (kPacked) best &= ~kPlace<kN>;
   const int from = __ffs(__ballot_sync(kAll, key[0] >= best)) - 1;
-  const int place = kPacked ? 7 - static_cast<int>(__shfl_sync(kAll, key[0], from) & 7u)
-                            : static_cast<int>(__shfl_sync(kAll, at, from) & 15u);
+  const uint32_t theirs =
+      __shfl_sync(kAll, kPacked ? key[0] : at, from) & (kPacked ? kPlace<kN> : 15u);
+  const int place = static_cast<int>(kPacked ? kPlace<kN> - theirs : theirs);
   if (lane == from) {
 #pragma unroll
     for (int i = 0; i + 1 < kN; ++i) key[i] = key[i + 1];
@@ -226,7 +229,7 @@ __device__ __forceinline__ void pick_sorted(uint32_t (&key)[kN], uint32_t& at, i
     if (!pick_one<kPacked>(key, at, j, lane, id, own)) break;
 }
 
-// Sorts by an odd-even merge network (Batcher): kN = 1, 2, 4 or 8.
+// Sorts by an odd-even merge network (Batcher): kN = 1, 2, 4, 8 or 16 (packed).
 template <int kN, typename Key>
 __device__ __forceinline__ void sort_network(Key (&v)[kN]) {
   if constexpr (kN > 1) {
@@ -251,16 +254,18 @@ __device__ __forceinline__ void sort_network(Key (&v)[kN]) {
   }
 }
 
-// Packed: two instructions an exchange, where 64 bits take six.  (Below 8 is none, from 8
-// a NaN, from kPackedInf -inf.)
+// Packed: two instructions an exchange, where 64 bits take six.  (Below kPlace + 1 is
+// none, then a NaN, from kPackedInf -inf.)
 constexpr uint32_t kPackedInf = 0x00800000u;
 template <bool kPacked, int kN>
 __device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[kN]) {
+  constexpr uint32_t kOnes = kPlace<kN>;
   uint32_t at = 0;
   if constexpr (kPacked) {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      key[i] = key[i] == 0 ? 0u : (max(key[i], key[i] == kMinusInf ? kPackedInf : 8u) & ~7u) | (7u - i);
+      key[i] = key[i] == 0 ? 0u
+                           : (max(key[i], key[i] == kMinusInf ? kPackedInf : kOnes + 1) & ~kOnes) | (kOnes - i);
     sort_network(key);
   } else {
     uint64_t v[kN];
@@ -275,16 +280,19 @@ __device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[kN]) {
   }
   return at;
 }
-// The key without its place: the value is at most eight steps above the key's.
+// The key without its place: the value is at most kPlace steps above the key's.
+template <int kN>
 __device__ __forceinline__ uint32_t unpacked(uint32_t key) {
-  return key < 8u ? 0u : key < 16u ? 1u : key < kPackedInf + 8u ? kMinusInf : key & ~7u;
+  constexpr uint32_t kOnes = kPlace<kN>;
+  return key <= kOnes ? 0u : key <= 2 * kOnes + 1 ? 1u : key <= kPackedInf + kOnes ? kMinusInf : key & ~kOnes;
 }
 // The key of a logit in bf16, whose lower half is all zeros (positive) or ones.
 __device__ __forceinline__ uint32_t whole_bf16(uint32_t key) {
   return key <= 1u ? key : (key >> 31) ? key & ~0xffffu : key | 0xffffu;
 }
+template <int kN>
 __device__ __forceinline__ uint32_t place_of(bool packed, uint32_t key, uint32_t at, int j) {
-  return packed ? 7u - (key & 7u) : at >> (4 * j) & 15u;
+  return packed ? kPlace<kN> - (key & kPlace<kN>) : at >> (4 * j) & 15u;
 }
 
 template <int kN, typename Key>
@@ -655,7 +663,8 @@ __device__ __noinline__ void choose_64(const RouterParams& p, const float (&l)[k
   }
 }
 
-template <typename T, int kN>
+// kSort: sorted lists (of 16: with a bias, and groups of whole lanes or none).
+template <typename T, int kN, bool kSort>
 __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const RouterParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31, e0 = lane * kN;
@@ -709,31 +718,34 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
 #pragma unroll
     for (int i = 0; i < kN; ++i) key[i] = l[i] == -kInf ? 0u : broken ? 1u : key_of(l[i]);
   }
-  // Keys are packed where their last three bits do not matter: scores are looked at
-  // again where they are near, logits in bf16 have none.
-  constexpr bool kSort = kN <= 8;
-  const bool packed = kSort && (sizeof(T) == 2 || by_score);
+  // Keys are packed where their last bits do not matter: scores are looked at again where
+  // they are near, logits in bf16 have none.
+  const bool packed = kSort && (kN > 8 || sizeof(T) == 2 || by_score);
   uint32_t at = 0;
-  if constexpr (kSort) at = packed ? sort_lane<true>(key) : sort_lane<false>(key);
+  if constexpr (kSort) {
+    if (packed) at = sort_lane<true>(key);
+    else if constexpr (kN <= 8) at = sort_lane<false>(key);
+  }
 
-  // (a packed value is up to eight steps below, 2^-20 of it: three quarters of that of two
-  // which are near each other)
-  const float slack = packed ? 0x1.cp-21f : 0x1p-22f;
+  // (a packed value is up to 8 or 16 steps below, 2^-20 or 2^-19 of it: three quarters of
+  // that of two which are near each other)
+  constexpr float kBelow = kN <= 8 ? 0x1.2p-20f : 0x1.2p-19f;
+  const float slack = packed ? (kN <= 8 ? 0x1.cp-21f : 0x1.cp-20f) : 0x1p-22f;
   auto near = [&](uint32_t hi, uint32_t lo) {
-    if (packed) hi = unpacked(hi), lo = unpacked(lo);
+    if (packed) hi = unpacked<kN>(hi), lo = unpacked<kN>(lo);
     const float x = value_of(hi), y = value_of(lo);
     return lo > 1u && !(x - y > tol + (fabsf(x) + fabsf(y)) * slack);
   };
   bool redo = false;
   if (groups) {
     uint32_t a, b;
-    if (kSort && !p.group_lanes) {  // (by the experts' own places: sorted keys have lost them)
+    if (kSort && kN <= 8 && !p.group_lanes) {  // (by the experts' own places: sorted keys have lost them)
       uint32_t own[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) own[i] = 0;
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const uint32_t place = place_of(packed, key[j], at, j);
+        const uint32_t place = place_of<kN>(packed, key[j], at, j);
 #pragma unroll
         for (int i = 0; i < kN; ++i) own[i] = place == static_cast<uint32_t>(i) ? key[j] : own[i];
       }
@@ -741,7 +753,7 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
     } else {
       group_top2(p, key, lane, kSort, a, b);
     }
-    if (packed) a = unpacked(a), b = unpacked(b);
+    if (packed) a = unpacked<kN>(a), b = unpacked<kN>(b);
     // keys are logits without a bias: their sums are the scores'
     const bool sums = p.group_top == 2;
     if (!by_score && sums) {
@@ -757,12 +769,12 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
       const float margin = tol + size * 0x1p-22f;
       const bool taken = mask >> lane & 1u;
       const float least = taken && total != 0 ? (size < kInf ? margin - v : kInf) : -kInf;
-      const float most = taken || total <= 1u || v == -kInf ? -kInf : size < kInf ? v + margin + (packed ? size * 0x1.2p-20f : 0.f) : kInf;
+      const float most = taken || total <= 1u || v == -kInf ? -kInf : size < kInf ? v + margin + (packed ? size * kBelow : 0.f) : kInf;
       const float highest = warp_fmax(most);
       redo = __any_sync(kAll, !taken && total != 0) && !(-warp_fmax(least) > highest);
     }
     const uint32_t in = in_groups<kN>(p, mask, e0);
-    if (kSort && !p.group_lanes) {
+    if (kSort && kN <= 8 && !p.group_lanes) {
       // (a lane may lie in several groups: its sorted list without those left out)
       uint32_t kept[kN], places = 0;
       int n = 0;
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
       for (int i = 0; i < kN; ++i) kept[i] = 0;
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const uint32_t place = place_of(packed, key[j], at, j);
+        const uint32_t place = place_of<kN>(packed, key[j], at, j);
         if (in >> place & 1u) {
 #pragma unroll
           for (int i = 0; i < kN; ++i)
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
   uint32_t own;
   if constexpr (kSort) {
     if (packed) pick_sorted<true>(key, at, p.k, lane, id, own);
-    else pick_sorted<false>(key, at, p.k, lane, id, own);
+    else if constexpr (kN <= 8) pick_sorted<false>(key, at, p.k, lane, id, own);
   } else {
     pick(key, p.k, lane, id, own);
   }
@@ -940,8 +952,15 @@ cudaError_t launch(const RouterParams& p, bool backward, cudaStream_t s) {
   // few tokens: a warp to a block, so that they lie on as many SMs as there are
   const int warps = p.T <= 8 * num_sms() ? 1 : backward ? 8 : kForwardThreads / 32;
   const dim3 grid(static_cast<unsigned>(ceil_div(p.T, warps))), block(32 * warps);
-  return backward ? launch_kernel(router_backward_kernel<T, kN>, grid, block, 0, s, 1, p)
-                  : launch_kernel(router_forward_kernel<T, kN>, grid, block, 0, s, 1, p);
+  if (backward) return launch_kernel(router_backward_kernel<T, kN>, grid, block, 0, s, 1, p);
+  if constexpr (kN == 16) {
+    // Lists of 16 are sorted where packed keys and whole lanes to a group make that enough
+    // (us, sorted and not, T=8192 with a bias: E=512 in 8 groups 28.2, 35.2; E=320 without groups
+    // 24.8, 32.1; in 64 bits, E=320 without a bias, 33 and 17).
+    if (p.bias && (p.topk_groups >= p.groups || p.group_lanes))
+      return launch_kernel(router_forward_kernel<T, kN, true>, grid, block, 0, s, 1, p);
+  }
+  return launch_kernel(router_forward_kernel<T, kN, kN <= 8>, grid, block, 0, s, 1, p);
 }
 
 template <typename T>

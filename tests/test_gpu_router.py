@@ -193,6 +193,35 @@ def test_groups_that_fp32_cannot_tell(E, dtype):
                                              group_top=top), logits, b)
 
 
+@pytest.mark.parametrize("E", [200, 320, 512, 1000])
+def test_neighbouring_scores_of_many_experts(E):
+    """Logits a float or two apart, with biases that differ by less than fp32 shows, over all lanes."""
+    T = 48
+    g = torch.Generator().manual_seed(E)
+    logits = torch.linspace(-2, 2, T)[:, None].expand(T, E).contiguous()
+    steps = torch.randint(0, 4, (T, E), generator=g)
+    for _ in range(4):
+        logits = torch.where(steps > 0, torch.nextafter(logits, torch.full_like(logits, 9.0)), logits)
+        steps -= 1
+    far = torch.rand(T, E, generator=g) < 0.97
+    logits = torch.where(far, logits - 3.0, logits)
+    tiny = torch.randint(0, 3, (E,), generator=g).float() * 2.0 ** -41
+    for score in ("softmax", "sigmoid"):
+        for b in (tiny, torch.zeros(E), 0.5 + tiny):
+            check(moe.RouterProblem.make(T, E, 8, score=score), logits, b)
+            p = moe.RouterProblem.make(T, E, 8, score=score, groups=4, topk_groups=2, group_top=2)
+            # Two pairs of neighbouring logits with the same sum have scores whose sums differ by
+            # the curvature, some 2^-52: 64 bits do not tell such groups.  A score takes four
+            # roundings of 2^-53 at most, its bias one, the sum of two one of 2^-52 (it is below
+            # 4): 2^-49 for a group, 2^-48 for the difference of two.
+            ids, s = reference(p, logits, b)
+            sums = (s + b.double()).view(T, 4, E // 4).topk(2).values.sum(2).sort(1, descending=True).values
+            told = (sums[:, 1] - sums[:, 2]) > 2.0 ** -48
+            idx, _ = run(p, logits, b)
+            assert torch.equal(idx[told], ids[told])
+            assert told.sum() >= 16  # (22 of 48 at the fewest: E=1000 without a bias)
+
+
 def test_biases_that_cancel_in_a_group():
     """Two best experts with biases of opposite sign and far above the scores: a sum as small as a score."""
     T, E = 300, 64
