@@ -739,7 +739,9 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
   bool redo = false;
   if (groups) {
     uint32_t a, b;
-    if (kSort && kN <= 8 && !p.group_lanes) {  // (by the experts' own places: sorted keys have lost them)
+    if (kSort && kN <= 8 && !p.group_lanes) {
+      // (by the experts' own places, which sorted keys have lost; a packed key of nothing has
+      // no place either, and adds nothing to any)
       uint32_t own[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) own[i] = 0;
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
       for (int j = 0; j < kN; ++j) {
         const uint32_t place = place_of<kN>(packed, key[j], at, j);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) own[i] = place == static_cast<uint32_t>(i) ? key[j] : own[i];
+        for (int i = 0; i < kN; ++i) own[i] |= place == static_cast<uint32_t>(i) ? key[j] : 0u;
       }
       group_top2(p, own, lane, false, a, b);
     } else {

@@ -476,3 +476,24 @@ def test_graph_replay_and_streams():
     moe.router_backward(p, buf, idx, dw, dl, stream=s)
     s.synchronize()
     assert torch.equal(w, first[0]) and torch.equal(dl, first[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E,groups", [(192, 8), (200, 4), (240, 6), (129, 3), (250, 10), (160, 4), (60, 4),
+                                      (400, 8), (256, 8)])
+def test_experts_out_of_the_choice_in_groups(E, groups, dtype):
+    """Logits of -inf beside the best experts of groups, above all at the places 8 i + 7: they take
+    nothing from their group's score."""
+    T = 40
+    logits, bias = draw(T, E, dtype, seed=61)
+    g = torch.Generator().manual_seed(E)
+    logits[torch.rand(T, E, generator=g) < 0.25] = NEG
+    for t in range(T):
+        for best in range(8 * (t % 5) + 7, E, 40):
+            logits[t, best] = 3.0 + 0.125 * int(torch.randint(0, 16, (1,), generator=g))
+            logits[t, best - 1 - t % 7] = NEG
+    for score in ("softmax", "sigmoid"):
+        for b in (None, bias):
+            for kept, top in ((1, 1), (groups // 2, 2), (groups - 1, 1)):
+                check(moe.RouterProblem.make(T, E, 8, dtype, score, groups=groups, topk_groups=kept,
+                                             group_top=top), logits, b)
