@@ -82,9 +82,10 @@ MOE_API int moe_router_backward(const moe_router_problem* p, const void* logits,
 
 /* ---- Quantisation ----------------------------------------------------------
  * For every block: scale = max |v| / 448 (1 where every v is 0, and 2^-126 at
- * least), code = E4M3(v / scale), rounded to nearest, ties to even.  A block with
- * a NaN, or an infinity, has that as its scale; its codes are what v / scale has
- * then (NaN, and 0 for the finite values next to an infinity). */
+ * least), code = E4M3(v / scale), rounded to nearest, ties to even; both quotients
+ * are those of fp32.  A block with a NaN, or an infinity, has that as its scale;
+ * its codes are what v / scale has then (NaN, and 0 for the finite values next to
+ * an infinity). */
 
 /* Rows: a block is 128 consecutive values of a row (the last one may be
  * shorter).  With swiglu a row of src holds 2H pre-activations and

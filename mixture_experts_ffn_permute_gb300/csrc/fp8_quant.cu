@@ -2,8 +2,9 @@
 // include/moe_experts.h).
 //
 // HBM bound: every value is read once and its code written once.  T=8192 H=7168 bf16
-// 28.9 us (6.2 TB/s, 0.90 of the copy rate), SwiGLU T=8192 H=14336 92.4 us (0.94), weights
-// E=8 N=4096 K=14336 with transposed codes 267 us (1.03).
+// 29.4 us (6.05 TB/s, 0.89 of the copy rate), SwiGLU T=8192 H=14336 95.2 us (0.91), weights
+// E=8 N=4096 K=14336 with transposed codes 272 us (1.01).  Codes of products with the rounded
+// reciprocal in place of quotients took 28.9, 92.4 and 267.
 //
 // Rows.  A thread takes 16 consecutive values (one or two 32-byte loads, one
 // 16-byte store), eight threads a block, whose maximum goes through three shuffles;
@@ -32,6 +33,7 @@ constexpr int kBlock = 128;
 constexpr int kPer = 16;                   // values of a thread
 constexpr int kThreadsPer = kBlock / kPer; // of a block
 constexpr float kE4m3Max = 448.f;
+constexpr float kDown = 0x1p-80f;
 
 // max(|a|, |b|), NaN where one is
 __device__ __forceinline__ float amax(float a, float b) {
@@ -91,18 +93,46 @@ struct Values<float, kWide> {
 
 // x / (1 + exp(-x)) by the exponential of -|x|, which is at most 1.  The fast
 // forms are off by about |x| 2^-24, far below a code's 2^-4, and without them the
-// arithmetic takes longer than the bytes.
+// arithmetic takes longer than the bytes.  (The divisor is 1 to 2: its reciprocal needs no
+// care for sizes.)
 __device__ __forceinline__ float silu(float x) {
   const float e = __expf(-fabsf(x));
-  return __fdividef(x < 0.f ? x * e : x, 1.f + e);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (x < 0.f ? x * e : x) * r;
 }
 
-__device__ __forceinline__ uint4 codes_of(const float (&v)[kPer], float inv) {
+// The reciprocal of a scale in two parts, 1 / s = y + y2.
+struct Inverse {
+  float y, y2;
+  bool big;  // y2 would be subnormal: those of kDown s, for kDown v
+};
+__device__ __forceinline__ Inverse inverse_of(float scale) {
+  Inverse r;
+  r.big = !(scale < 0x1p100f);  // (or the scale is NaN)
+  const float s = r.big ? scale * kDown : scale;
+  r.y = 1.f / s;
+  const float e = __fmaf_rn(-s, r.y, 1.f), d = e * r.y;
+  r.y2 = s < INFINITY ? __fmaf_rn(__fmaf_rn(-d, s, e), r.y, d) : 0.f;  // e / s (Markstein 1990)
+  return r;
+}
+
+// The codes of v / s in fp32.  A product with the rounded reciprocal is two roundings, and a
+// quotient that lies on the border of two codes (of bf16 values one in some 2000) would fall to
+// either side; v y + v y2 has one that counts.  Every value and scale whose result could lie on
+// another side of a border than their quotient in fp32 were gone through: none does.  (v y2 is
+// rounded down, as a sum with -0, so that a zero keeps its sign.)
+__device__ __forceinline__ uint4 codes_of(float (&v)[kPer], const Inverse& r) {
+  if (r.big) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] *= kDown;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = __fmaf_rn(v[i], r.y, __fmaf_rd(v[i], r.y2, -0.f));
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = f32x2_to_e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) |
-           f32x2_to_e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    c[i] = f32x2_to_e4m3x2(v[4 * i], v[4 * i + 1]) | f32x2_to_e4m3x2(v[4 * i + 2], v[4 * i + 3]) << 16;
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
@@ -163,7 +193,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
     for (int o = 1; o < kThreadsPer; o *= 2) m = amax(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float scale = scale_of(m);
     if (in) {
-      p.codes[(t * p.H + c) / kPer] = codes_of(v, 1.f / scale);
+      p.codes[(t * p.H + c) / kPer] = codes_of(v, inverse_of(scale));
       if (sub == 0) p.scales[q] = scale;
     }
   }
@@ -189,8 +219,9 @@ __device__ __forceinline__ void transpose4(const uint32_t (&w)[4], uint32_t (&ou
 
 // One CTA per 128 x 128 block: thread i has the rows 4 (i / 8) .. + 3, the columns
 // 16 (i % 8) .. + 15.
+// (bf16: 80 registers, three CTAs to an SM; a form of 127 registers took 329 us for the 272 above)
 template <typename T, bool kWide, bool kTransposed>
-__global__ void __launch_bounds__(256) quantize_weights_kernel(const WeightParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) quantize_weights_kernel(const WeightParams p) {
   __shared__ float s_max[8];
   // codes by column, in words of four rows; the words of column k change places
   // by k / 16, so that a warp's words lie in 32 banks
@@ -222,7 +253,8 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const WeightParam
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) m = amax(m, s_max[w]);
-  const float scale = scale_of(m), inv = 1.f / scale;
+  const float scale = scale_of(m);
+  const Inverse inv = inverse_of(scale);
   if (threadIdx.x == 0) {
     p.scales[blk] = scale;
     if (kTransposed) p.scales_t[(e * p.k_blocks + bk) * p.n_blocks + bn] = scale;

@@ -205,6 +205,58 @@ def test_weights_with_infinities_and_nan():
     assert not c[:, 128:].isnan().any() and scales[0, :, 1].isfinite().all()
 
 
+def codes_by_quotient(src, scale):
+    """What the definition gives of one scale a row: E4M3 of the quotient in fp32."""
+    return (src.float() / scale[:, None]).clamp(-448, 448).to(E4M3).view(torch.uint8)
+
+
+def blocks_of_ties(dtype):
+    """Rows of one block each, [n, 128]: every mantissa of bf16 over every other, at twelve sizes;
+    and (fp32) values a few steps from every border between two codes, of scales of every size."""
+    c, top = torch.arange(127), 2 * (1 + torch.arange(128) / 128)
+    rows = []
+    for j in range(12):
+        v = (1 + ((c + 11 * j) % 128) / 128) * 2.0 ** -j * (1 - 2 * (c % 2))
+        rows.append(torch.cat([top[:, None], v.expand(128, -1)], 1))
+    rows = torch.cat(rows)
+    if dtype is BF:
+        return rows
+    g = torch.Generator().manual_seed(12)
+    n = 4000
+    size = torch.exp2(torch.randint(-148, 126, (n,), generator=g).double())
+    size[: n // 2] = 1.0
+    top = ((1 + torch.rand(n, generator=g, dtype=torch.float64)) * size).float()
+    scale = (top / torch.full_like(top, 448.0)).clamp(min=2.0 ** -126)
+    odd = torch.cat([torch.arange(17, 32, 2) * 2.0 ** e for e in range(-10, 4)]
+                    + [torch.arange(1, 16, 2) * 2.0 ** -10])  # the borders
+    v = odd[torch.randint(0, len(odd), (n, 127), generator=g)].double() * scale[:, None].double()
+    bits = v.float().view(torch.int32) + torch.randint(-3, 4, (n, 127), generator=g, dtype=torch.int32)
+    v = torch.minimum(bits.clamp(min=0).view(F32), top[:, None])
+    v = v * (1 - 2 * torch.randint(0, 2, (n, 127), generator=g))
+    return torch.cat([rows, torch.cat([top[:, None], v], 1)])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_codes_are_those_of_the_quotient(dtype):
+    """scale = max |v| / 448 and code = E4M3(v / scale), both quotients in fp32, bit by bit: ties go to
+    the even code.  (Block maximum 1.078125, v = 0.80859375: 336 in fp32, code 320; times a rounded
+    reciprocal 336.00003, code 352.)"""
+    src = blocks_of_ties(dtype).to(dtype)
+    src[5, 9] = -0.0
+    n = src.shape[0]
+    want_s = (src.float().abs().amax(1) / torch.full((n,), 448.0)).clamp(min=2.0 ** -126)
+    want = codes_by_quotient(src, want_s)
+    _, codes, scales = rows_case(n, 128, dtype, src=src)
+    assert torch.equal(scales[:, 0], want_s)
+    assert torch.equal(codes.view(torch.uint8), want), int((codes.view(torch.uint8) != want).sum())
+    # the same as blocks of weights, [1, 128] each
+    p = moe.QuantWeightsProblem.make(n, 1, 128, dtype)
+    codes, scales = torch.empty(n, 1, 128, dtype=E4M3, device=DEV), torch.empty(n, 1, 1, device=DEV)
+    moe.fp8_quantize_weights(p, src.view(n, 1, 128).to(DEV), codes, scales)
+    assert torch.equal(scales.view(-1).cpu(), want_s)
+    assert torch.equal(codes.view(torch.uint8).cpu().view(n, 128), want)
+
+
 # ------------------------------------------------------------------ product
 def operands(M, N, K, E, seed=0, std=1.0):
     g = torch.Generator().manual_seed(seed + M + N + K)
