@@ -51,7 +51,6 @@ class RouterProblem(ctypes.Structure):
                 int(bool(renormalize)), float(scale), ld)
         p._l, p._rows, p._ld = logits_dtype, (T, E), (ld or E, 1)
         p._bias, p._topk = (E,), (T, k)
-        p._ref = ctypes.byref(p)
         return p
 
 
@@ -71,7 +70,6 @@ class QuantProblem(ctypes.Structure):
         width = 2 * H if swiglu else H
         p._s, p._src, p._ld = src_dtype, (T, width), (ld or width, 1)
         p._codes, p._scales = (T, H), (T, _blocks(H))
-        p._ref = ctypes.byref(p)
         return p
 
 
@@ -86,7 +84,6 @@ class QuantWeightsProblem(ctypes.Structure):
         p = cls(E, N, K, _dtype(src_dtype))
         p._s, p._codes, p._codes_t = src_dtype, (E, N, K), (E, K, N)
         p._scales, p._scales_t = (E, _blocks(N), _blocks(K)), (E, _blocks(K), _blocks(N))
-        p._ref = ctypes.byref(p)
         return p
 
 
@@ -101,7 +98,6 @@ class FP8Problem(ctypes.Structure):
         p = cls(M, N, K, E, _dtype(out_dtype))
         p._o, p._out, p._x, p._xs = out_dtype, (M, N), (M, K), (M, _blocks(K))
         p._w, p._ws, p._offsets = (E, N, K), (E, _blocks(N), _blocks(K)), (E + 1,)
-        p._ref = ctypes.byref(p)
         return p
 
 
@@ -125,7 +121,7 @@ def router_forward(p: RouterProblem, logits, topk_idx, topk_w, bias=None, stream
     score plus ``bias`` ([E] fp32), best first, ties to the lowest id; weights of the scores alone.
     Slots for which no expert is left (logits of -inf) get -1 and 0."""
     rc = load().moe_router_forward(
-        p._ref, _rows(logits, p._l, p._rows, p._ld),
+        ctypes.byref(p), _rows(logits, p._l, p._rows, p._ld),
         _dense(bias, torch.float32, p._bias), _dense(topk_idx, torch.int32, p._topk),
         _dense(topk_w, torch.float32, p._topk), _raw_stream(stream))
     if rc != MOE_OK:
@@ -135,7 +131,7 @@ def router_forward(p: RouterProblem, logits, topk_idx, topk_w, bias=None, stream
 def router_backward(p: RouterProblem, logits, topk_idx, d_topk_w, d_logits, stream=None) -> None:
     """d_logits [T, E] (of the logits' type and strides) from the gradients of topk_w."""
     rc = load().moe_router_backward(
-        p._ref, _rows(logits, p._l, p._rows, p._ld),
+        ctypes.byref(p), _rows(logits, p._l, p._rows, p._ld),
         _dense(topk_idx, torch.int32, p._topk), _dense(d_topk_w, torch.float32, p._topk),
         _rows(d_logits, p._l, p._rows, p._ld), _raw_stream(stream))
     if rc != MOE_OK:
@@ -146,7 +142,7 @@ def fp8_quantize_rows(p: QuantProblem, src, codes, scales, stream=None) -> None:
     """codes [T, H] E4M3 and scales [T, ceil(H / 128)] fp32 of the rows of src, or of the SwiGLU of
     their gate and up values: scale = max |v| / 448 of every 128 values, code = v / scale."""
     rc = load().moe_fp8_quantize_rows(
-        p._ref, _rows(src, p._s, p._src, p._ld), _codes(codes, p._codes),
+        ctypes.byref(p), _rows(src, p._s, p._src, p._ld), _codes(codes, p._codes),
         _dense(scales, torch.float32, p._scales), _raw_stream(stream))
     if rc != MOE_OK:
         raise MoEError("moe_fp8_quantize_rows", rc)
@@ -157,7 +153,7 @@ def fp8_quantize_weights(p: QuantWeightsProblem, src, codes, scales, codes_t=Non
     """codes [E, N, K] E4M3 and scales [E, ceil(N / 128), ceil(K / 128)] fp32 of src [E, N, K], a
     scale for every 128 x 128; ``codes_t`` and ``scales_t`` get the same blocks transposed."""
     rc = load().moe_fp8_quantize_weights(
-        p._ref, _dense(src, p._s, p._codes), _codes(codes, p._codes),
+        ctypes.byref(p), _dense(src, p._s, p._codes), _codes(codes, p._codes),
         _dense(scales, torch.float32, p._scales), _codes(codes_t, p._codes_t),
         _dense(scales_t, torch.float32, p._scales_t), _raw_stream(stream))
     if rc != MOE_OK:
@@ -176,7 +172,7 @@ def fp8_matmul(p: FP8Problem, x, x_scale, w, w_scale, out, ws, expert_offsets=No
     are expert_offsets[e] .. expert_offsets[e + 1] (int32 [E + 1]; None: one expert has them all).
     Rows of out that are no expert's are left as they were."""
     rc = load().moe_fp8_matmul(
-        p._ref, _codes(x, p._x), _dense(x_scale, torch.float32, p._xs), _codes(w, p._w),
+        ctypes.byref(p), _codes(x, p._x), _dense(x_scale, torch.float32, p._xs), _codes(w, p._w),
         _dense(w_scale, torch.float32, p._ws), _dense(expert_offsets, torch.int32, p._offsets),
         _dense(out, p._o, p._out), *_workspace(ws), _raw_stream(stream))
     if rc != MOE_OK:

@@ -1,6 +1,8 @@
 """CPU checks of the entry points of include/moe_experts.h: bad arguments are refused on the host,
 before any CUDA call (no kernel is launched here)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -164,3 +166,39 @@ def test_binding_rejects_tensors_that_are_not_the_problems():
         moe.alloc_fp8_matmul_workspace(moe.FP8Problem.make(4, 8, 24))
     with pytest.raises(ValueError):
         moe.FP8Experts(torch.zeros(2, 64, 256), torch.zeros(2, 256, 48), 1)
+
+
+@pytest.mark.parametrize("p,field,other", [
+    (moe.RouterProblem.make(8, 64, 4, scale=2.5), "E", 1032),
+    (moe.QuantProblem.make(8, 256), "H", 264),
+    (moe.QuantWeightsProblem.make(2, 256, 384), "K", 388),
+    (moe.FP8Problem.make(64, 256, 384, 4), "K", 392)])
+def test_a_copied_problem_is_the_one_that_a_call_uses(p, field, other, lib, monkeypatch):
+    """A copy with a field that the library refuses: calls with it are refused, those with the
+    original are not."""
+    monkeypatch.setattr(moe.experts, "_dense", lambda t, *_: t)
+    monkeypatch.setattr(moe.experts, "_rows", lambda t, *_: t)
+    monkeypatch.setattr(moe.experts, "_codes", lambda t, *_: t)
+    monkeypatch.setattr(moe.experts, "_workspace", lambda t: (t, BIG))
+    monkeypatch.setattr(moe.experts, "_raw_stream", lambda s: None)
+    calls = {moe.RouterProblem: [lambda q: moe.router_forward(q, None, A, A),
+                                 lambda q: moe.router_backward(q, None, A, A, A)],
+             moe.QuantProblem: [lambda q: moe.fp8_quantize_rows(q, A + 8, A, A)],
+             moe.QuantWeightsProblem: [lambda q: moe.fp8_quantize_weights(q, A + 8, A, A)],
+             moe.FP8Problem: [lambda q: moe.fp8_matmul(q, A + 8, A, A, A, A, A, expert_offsets=A)]}[type(p)]
+
+    def status(call, q):
+        with pytest.raises(moe.MoEError) as e:  # (a bad tensor: no kernel is launched)
+            call(q)
+        return e.value.status
+
+    copies = [copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))]
+    for call in calls:
+        want = status(call, p)
+        for q in copies:
+            assert bytes(q) == bytes(p) and status(call, q) == want
+    for q in copies:
+        setattr(q, field, other)
+        for call in calls:
+            assert status(call, q) == 2
+            assert status(call, p) == (1 if type(p) is moe.RouterProblem else 3)
