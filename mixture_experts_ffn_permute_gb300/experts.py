@@ -212,7 +212,7 @@ class FP8Experts:
         def empty(*shape, dtype=torch.int32):
             return torch.empty(*shape, dtype=dtype, device=dev)
 
-        self._T = T
+        self._T = -1  # no plan until all of it is there: an allocation may fail
         self._p = Problem.make(T, H, F, E, self.k)
         self._p_in = QuantProblem.make(T, H)
         self._p_h = QuantProblem.make(R, F, swiglu=True, glu_interleave=self.glu_interleave,
@@ -227,6 +227,7 @@ class FP8Experts:
         self.ws = alloc_workspace(self._p, dev)  # of the permutation
         clear_device_status(self.ws)
         self.ws_matmul = alloc_fp8_matmul_workspace(self._p1, dev)
+        self._T = T
 
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -202,3 +202,57 @@ def test_a_copied_problem_is_the_one_that_a_call_uses(p, field, other, lib, monk
         for call in calls:
             assert status(call, q) == 2
             assert status(call, p) == (1 if type(p) is moe.RouterProblem else 3)
+
+
+# ------------------------------------------------------------------ FP8Experts on the host
+@pytest.fixture
+def layer(lib, monkeypatch):
+    """A layer whose kernels are records of the tensors they were given (nothing is launched)."""
+    m = moe.experts
+    calls = []
+    for name in ("fp8_quantize_rows", "permute", "permute_rows", "fp8_matmul", "unpermute_combine"):
+        monkeypatch.setattr(m, name, lambda *a, _n=name, **kw: calls.append((_n, a, kw)))
+    monkeypatch.setattr(m, "_dense", lambda t, *_: t)
+    monkeypatch.setattr(m, "clear_device_status", lambda ws: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    capturing = [False]
+    monkeypatch.setattr(m.FP8Experts, "_quantize", staticmethod(lambda w: (w, w)))
+    layer = moe.FP8Experts(torch.zeros(4, 512, 256), torch.zeros(4, 256, 256), 2)
+
+    def call(T):
+        calls.clear()
+        layer(torch.zeros(T, 256), torch.zeros(T, 2, dtype=torch.int32), torch.zeros(T, 2))
+        for _, args, kw in calls:  # every buffer is one of T tokens
+            p = args[0]
+            assert (p.T if hasattr(p, "T") else p.M) in (T, 2 * T)
+            for t in (*args[1:], *kw.values()):
+                if isinstance(t, torch.Tensor) and t.dim() > 1 and t.shape[0] != 4:
+                    assert t.shape[0] in (T, 2 * T)
+        return [t.data_ptr() for _, a, kw in calls for t in (*a[1:], *kw.values()) if isinstance(t, torch.Tensor)]
+
+    call.layer, call.calls, call.capturing = layer, calls, capturing
+    return call
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_a_plan_that_fails_is_not_used(layer, first, monkeypatch):
+    """Memory that runs out while a plan is made: the next call makes it again, whole."""
+    if not first:
+        layer(8)
+    real, fail_at = torch.empty, [0]
+
+    def empty(*a, **kw):
+        fail_at[0] -= 1
+        if fail_at[0] == 0:
+            raise torch.OutOfMemoryError("no memory left")
+        return real(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    for n in range(1, 15):
+        fail_at[0] = n
+        with pytest.raises(torch.OutOfMemoryError):
+            layer(32)
+        fail_at[0] = 0
+        layer(32)
+        layer(8)
+
