@@ -233,6 +233,8 @@ class FP8Experts:
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """out [T, H] bf16 for x [T, H] bf16 and the routing that ``router_forward`` writes."""
         T = x.shape[0]
+        if x.device != self.w1.device:
+            raise ValueError(f"expected rows on the weights' {self.w1.device}, got {x.device}")
         if out is None:
             out = torch.empty_like(x)
         if T == 0:

@@ -256,3 +256,12 @@ def test_a_plan_that_fails_is_not_used(layer, first, monkeypatch):
         layer(32)
         layer(8)
 
+
+
+def test_rows_of_another_device_are_refused_before_a_plan(layer):
+    before = layer(8)
+    with pytest.raises(ValueError):
+        layer.layer(torch.zeros(16, 256, device="meta"), torch.zeros(16, 2, dtype=torch.int32, device="meta"),
+                    torch.zeros(16, 2, device="meta"))
+    assert layer.layer._T == 8
+    assert layer(8)[1:3] == before[1:3]  # (codes and scales: the plan is the same)
