@@ -184,7 +184,8 @@ class FP8Experts:
     ``w2`` [E, H, F], bf16 or fp32) and the reusable workspaces of one token count.  A call runs the
     layer of given routing on bf16 rows: quantise, permute, first product, SwiGLU and quantise,
     second product, weighted sum.  H is a multiple of 256 and F one of 128, as the layer's are; the
-    workspaces are its own, so one call runs at a time."""
+    workspaces are its own, so one call runs at a time.  A call of another token count takes new
+    ones; those of calls that a graph has captured stay as long as the layer, for its replays."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int, glu_interleave=0,
                  swiglu_clamp=0.0):
@@ -197,6 +198,7 @@ class FP8Experts:
         self.w1, self.s1 = self._quantize(w1)
         self.w2, self.s2 = self._quantize(w2)
         self._T = -1
+        self._captured, self._kept = False, []
 
     @staticmethod
     def _quantize(w):
@@ -213,6 +215,9 @@ class FP8Experts:
             return torch.empty(*shape, dtype=dtype, device=dev)
 
         self._T = -1  # no plan until all of it is there: an allocation may fail
+        if self._captured:  # a graph's replays write to the buffers
+            self._kept.append([t for t in vars(self).values() if isinstance(t, torch.Tensor)])
+            self._captured = False
         self._p = Problem.make(T, H, F, E, self.k)
         self._p_in = QuantProblem.make(T, H)
         self._p_h = QuantProblem.make(R, F, swiglu=True, glu_interleave=self.glu_interleave,
@@ -244,6 +249,7 @@ class FP8Experts:
         _dense(out, torch.bfloat16, (T, self.H))
         if T != self._T:
             self._plan(T, x.device)
+        self._captured |= torch.cuda.is_current_stream_capturing()
         fp8_quantize_rows(self._p_in, x, self._x, self._xs)
         permute(self._p, topk_idx, None, None, self._row_id, self._token, self.tokens_per_expert,
                 self._offsets, self.ws)

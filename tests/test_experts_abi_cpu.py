@@ -2,7 +2,9 @@
 before any CUDA call (no kernel is launched here)."""
 import copy
 import ctypes
+import gc
 import pickle
+import weakref
 
 import pytest
 import torch
@@ -265,3 +267,25 @@ def test_rows_of_another_device_are_refused_before_a_plan(layer):
                     torch.zeros(16, 2, device="meta"))
     assert layer.layer._T == 8
     assert layer(8)[1:3] == before[1:3]  # (codes and scales: the plan is the same)
+
+
+def test_buffers_of_a_captured_call_stay(layer):
+    """Another token count frees the buffers of the one before it, but not those that a graph
+    replays into."""
+    def buffers():
+        return [weakref.ref(t) for _, a, kw in layer.calls for t in (*a[1:], *kw.values())
+                if isinstance(t, torch.Tensor) and t.dim() and any(t is b for b in vars(layer.layer).values())]
+
+    layer(8)
+    eager = buffers()
+    layer.capturing[0] = True
+    layer(16)
+    layer.capturing[0] = False
+    captured = buffers()
+    layer(24)
+    layer(32)
+    layer.calls.clear()
+    gc.collect()
+    assert len(captured) > 10 and all(r() is not None for r in captured)
+    weights = [layer.layer.w1, layer.layer.w2]
+    assert all(r() is None or any(r() is w for w in weights) for r in eager)

@@ -212,3 +212,34 @@ def test_layer_changes_its_token_count_and_masks():
     assert torch.equal(again, whole)
     assert layer(x[:0], idx[:0], w[:0]).shape == (0, H)
     assert moe.get_device_status(layer.ws) == moe.MOE_OK
+
+
+def test_layer_in_a_graph_while_its_token_count_changes():
+    """A captured call of FP8Experts replays into its own buffers after eager calls of other counts
+    took new ones; memory freed meanwhile belongs to others and stays as they wrote it."""
+    E, H, F, k, T = 8, 256, 256, 2, 96
+    g = torch.Generator(device=DEV).manual_seed(7)
+    layer = moe.FP8Experts(torch.randn(E, 2 * F, H, generator=g, device=DEV) / 16,
+                           torch.randn(E, H, F, generator=g, device=DEV) / 16, k)
+    x = torch.randn(T, H, generator=g, device=DEV).to(BF)
+    p = moe.RouterProblem.make(T, E, k, score="sigmoid")
+    idx, w = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    moe.router_forward(p, torch.randn(T, E, generator=g, device=DEV), idx, w)
+    want = layer(x, idx, w)  # (and the plan, outside the graph)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(x, idx, w, out=out)
+    others = []
+    for n in (8, 96, 40):
+        part = layer(x[:n], idx[:n].contiguous(), w[:n].contiguous())
+        others.append((n, part))
+        others += [(None, torch.full((n * H,), 5, dtype=torch.uint8, device=DEV)) for _ in range(40)]
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for n, t in others:
+        assert torch.equal(t, want[:n]) if n else (t == 5).all()
+    assert moe.get_device_status(layer.ws) == moe.get_device_status(layer.ws_matmul) == moe.MOE_OK
