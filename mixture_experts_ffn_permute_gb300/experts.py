@@ -216,7 +216,7 @@ class FP8Experts:
 
         self._T = -1  # no plan until all of it is there: an allocation may fail
         if self._captured:  # a graph's replays write to the buffers
-            self._kept.append([t for t in vars(self).values() if isinstance(t, torch.Tensor)])
+            self._kept.append(self._tensors())
             self._captured = False
         self._p = Problem.make(T, H, F, E, self.k)
         self._p_in = QuantProblem.make(T, H)
@@ -232,7 +232,10 @@ class FP8Experts:
         self.ws = alloc_workspace(self._p, dev)  # of the permutation
         clear_device_status(self.ws)
         self.ws_matmul = alloc_fp8_matmul_workspace(self._p1, dev)
-        self._T = T
+        self._T, self._streams = T, {_raw_stream(None)}
+
+    def _tensors(self):
+        return [t for t in vars(self).values() if isinstance(t, torch.Tensor)]
 
     def __call__(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -249,6 +252,11 @@ class FP8Experts:
         _dense(out, torch.bfloat16, (T, self.H))
         if T != self._T:
             self._plan(T, x.device)
+        stream = _raw_stream(None)
+        if stream not in self._streams:  # (the allocator knows of the one they were made on)
+            for t in self._tensors():
+                t.record_stream(torch.cuda.current_stream())
+            self._streams.add(stream)
         self._captured |= torch.cuda.is_current_stream_capturing()
         fp8_quantize_rows(self._p_in, x, self._x, self._xs)
         permute(self._p, topk_idx, None, None, self._row_id, self._token, self.tokens_per_expert,

@@ -216,6 +216,7 @@ def layer(lib, monkeypatch):
         monkeypatch.setattr(m, name, lambda *a, _n=name, **kw: calls.append((_n, a, kw)))
     monkeypatch.setattr(m, "_dense", lambda t, *_: t)
     monkeypatch.setattr(m, "clear_device_status", lambda ws: None)
+    monkeypatch.setattr(m, "_raw_stream", lambda s=None: 0)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
     capturing = [False]
     monkeypatch.setattr(m.FP8Experts, "_quantize", staticmethod(lambda w: (w, w)))
@@ -289,3 +290,30 @@ def test_buffers_of_a_captured_call_stay(layer):
     assert len(captured) > 10 and all(r() is not None for r in captured)
     weights = [layer.layer.w1, layer.layer.w2]
     assert all(r() is None or any(r() is w for w in weights) for r in eager)
+
+
+def test_buffers_are_kept_for_every_stream_that_uses_them(layer, monkeypatch):
+    """Calls on another stream than the one the buffers were made on say so to the allocator, which
+    would else give them away, when another token count frees them, under that stream's work."""
+    stream, told = [1], []
+    monkeypatch.setattr(moe.experts, "_raw_stream", lambda s=None: stream[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: stream[0])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: told.append((t, s)))
+    layer(8)
+    layer(8)
+    assert not told
+    stream[0] = 2
+    layer(8)
+    used = [t for _, a, kw in layer.calls for t in (*a[1:], *kw.values()) if isinstance(t, torch.Tensor)]
+    mine = [t for t in vars(layer.layer).values() if isinstance(t, torch.Tensor)]
+    for t in mine:
+        if any(t is u for u in used):
+            assert any(t is u and s == 2 for u, s in told)
+    told.clear()
+    layer(8)  # (once is enough)
+    assert not told
+    layer(16)  # made on this stream
+    assert not told
+    stream[0] = 1
+    layer(16)
+    assert len(told) >= 14 and {s for _, s in told} == {1}

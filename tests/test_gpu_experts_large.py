@@ -243,3 +243,32 @@ def test_layer_in_a_graph_while_its_token_count_changes():
     for n, t in others:
         assert torch.equal(t, want[:n]) if n else (t == 5).all()
     assert moe.get_device_status(layer.ws) == moe.get_device_status(layer.ws_matmul) == moe.MOE_OK
+
+
+def test_layer_on_two_streams_while_its_token_count_changes():
+    """Buffers made on one stream and used on another are not given away under the other's work."""
+    E, H, F, k = 8, 512, 512, 2
+    g = torch.Generator(device=DEV).manual_seed(8)
+    layer = moe.FP8Experts(torch.randn(E, 2 * F, H, generator=g, device=DEV) / 22,
+                           torch.randn(E, H, F, generator=g, device=DEV) / 22, k)
+    x = torch.randn(2048, H, generator=g, device=DEV).to(BF)
+    idx = torch.randint(0, E, (2048, k), generator=g, device=DEV, dtype=torch.int32)
+    w = torch.rand(2048, k, generator=g, device=DEV)
+    want = layer(x, idx, w)
+    small = layer(x[:64], idx[:64].contiguous(), w[:64].contiguous())
+    outs = []
+    s = torch.cuda.Stream()
+    layer(x, idx, w)
+    for _ in range(5):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(layer(x, idx, w))
+        filler = [torch.full((2048 * k, 2 * F), 1.0, dtype=BF, device=DEV) for _ in range(4)]
+        layer._plan(64, x.device)
+        del filler
+        torch.cuda.current_stream().wait_stream(s)
+        outs.append(layer(x[:64], idx[:64].contiguous(), w[:64].contiguous()))
+        layer._plan(2048, x.device)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want if o.shape[0] == 2048 else small)
