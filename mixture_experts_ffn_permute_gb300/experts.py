@@ -229,7 +229,8 @@ class FP8Experts:
         self._h, self._hs = empty(R, F, dtype=_E4M3), empty(R, _blocks(F), dtype=torch.float32)
         self._row_id, self._token = empty(T, self.k), empty(R)
         self.tokens_per_expert, self._offsets = empty(E), empty(E + 1)
-        self.ws = alloc_workspace(self._p, dev)  # of the permutation
+        # of the permutation, which uses none that goes with the rows' width
+        self.ws = alloc_workspace(Problem.make(T, 0, 0, E, self.k), dev)
         clear_device_status(self.ws)
         self.ws_matmul = alloc_fp8_matmul_workspace(self._p1, dev)
         self._T, self._streams = T, {_raw_stream(None)}

@@ -317,3 +317,12 @@ def test_buffers_are_kept_for_every_stream_that_uses_them(layer, monkeypatch):
     stream[0] = 1
     layer(16)
     assert len(told) >= 14 and {s for _, s in told} == {1}
+
+
+def test_the_layers_workspace_is_that_of_the_permutation(layer):
+    """Of the permutation's regions alone: nothing that grows with the rows' width."""
+    layer(4096)
+    l = layer.layer
+    routing = moe.workspace_size(moe.Problem.make(4096, 0, 0, l.E, l.k))
+    assert l.ws.numel() == routing < 4096 * l.k * 100
+    assert moe.workspace_size(l._p) > 4096 * l.k * (4 * l.H + 2 * l.F)
