@@ -185,7 +185,9 @@ class FP8Experts:
     layer of given routing on bf16 rows: quantise, permute, first product, SwiGLU and quantise,
     second product, weighted sum.  H is a multiple of 256 and F one of 128, as the layer's are; the
     workspaces are its own, so one call runs at a time.  A call of another token count takes new
-    ones; those of calls that a graph has captured stay as long as the layer, for its replays."""
+    ones; those of calls that a graph has captured stay as long as the layer, for its replays.
+    ``get_device_status`` of ``ws`` tells of ids beyond the experts, of ``ws_matmul`` of products
+    that did not finish."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int, glu_interleave=0,
                  swiglu_clamp=0.0):
