@@ -18,8 +18,8 @@
 //
 // Bound by latency and instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate);
 // k = 8 with a bias and 8 groups takes 14.4 us (a token 8000 cycles, in 1.7 waves; near
-// picks 4500 cycles more, near groups 20000, fp64 30000), without a bias and groups 10.0;
-// T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 25 us).
+// picks 4500 cycles more, near groups 20000, fp64 30000), without a bias and groups 10.0, k = 32
+// with a bias 28; T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 25 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -190,6 +190,16 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
       own = best;
     }
   }
+}
+
+// Of 32 picks: `next`, and in the last lane, whose next pick no lane has, the highest key left.
+template <int kN, typename Key>
+__device__ __forceinline__ Key runner_up(const Key (&key)[kN], int lane, Key next) {
+  Key left = key[0];
+#pragma unroll
+  for (int i = 1; i < kN; ++i) left = left > key[i] ? left : key[i];
+  left = warp_max(left);
+  return lane == 31 ? left : next;
 }
 
 // The same from lists that every lane has sorted, highest first and the first among
@@ -568,13 +578,14 @@ __device__ __noinline__ bool choose_two(const RouterParams& p, const T* row, flo
     for (int i = 0; i < kN; ++i)
       if (!(in >> i & 1u)) key[i] = 0;
     pick(key, p.k, lane, id, own);
-    const uint64_t next = __shfl_down_sync(kAll, own, 1);
+    uint64_t next = __shfl_down_sync(kAll, own, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    bool close = p.k == 32;  // (no lane for the runner-up)
-    if (lane < p.k && lane < 31 && next != 0) {
+    if (p.k == 32) next = runner_up(key, lane, next);
+    bool close = false;
+    if (lane < p.k && next != 0) {
       const float b = __ldg(p.bias + id);
-      close |= !(minus(own, next) > 0x1p-40f * (1.f + fabsf(b))) &&
-               !(to_float(row[id]) == to_float(row[next_id]) && b == __ldg(p.bias + next_id));
+      close = !(minus(own, next) > 0x1p-40f * (1.f + fabsf(b))) &&
+              !(lane < 31 && to_float(row[id]) == to_float(row[next_id]) && b == __ldg(p.bias + next_id));
     }
     return !__any_sync(kAll, close);
   }
@@ -812,15 +823,15 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
   }
   bool fine = true;  // pairs of fp32 may tell
   if (by_score) {
-    // lane j against pick j + 1 (k of 32 has no lane for the runner-up: always
-    // looked at again)
-    const uint32_t next = __shfl_down_sync(kAll, own, 1);
+    // lane j against pick j + 1
+    uint32_t next = __shfl_down_sync(kAll, own, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    bool close = lane < p.k && lane < 31 && near(own, next);
+    if (p.k == 32) next = runner_up(key, lane, next);
+    bool close = lane < p.k && near(own, next);
     if (close)  // the same logit and bias are the same score, and in order
-      close = !(to_float(row[id]) == to_float(row[next_id]) &&
+      close = !(lane < 31 && to_float(row[id]) == to_float(row[next_id]) &&
                 __ldg(p.bias + id) == __ldg(p.bias + next_id));
-    bool tie = __any_sync(kAll, close) || p.k == 32;
+    bool tie = __any_sync(kAll, close);
     if constexpr (kSort) {
       if (tie && !redo && !broken && p.k < 31) {
         // More picks, until one lies clear of the one before it; then they are put in

@@ -497,3 +497,26 @@ def test_experts_out_of_the_choice_in_groups(E, groups, dtype):
             for kept, top in ((1, 1), (groups // 2, 2), (groups - 1, 1)):
                 check(moe.RouterProblem.make(T, E, 8, dtype, score, groups=groups, topk_groups=kept,
                                              group_top=top), logits, b)
+
+
+@pytest.mark.parametrize("E", [33, 60, 256, 320, 512, 1000])
+def test_runner_up_of_32_picks(E):
+    """k = 32 with a bias: picks far apart but for the last one and the first left out, which differ by
+    a step or two of fp32, by less than fp32 shows, or not at all."""
+    T = 60
+    g = torch.Generator().manual_seed(E)
+    order = torch.stack([torch.randperm(E, generator=g) for _ in range(T)])
+    place = torch.arange(E).clamp(max=60).float()
+    values = 3.0 - 0.1 * place + 0.02 * torch.rand(T, E, generator=g)
+    values[:, 32] = values[:, 31]
+    for t in range(T):
+        for _ in range(t % 3):
+            values[t, 32] = torch.nextafter(values[t, 32], torch.tensor(9.0 if t % 2 else -9.0))
+    logits = torch.empty(T, E).scatter_(1, order, values)
+    tiny = torch.randint(0, 3, (E,), generator=g).float() * 2.0 ** -42
+    for score in ("softmax", "sigmoid"):
+        for b in (torch.zeros(E), tiny):
+            check(moe.RouterProblem.make(T, E, 32, score=score), logits, b)
+            if E % 4 == 0 and E > 60:
+                check(moe.RouterProblem.make(T, E, 32, score=score, groups=4, topk_groups=3, group_top=2),
+                      logits, b)
