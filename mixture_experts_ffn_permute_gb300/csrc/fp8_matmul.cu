@@ -64,8 +64,8 @@ namespace {
 
 constexpr int kBlk = 128;                       // a scale's extent along K and N
 constexpr uint32_t kPlane = 128 * kBlk;         // 128 rows x 128 codes, 16 KB
-constexpr int kMaxStages = 6;
 constexpr uint32_t kRing = 3 * 4 * kPlane;      // stages of two blocks of both operands
+constexpr int kMaxStages = kRing / (2 * kPlane + 2 * kBlk * 64);  // (of the lowest tiles: 4)
 constexpr int kMaxE = MOE_MAX_EXPERTS;
 constexpr int kGroupM = 8;  // row tiles whose sweep over the columns shares weight tiles in L2
 constexpr int kNarrow = 128;                    // rows of a narrow tile at most
@@ -1041,7 +1041,7 @@ cudaError_t launch_tiles(const moe_fp8_problem* p, const void* x, const void* w,
   if (!make_codes_map(&maps.w, w, p->K, p->N, p->E, k.planes, 128)) return cudaErrorInvalidValue;
   k.n_tiles = ceil_div(p->N, 128 * kCtas);
   k.x_stage = 2 * kBlk * (kPair ? 128 : k.tile_rows);
-  k.stages = std::min<int>(kMaxStages, kRing / (2 * kPlane + k.x_stage));
+  k.stages = static_cast<int>(kRing / (2 * kPlane + k.x_stage));
   const long most = most_tiles(p, k.tile_rows, k.n_tiles);
   k.splits = kPair ? 1 : splits_of(most, k.kblocks);
   const int ctas = kPair ? 2 : k.splits;  // of a tile
