@@ -452,6 +452,24 @@ def test_gradient_of_the_rows_by_the_transposed_weights():
     assert ((dx.cpu().double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("M,N,K,E", [(300, 272, 400, 5), (64, 512, 256, 40), (700, 144, 128, 3)])
+def test_gradient_of_the_rows_of_experts(M, N, K, E):
+    """d_x of rows grouped by expert, empty experts and rows of none among them: the product with the
+    transposed codes of the weights, which are the codes themselves turned around."""
+    g = torch.Generator().manual_seed(M)
+    wf = (torch.randn(E, N, K, generator=g) / math.sqrt(K)).to(BF)
+    d_out = torch.randn(M, N, generator=g).to(BF)
+    w, ws = torch.empty(E, N, K, dtype=E4M3, device=DEV), torch.empty(E, blocks(N), blocks(K), device=DEV)
+    wt, wts = torch.empty(E, K, N, dtype=E4M3, device=DEV), torch.empty(E, blocks(K), blocks(N), device=DEV)
+    moe.fp8_quantize_weights(moe.QuantWeightsProblem.make(E, N, K), wf.to(DEV), w, ws, codes_t=wt, scales_t=wts)
+    dq, ds = torch.empty(M, N, dtype=E4M3, device=DEV), torch.empty(M, blocks(N), device=DEV)
+    moe.fp8_quantize_rows(moe.QuantProblem.make(M, N), d_out.to(DEV), dq, ds)
+    back = (w.view(torch.uint8).transpose(1, 2).contiguous().view(E4M3), ws.transpose(1, 2).contiguous())
+    assert torch.equal(wt.view(torch.uint8), back[0].view(torch.uint8)) and torch.equal(wts, back[1])
+    for dtype in (BF, F32):
+        check_product(M, K, N, E, dtype, cut(M, E, tail=7), ops=[t.cpu() for t in (dq, ds, wt, wts)])
+
+
 def test_graph_replay_and_streams():
     M, N, K, E = 200, 272, 384, 4
     x, xs, w, ws = (t.to(DEV) for t in operands(M, N, K, E))
