@@ -192,14 +192,13 @@ __device__ __forceinline__ void pick(Key (&key)[kN], int k, int lane, int& id, K
   }
 }
 
-// Of 32 picks: `next`, and in the last lane, whose next pick no lane has, the highest key left.
-template <int kN, typename Key>
-__device__ __forceinline__ Key runner_up(const Key (&key)[kN], int lane, Key next) {
+// The highest key that is left after picks.
+template <bool kSorted, int kN, typename Key>
+__device__ __forceinline__ Key highest_left(const Key (&key)[kN]) {
   Key left = key[0];
 #pragma unroll
-  for (int i = 1; i < kN; ++i) left = left > key[i] ? left : key[i];
-  left = warp_max(left);
-  return lane == 31 ? left : next;
+  for (int i = 1; i < (kSorted ? 1 : kN); ++i) left = left > key[i] ? left : key[i];
+  return warp_max(left);
 }
 
 // The same from lists that every lane has sorted, highest first and the first among
@@ -455,6 +454,12 @@ __device__ __forceinline__ Two inverse(Two d) {
   return fast_two_sum(y, y * __fmaf_rn(-y, d.lo, __fmaf_rn(-y, d.hi, 1.f)));
 }
 
+// The same logit and bias: the same score, whatever its rounding.
+template <typename T>
+__device__ __forceinline__ bool same_expert(const RouterParams& p, const T* row, int a, int b) {
+  return to_float(row[a]) == to_float(row[b]) && __ldg(p.bias + a) == __ldg(p.bias + b);
+}
+
 // The first n picks, lane j's in lane j, in the order of their scores' 41 bits: all
 // of them are there that can be among the first n - 1.  False where they do not tell
 // two apart that are not the same logit and bias.
@@ -580,12 +585,16 @@ __device__ __noinline__ bool choose_two(const RouterParams& p, const T* row, flo
     pick(key, p.k, lane, id, own);
     uint64_t next = __shfl_down_sync(kAll, own, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    if (p.k == 32) next = runner_up(key, lane, next);
+    const uint64_t left = highest_left<false>(key);
+    if (lane == 31) next = left;  // (the last of 32 picks)
     bool close = false;
     if (lane < p.k && next != 0) {
-      const float b = __ldg(p.bias + id);
-      close = !(minus(own, next) > 0x1p-40f * (1.f + fabsf(b))) &&
-              !(lane < 31 && to_float(row[id]) == to_float(row[next_id]) && b == __ldg(p.bias + next_id));
+      const float eps = 0x1p-40f * (1.f + fabsf(__ldg(p.bias + id)));
+      close = !(minus(own, next) > eps);
+      // the same score, and in order; but behind a runner-up that is the last pick's like
+      // there may be a near one that is not
+      if (close && lane < 31 && same_expert(p, row, id, next_id))
+        close = lane == p.k - 1 && left != 0 && !(minus(own, left) > eps);
     }
     return !__any_sync(kAll, close);
   }
@@ -826,12 +835,20 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
     // lane j against pick j + 1
     uint32_t next = __shfl_down_sync(kAll, own, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    if (p.k == 32) next = runner_up(key, lane, next);
-    bool close = lane < p.k && near(own, next);
-    if (close)  // the same logit and bias are the same score, and in order
-      close = !(lane < 31 && to_float(row[id]) == to_float(row[next_id]) &&
-                __ldg(p.bias + id) == __ldg(p.bias + next_id));
-    bool tie = __any_sync(kAll, close);
+    if (p.k == 32) {  // no lane has the runner-up
+      const uint32_t left = highest_left<kSort>(key);
+      if (lane == 31) next = left;
+    }
+    const bool close = lane < p.k && near(own, next);
+    bool tie = false;
+    if (__any_sync(kAll, close)) {
+      // the same logit and bias are the same score, and in order
+      const bool same = close && lane < 31 && same_expert(p, row, id, next_id);
+      tie = __any_sync(kAll, close && !same);
+      // (behind a runner-up that is the last pick's like there may be a near one that is not)
+      if (!tie && __any_sync(kAll, same && lane == p.k - 1))
+        tie = near(__shfl_sync(kAll, own, p.k - 1), highest_left<kSort>(key));
+    }
     if constexpr (kSort) {
       if (tie && !redo && !broken && p.k < 31) {
         // More picks, until one lies clear of the one before it; then they are put in

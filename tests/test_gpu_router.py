@@ -520,3 +520,29 @@ def test_runner_up_of_32_picks(E):
             if E % 4 == 0 and E > 60:
                 check(moe.RouterProblem.make(T, E, 32, score=score, groups=4, topk_groups=3, group_top=2),
                       logits, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [37, 64, 100, 256, 320, 600, 1000])
+def test_equal_experts_at_the_border_of_the_choice(E, dtype):
+    """The last pick and the first expert left out are the same, and one behind them is higher by less
+    than fp32 shows, or lower, or the same too; with and without groups, with picks above them."""
+    T = 48
+    g = torch.Generator().manual_seed(E)
+    logits = torch.rand(T, E, generator=g) - 8.0
+    next_up = float(torch.nextafter(torch.tensor(0.5), torch.tensor(9.0)))
+    for t in range(T):
+        ids = torch.randperm(E, generator=g)[:8].sort().values
+        low, high = ((27.5, 81.5), (20.0, 20.125), (0.5, next_up), (0.5, 0.50390625))[t % 4]
+        logits[t, ids] = low
+        for i in ids[2 + t % 5:].tolist():
+            logits[t, i] = (high, low, low - 0.125)[int(torch.randint(0, 3, (1,), generator=g))]
+        if t % 4 > 1:
+            logits[t, ids[torch.randperm(8, generator=g)[:2]]] = torch.tensor([3.0, 4.0])
+    for score in ("sigmoid", "softmax"):
+        l = logits if score == "sigmoid" else torch.where(logits > 0, logits * 2.0 ** -10, logits)
+        for b in (torch.zeros(E), torch.full((E,), 0.25)):
+            for k in (1, 2, 3, 5, 7, 31, 32):
+                check(moe.RouterProblem.make(T, E, k, dtype, score), l.to(dtype), b)
+            if E % 4 == 0:
+                check(moe.RouterProblem.make(T, E, 2, dtype, score, groups=4, topk_groups=3), l.to(dtype), b)
