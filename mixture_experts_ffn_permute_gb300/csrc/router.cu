@@ -791,7 +791,10 @@ __global__ void __launch_bounds__(kForwardThreads) router_forward_kernel(const R
       const float margin = tol + size * 0x1p-22f;
       const bool taken = mask >> lane & 1u;
       const float least = taken && total != 0 ? (size < kInf ? margin - v : kInf) : -kInf;
-      const float most = taken || total <= 1u || v == -kInf ? -kInf : size < kInf ? v + margin + (packed ? size * kBelow : 0.f) : kInf;
+      // (a packed -inf may have been the lowest finite value: beside +inf that is +inf, not NaN)
+      const bool opposite = total == 1u && a > 1u && b > 1u;
+      const float most = taken || (total <= 1u && !opposite) || v == -kInf ? -kInf
+                         : size < kInf ? v + margin + (packed ? size * kBelow : 0.f) : kInf;
       const float highest = warp_fmax(most);
       redo = __any_sync(kAll, !taken && total != 0) && !(-warp_fmax(least) > highest);
     }

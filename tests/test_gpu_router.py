@@ -546,3 +546,24 @@ def test_equal_experts_at_the_border_of_the_choice(E, dtype):
                 check(moe.RouterProblem.make(T, E, k, dtype, score), l.to(dtype), b)
             if E % 4 == 0:
                 check(moe.RouterProblem.make(T, E, 2, dtype, score, groups=4, topk_groups=3), l.to(dtype), b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E,groups", [(20, 4), (64, 8), (192, 8), (256, 8), (512, 8), (1000, 5)])
+def test_an_infinite_bias_beside_the_lowest(E, groups, dtype):
+    """A group's two best are an expert of +inf and one of the type's lowest value (their sum is +inf), of
+    -inf (no number), or a few steps above the lowest."""
+    T, per = 30, E // groups
+    logits, bias = draw(T, E, dtype, seed=71)
+    low = torch.finfo(F32).min
+    for g, other in ((1, low), (2, NEG), (3, low * (1 - 2.0 ** -22))):
+        lo = g * per
+        logits[:, lo + 2:lo + per] = NEG
+        logits[::3, lo + 1] = NEG  # (alone in its group)
+        bias[lo], bias[lo + 1] = (math.inf, other) if g != 2 else (other, math.inf)
+    for score in ("softmax", "sigmoid"):
+        for kept, top in ((1, 2), (2, 2), (3, 2), (2, 1)):
+            p = moe.RouterProblem.make(T, E, min(3, kept * per), dtype, score, groups=groups, topk_groups=kept,
+                                       group_top=top)
+            ids, _ = reference(p, logits, bias)
+            assert torch.equal(run(p, logits, bias)[0], ids), (score, kept, top)
