@@ -41,10 +41,10 @@ extern "C" {
  * The experts lie in `groups` equal groups of consecutive ids.  A group's score is
  * the sum of its group_top highest c; the topk_groups groups of the highest scores
  * stay, and of their experts the k of the highest c are chosen, highest first.
- * Equal c (equal scores) go to the lowest id.  Without a bias the experts are
- * ordered by their logits; otherwise c and the groups' scores are compared as 64
- * bits have them: fp32 values that are too near to tell are computed again, in pairs
- * of fp32 and in fp64 where those do not tell.
+ * Equal c (equal scores) go to the lowest id.  Without a bias the experts, and
+ * groups by one expert, are ordered by their logits; otherwise c and the groups'
+ * scores are compared as 64 bits have them: fp32 values that are too near to tell are
+ * computed again, in pairs of fp32 and in fp64 where those do not tell.
  *   w_j   = scale * s_j / (renormalize ? sum over the chosen of s : 1)
  * An expert whose logit is -infinity is out of the token's choice: it counts in
  * no group, and slots for which no expert is left get the id -1, which masks a
@@ -72,8 +72,9 @@ MOE_API int moe_router_forward(const moe_router_problem* p, const void* logits, 
                                int32_t* topk_idx, float* topk_w, void* stream);
 
 /* Gradient of the logits from the gradients of the weights; the choice passes
- * none.  Every element of d_logits [T, E] is written (not what lies between its
- * rows).
+ * none.  Sigmoids' and renormalised weights go by the chosen experts' logits alone,
+ * and so does their gradient: the others get 0, whatever their logits are.  Every
+ * element of d_logits [T, E] is written (not what lies between its rows).
  *   topk_idx  [T, k] as the forward wrote it; an id outside [0, E) is a masked slot
  *   d_topk_w  [T, k] fp32 (masked slots' values are not used) */
 MOE_API int moe_router_backward(const moe_router_problem* p, const void* logits,
@@ -128,7 +129,8 @@ MOE_API int moe_fp8_quantize_weights(const moe_quant_weights_problem* p, const v
  *   out[r, n] = sum over blocks b of 128 along K of
  *     x_scale[r, b] * w_scale[e, n / 128, b] * <x[r, b], w[e, n, b]>
  * for the rows r of every expert e.  A block's products are summed by the tensor
- * cores, the blocks in fp32.  The gradient of the rows is the same product with
+ * cores, the blocks in fp32; the two scales are multiplied first, so that their
+ * product has to be a number of fp32 (it loses bits below 2^-126).  The gradient of the rows is the same product with
  * the transposed codes: d_x[r] = d_out[r] W_e, rows of d_out quantised as x. */
 typedef struct moe_fp8_problem {
   int32_t M, N, K;    /* rows of all experts; width of out; length of the sums, a multiple of 16 */

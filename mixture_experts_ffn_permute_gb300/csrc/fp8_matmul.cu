@@ -34,8 +34,9 @@
 // commits some 100, and the epilogue 770: reading TMEM and FMAs, 250 cycles each and
 // behind one another (the two warps of a scheduler go in step), and 270 for the
 // hand-over.  A tile's end, whose sums go out while nothing else is done, takes 5000
-// of its 31000.  M=8192 E=8 N=28672 K=4096: 0.75 ms, 2580 TFLOP/s; without the FMAs, before
-// they were packed, 0.72 for 0.87, and the copies and hand-overs alone take 0.57.
+// of its 31000.  M=8192 E=8 N=28672 K=4096: 0.75 ms in short runs (2580 TFLOP/s), 0.85 in
+// long ones or on another GB300 (2260); without the FMAs, before they were packed, 0.72 for
+// 0.87, and the copies and hand-overs alone take 0.57.
 // Measured and not kept, us at that size: 16 epilogue warps (870 to 1000), loads of the
 // next columns under the FMAs (745 to 1100: registers move), four accumulators of 128
 // columns (the MMA is slower at N = 128; 985 to 1150), tiles of 192 columns (877 to 1007),

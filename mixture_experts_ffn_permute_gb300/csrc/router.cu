@@ -16,8 +16,8 @@
 // What those do not tell: the token in fp64.  With 256 sigmoid scores and a random bias
 // nine tokens of 8192 are looked at.
 //
-// Bound by latency and instruction issue: T=8192 E=256 reads 8.4 MB (1.2 us at HBM rate);
-// k = 8 with a bias and 8 groups takes 14.4 us (a token 8000 cycles, in 1.7 waves; near
+// Bound by latency (half of the issue slots are empty): T=8192 E=256 reads 8.4 MB (1.2 us at
+// HBM rate); k = 8 with a bias and 8 groups takes 14.4 to 15 us (a token 8000 cycles, in 1.7 waves; near
 // picks 4500 cycles more, near groups 20000, fp64 30000), without a bias and groups 10.0, k = 32
 // with a bias 28; T=131072 160 us.  The backward takes 5 us, most of it the call (T=65536 25 us).
 #include <cuda_runtime.h>

@@ -1,9 +1,9 @@
 """GPU parity of the quantisation to E4M3 and of the product of the codes against 64 bits.
 
 Quantisation: a scale is one quotient in fp32 (2^-24 of it; SwiGLU's values are off by their fast
-exponential, (|g| + 4) 2^-23).  A code is the nearest to v / scale, which the kernel has as v times
-a reciprocal, 2^-22 of it off: the code's distance from the exact quotient is at most half a step
-and that.
+exponential, (|g| + 4) 2^-23).  A code is that of the quotient v / scale in fp32: its distance from
+the exact quotient is at most half a step and 2^-22 of it, with room; bit by bit it is looked at by
+the tests of the borders between codes.
 
 Product: one rounding of the result; every block's sum is taken by the tensor core in four steps of
 32 products (each rounded or cut in the accumulator: 36 2^-23 of the terms' magnitude at most) and
