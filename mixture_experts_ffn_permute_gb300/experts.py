@@ -185,7 +185,8 @@ class FP8Experts:
     layer of given routing on bf16 rows: quantise, permute, first product, SwiGLU and quantise,
     second product, weighted sum.  H is a multiple of 256 and F one of 128, as the layer's are; the
     workspaces are its own, so one call runs at a time.  A call of another token count takes new
-    ones; those of calls that a graph has captured stay as long as the layer, for its replays.
+    ones; those of calls that a graph has captured stay as long as the layer, for its replays.  (A
+    captured call that no eager one of its token count came before has buffers of its own.)
     ``get_device_status`` of ``ws`` tells of ids beyond the experts, of ``ws_matmul`` of products
     that did not finish."""
 
@@ -200,7 +201,7 @@ class FP8Experts:
         self.w1, self.s1 = self._quantize(w1)
         self.w2, self.s2 = self._quantize(w2)
         self._T = -1
-        self._captured, self._kept = False, []
+        self._captured, self._made_captured, self._kept = False, False, []
 
     @staticmethod
     def _quantize(w):
@@ -253,14 +254,16 @@ class FP8Experts:
         _dense(topk_idx, torch.int32, (T, self.k))
         _dense(topk_w, torch.float32, (T, self.k))
         _dense(out, torch.bfloat16, (T, self.H))
-        if T != self._T:
+        capturing = torch.cuda.is_current_stream_capturing()
+        if T != self._T or self._made_captured:
             self._plan(T, x.device)
+            self._made_captured = capturing  # the graph clears the status words: no other call's
         stream = _raw_stream(None)
         if stream not in self._streams:  # (the allocator knows of the one they were made on)
             for t in self._tensors():
                 t.record_stream(torch.cuda.current_stream())
             self._streams.add(stream)
-        self._captured |= torch.cuda.is_current_stream_capturing()
+        self._captured |= capturing
         fp8_quantize_rows(self._p_in, x, self._x, self._xs)
         permute(self._p, topk_idx, None, None, self._row_id, self._token, self.tokens_per_expert,
                 self._offsets, self.ws)

@@ -326,3 +326,15 @@ def test_the_layers_workspace_is_that_of_the_permutation(layer):
     routing = moe.workspace_size(moe.Problem.make(4096, 0, 0, l.E, l.k))
     assert l.ws.numel() == routing < 4096 * l.k * 100
     assert moe.workspace_size(l._p) > 4096 * l.k * (4 * l.H + 2 * l.F)
+
+
+def test_buffers_made_in_a_capture_are_that_calls_alone(layer):
+    """Their status words are cleared by the graph, so that no other call may read them."""
+    layer.capturing[0] = True
+    first = layer(8)
+    second = layer(8)
+    layer.capturing[0] = False
+    eager = layer(8)
+    again = layer(8)
+    assert not set(first[1:3]) & set(second[1:3]) and not set(second[1:3]) & set(eager[1:3])
+    assert eager[1:3] == again[1:3]

@@ -272,3 +272,31 @@ def test_layer_on_two_streams_while_its_token_count_changes():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want if o.shape[0] == 2048 else small)
+
+
+def test_layer_captured_without_a_call_before():
+    """Two graphs of a layer whose first calls they are; an eager call before the first replay."""
+    E, H, F, k, T = 8, 256, 256, 2, 50
+    g = torch.Generator(device=DEV).manual_seed(9)
+    w1, w2 = torch.randn(E, 2 * F, H, generator=g, device=DEV) / 16, torch.randn(E, H, F, generator=g, device=DEV) / 16
+    x = torch.randn(T, H, generator=g, device=DEV).to(BF)
+    idx = torch.stack([torch.randperm(E, generator=g, device=DEV)[:k] for _ in range(T)]).to(torch.int32)
+    w = torch.rand(T, k, generator=g, device=DEV)
+    want = moe.FP8Experts(w1, w2, k)(x, idx, w)
+    layer = moe.FP8Experts(w1, w2, k)
+    outs, graphs, status = [torch.zeros_like(want) for _ in range(2)], [], []
+    torch.cuda.synchronize()
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer(x, idx, w, out=o)
+        graphs.append(graph)
+        status.append((layer.ws, layer.ws_matmul))
+    assert torch.equal(layer(x, idx, w), want)
+    status.append((layer.ws, layer.ws_matmul))
+    for graph in reversed(graphs):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    for a, b in status:
+        assert moe.get_device_status(a) == moe.get_device_status(b) == moe.MOE_OK
